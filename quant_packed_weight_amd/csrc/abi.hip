@@ -6,9 +6,7 @@
 // "Roadmap" and "Try it").  The library owns no memory and keeps no per-call
 // state; the only process-wide state is per device: the architecture check
 // and whether the GEMM kernels' LDS limit has been raised.
-#include <atomic>
-#include <cstring>
-
+#include "abi_util.h"
 #include "gemmq.h"
 #include "launch.h"
 
@@ -30,7 +28,11 @@ int launch_skinny_silu(int fmt, const Group& g, const uint8_t* Xq, int M, int64_
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using gemmq::aligned;
+using gemmq::check_device;
+using gemmq::clear_pending;
+using gemmq::launched;
+
 // activation rows the small-M MFMA kernels take: q4_K up to 64, q6_K up to 16
 // (automatic choice: from 3)
 constexpr int64_t kSkinnyMinM = 3, kSkinnyMaxM = 64, kSkinnyQ6MaxM = 16;
@@ -55,7 +57,6 @@ constexpr int64_t kSkinnyColTiles = 20480;
 constexpr int64_t kSkinnyQ6Cols = 16384;
 constexpr int64_t kSkinnyQ6Work = int64_t(1) << 16;
 constexpr int64_t kSkinnyQ6LongWork = int64_t(1) << 18;
-std::atomic<int> g_arch_ok[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
 
 // the largest M the small-M kernel takes in this format (0: not available)
 int64_t skinny_max_m(int fmt) {
@@ -63,22 +64,6 @@ int64_t skinny_max_m(int fmt) {
   if (fmt == GEMMQ_Q6_K || fmt == GEMMQ_Q6_K_R) return kSkinnyQ6MaxM;
   return 0;
 }
-
-int check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GEMMQ_E_DEVICE;
-  if (dev >= kMaxDevices) return GEMMQ_E_DEVICE;
-  int state = g_arch_ok[dev].load(std::memory_order_acquire);
-  if (state == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMMQ_E_DEVICE;
-    state = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-    g_arch_ok[dev].store(state, std::memory_order_release);
-  }
-  return state == 1 ? GEMMQ_OK : GEMMQ_E_DEVICE;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int fmt_bytes(int fmt) {
   switch (fmt) {
@@ -100,20 +85,6 @@ uintptr_t fmt_align(int fmt) {
   return fmt == GEMMQ_Q4_K || fmt == GEMMQ_Q5_K || fmt == GEMMQ_Q3_K_R || fmt == GEMMQ_Q6_K_R ? 16
                                                                                                  : 4;
 }
-
-// Launcher outcome: -1 means the shape does not fit the kernel's launch
-// geometry, -2 that the runtime refused a per-device kernel attribute; the
-// callers check both before enqueuing anything (shape_matmul, prepare_matmul),
-// so here they only guard the launchers' own checks.  The thread's pending HIP error is
-// cleared just before each launch (see clear_pending), so an error read here
-// belongs to our launch.
-int launched(int rc) {
-  if (rc == -1) return GEMMQ_E_SHAPE;
-  if (rc != 0) return GEMMQ_E_LAUNCH;
-  return hipGetLastError() == hipSuccess ? GEMMQ_OK : GEMMQ_E_LAUNCH;
-}
-
-void clear_pending() { (void)hipGetLastError(); }
 
 // Bounds that keep every byte offset below 2^62 and every grid dimension legal.
 constexpr int64_t kMaxK = (int64_t)1 << 24;
@@ -145,7 +116,8 @@ const char* gemmq_status_str(int status) {
     case GEMMQ_E_SHAPE:
       return "GEMMQ_E_SHAPE: K must be a positive multiple of 256 up to 2^24, rows up to 2^31; "
              "the GEMV path takes M <= 8, the small-M path M <= 64 (q6_K: 16), the GEMM path M <= "
-             "4194240";
+             "4194240; the int8 calls take K <= 131071, rows up to 2^24, pitches of int8 matrices "
+             "from K to 2^20 in multiples of 16, and at least one vocabulary row";
     case GEMMQ_E_ALIGNMENT: return "GEMMQ_E_ALIGNMENT: a pointer breaks the documented alignment";
     case GEMMQ_E_DEVICE: return "GEMMQ_E_DEVICE: the current HIP device is not a gfx950";
     case GEMMQ_E_LAUNCH: return "GEMMQ_E_LAUNCH: the HIP runtime rejected a kernel launch";

@@ -1,0 +1,100 @@
+// i8.h -- internal interface of the int8 half (gemmq_i8.h): the argument blocks
+// and launchers behind i8_abi.hip.  Every launcher assumes validated arguments
+// and returns 0, or -1 when the problem does not fit a grid.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemmq_i8.h"
+
+namespace gemmq {
+namespace i8 {
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t type_bytes(int type) { return type == GEMMQ_F32 ? 4 : 2; }
+
+// bf16 numbers that carry one value of `type` in the gradient's products
+// (8 significant bits each): all of a bf16, f16's 11 bits, all of an f32.
+inline int planes_of(int type) { return type == GEMMQ_BF16 ? 1 : type == GEMMQ_F16 ? 2 : 3; }
+
+// The int8 operands: sum over k of X[m, k] * W[n, k] for m < M, n < N, and
+// their scales.
+struct Operands {
+  const int8_t* W;
+  const float* sw;
+  const int8_t* X;
+  const float* sx;
+  int64_t ldw, ldx;
+  int M, N, K;
+};
+
+// y = sx sw I (+ bias)
+struct LinearOut {
+  const float* bias;
+  void* Y;
+  int64_t ldy;
+  int type;
+  bool wide;  // four consecutive values of a row may be stored at once
+};
+
+// Softmax statistics per column tile: (max, sum of exp2(z - max)) of the base-2
+// logits of row m in tile t at part[m * ntiles + t]; zt[m] the target's logit.
+struct LossOut {
+  const int64_t* target;
+  float2* part;
+  float* zt;
+  int ntiles;
+};
+
+// The softmax factor (exp(z - lse) - [n == target]) * sw of one piece of the
+// vocabulary (operands' row 0 is vocabulary row n0) as `planes` bf16 matrices of
+// [M, pitch], plane p at P + p * M * pitch; columns from N to the pitch are zero.
+struct FactorOut {
+  const int64_t* target;
+  const float* lse;
+  uint16_t* P;
+  int64_t pitch, n0;
+  int planes;
+};
+
+int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
+                    int K, hipStream_t st);
+
+// i8_gemm.hip: each with its own check of the grid
+bool linear_fits(int M, int N);
+int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st);
+int loss_tiles(int M, int N, int K);  // column tiles of the loss launch (LossOut::ntiles)
+bool loss_fits(int M, int N, int K);
+int launch_loss(const Operands& op, const LossOut& out, hipStream_t st);
+int launch_loss_join(const LossOut& o, float* loss, float* lse, int M, int N, hipStream_t st);
+bool factor_fits(int M, int N);
+int launch_factor(const Operands& op, const FactorOut& out, hipStream_t st);
+
+// i8_grad.hip: acc[s][m][k] (+)= sum over the s-th range of n of
+// (sum of planes)[m, n] * W[n, k], the ranges covering the piece's columns.
+struct GradArgs {
+  const int8_t* W;     // the piece's first row
+  int64_t ldw;
+  const uint16_t* P;   // planes of [M, pitch]
+  int64_t pitch;       // a multiple of 64
+  float* acc;          // [splits][M][kp]
+  int64_t kp;          // pitch of a row of acc, a multiple of 4, >= K
+  int M, N, K, planes, splits;
+  bool add;            // add to what acc holds (a later piece)
+};
+int grad_splits(int M, int N, int K, int planes);
+bool grad_fits(int M, int K, int splits);
+int launch_grad(const GradArgs& a, hipStream_t st);
+
+// planes of dY * sw for columns [n0, n0 + N) of dY; columns up to the pitch zero
+int launch_planes(int type, const void* dY, int64_t lddy, const float* sw, uint16_t* P,
+                  int64_t pitch, int planes, int M, int N, hipStream_t st);
+
+// dX = g[m] * sum over splits of acc (g null: 1); rows with target[m] < 0 zero,
+// with target[m] >= nvocab NaN
+int launch_finish(const float* acc, int64_t kp, int splits, const float* g, const int64_t* target,
+                  int64_t nvocab, int type, void* dX, int64_t lddx, int M, int K, hipStream_t st);
+
+}  // namespace i8
+}  // namespace gemmq

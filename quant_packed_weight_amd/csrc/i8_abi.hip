@@ -1,0 +1,287 @@
+// i8_abi.hip -- the int8 half of the C ABI (gemmq_i8.h): validation, workspace
+// layout and the order of launches.  As in abi.hip, a bad call returns a named
+// status and launches nothing, and the library owns no memory.
+#include "abi_util.h"
+#include "gemmq_i8.h"
+#include "i8.h"
+
+using gemmq::aligned;
+using gemmq::check_device;
+using gemmq::clear_pending;
+using gemmq::launched;
+using namespace gemmq::i8;
+
+namespace {
+
+constexpr int64_t kMaxPitchElems = (int64_t)1 << 40;  // keeps element offsets below 2^63
+
+bool known(int type) { return type == GEMMQ_F32 || type == GEMMQ_BF16 || type == GEMMQ_F16; }
+
+int check_shape(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0) return GEMMQ_E_INVALID_ARG;
+  if (K < 1 || K > GEMMQ_I8_MAX_K || M > GEMMQ_I8_MAX_ROWS || N > GEMMQ_I8_MAX_ROWS)
+    return GEMMQ_E_SHAPE;
+  return GEMMQ_OK;
+}
+
+// an int8 matrix with its scales
+int check_i8(const void* p, int64_t ld, const void* s, int64_t K) {
+  if (!p || !s) return GEMMQ_E_INVALID_ARG;
+  if (ld < K || ld > GEMMQ_I8_MAX_PITCH) return GEMMQ_E_SHAPE;
+  if (ld % 16 != 0 || !aligned(p, 16) || !aligned(s, 4)) return GEMMQ_E_ALIGNMENT;
+  return GEMMQ_OK;
+}
+
+// a matrix of element type `type`
+int check_rows(int type, const void* p, int64_t ld, int64_t width) {
+  if (!known(type) || !p) return GEMMQ_E_INVALID_ARG;
+  if (ld < width || ld > kMaxPitchElems) return GEMMQ_E_SHAPE;
+  if (!aligned(p, (uintptr_t)type_bytes(type))) return GEMMQ_E_ALIGNMENT;
+  return GEMMQ_OK;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return GEMMQ_E_INVALID_ARG;
+  return aligned(ws, 16) ? GEMMQ_OK : GEMMQ_E_ALIGNMENT;
+}
+
+size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
+
+// The gradients walk N in pieces whose bf16 factor stays within this many bytes
+// (it then stays in the 256 MB last-level cache between the launch that writes
+// it and the one that reads it, and bounds the workspace), or of kMinPiece
+// columns where the rows alone are more.
+constexpr int64_t kFactorBytes = (int64_t)128 << 20;
+constexpr int64_t kMinPiece = 1024;
+
+struct GradPlan {
+  int planes, splits;
+  int64_t piece, kp;
+  size_t factor_bytes, acc_bytes;
+  size_t bytes() const { return factor_bytes + acc_bytes; }
+};
+
+GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K) {
+  GradPlan p;
+  p.planes = planes_of(type);
+  int64_t most = kFactorBytes / (2 * p.planes * M) / 256 * 256;
+  if (most < kMinPiece) most = kMinPiece;
+  const int64_t n64 = (int64_t)align_up(N < 1 ? 1 : N, 64);
+  // equal pieces, in multiples of 256 columns
+  const int64_t pieces = ceil_div(n64, most);
+  p.piece = pieces == 1 ? n64 : (int64_t)align_up(ceil_div(n64, pieces), 256);
+  p.kp = (int64_t)align_up(K, 4);
+  p.splits = grad_splits((int)M, (int)p.piece, (int)K, p.planes);
+  p.factor_bytes = align_up(2 * p.planes * M * p.piece, 256);
+  p.acc_bytes = align_up(4 * p.splits * M * p.kp, 256);
+  return p;
+}
+
+bool grad_shape_ok(int64_t M, int64_t N, int64_t K, const GradPlan& p) {
+  return grad_fits((int)M, (int)K, p.splits) && factor_fits((int)M, (int)p.piece) &&
+         ceil_div(M * (p.piece / 4), 256) <= 0x7fffffff && N >= 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemmq_i8_abi_version(void) { return GEMMQ_I8_ABI_VERSION; }
+
+int gemmq_quantize_i8(int xtype, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s,
+                      int64_t M, int64_t K, void* stream) {
+  int rc = check_shape(M, 0, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(xtype)) return GEMMQ_E_INVALID_ARG;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_rows(xtype, X, ldx, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Q, ldq, s, K);
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  clear_pending();
+  return launched(launch_quantize(xtype, X, ldx, Q, ldq, s, (int)M, (int)K,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// the product's own checks and its argument blocks
+int check_product(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
+                  const float* sx, const float* bias, int ytype, void* Y, int64_t ldy, int64_t M,
+                  int64_t N, int64_t K, Operands& op, LinearOut& out) {
+  int rc = check_i8(W, ldw, sw, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc == GEMMQ_OK) rc = check_rows(ytype, Y, ldy, N);
+  if (rc != GEMMQ_OK) return rc;
+  if (bias && !aligned(bias, 4)) return GEMMQ_E_ALIGNMENT;
+  if (!linear_fits((int)M, (int)N)) return GEMMQ_E_SHAPE;
+  op = Operands{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
+  out = LinearOut{bias, Y, ldy, ytype,
+                  ldy % 4 == 0 && aligned(Y, (uintptr_t)(4 * type_bytes(ytype)))};
+  return GEMMQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemmq_gemm_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
+                  const float* sx, const float* bias, int ytype, void* Y, int64_t ldy, int64_t M,
+                  int64_t N, int64_t K, void* stream) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(ytype)) return GEMMQ_E_INVALID_ARG;
+  if (M == 0 || N == 0) return GEMMQ_OK;
+  Operands op;
+  LinearOut out;
+  rc = check_product(W, ldw, sw, Xq, ldq, sx, bias, ytype, Y, ldy, M, N, K, op, out);
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  clear_pending();
+  return launched(launch_linear(op, out, static_cast<hipStream_t>(stream)));
+}
+
+int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, const void* X,
+                    int64_t ldx, int8_t* Xq, int64_t ldq, float* sx, const float* bias, int ytype,
+                    void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* stream) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(xtype) || !known(ytype)) return GEMMQ_E_INVALID_ARG;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_rows(xtype, X, ldx, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc != GEMMQ_OK) return rc;
+  Operands op;
+  LinearOut out;
+  if (N > 0) rc = check_product(W, ldw, sw, Xq, ldq, sx, bias, ytype, Y, ldy, M, N, K, op, out);
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  clear_pending();
+  rc = launched(launch_quantize(xtype, X, ldx, Xq, ldq, sx, (int)M, (int)K, st));
+  if (rc != GEMMQ_OK || N == 0) return rc;
+  return launched(launch_linear(op, out, st));
+}
+
+size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
+  if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0) return 0;
+  const GradPlan p = grad_plan(type, M, N, K);
+  return grad_shape_ok(M, N, K, p) ? p.bytes() : 0;
+}
+
+int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type, const void* dY,
+                         int64_t lddy, void* dX, int64_t lddx, int64_t M, int64_t N, int64_t K,
+                         void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(type)) return GEMMQ_E_INVALID_ARG;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_rows(type, dX, lddx, K);
+  if (rc == GEMMQ_OK && N > 0) rc = check_i8(W, ldw, sw, K);
+  if (rc == GEMMQ_OK && N > 0) rc = check_rows(type, dY, lddy, N);
+  if (rc != GEMMQ_OK) return rc;
+  const GradPlan p = grad_plan(type, M, N, K);
+  if (!grad_shape_ok(M, N, K, p)) return GEMMQ_E_SHAPE;
+  rc = check_ws(ws, ws_bytes, p.bytes());
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint16_t* P = static_cast<uint16_t*>(ws);
+  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.factor_bytes);
+  clear_pending();
+  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
+    const int64_t n = N - n0 < p.piece ? N - n0 : p.piece;
+    const int64_t pitch = (int64_t)align_up(n, 64);
+    const uint8_t* dy = static_cast<const uint8_t*>(dY) + n0 * type_bytes(type);
+    rc = launched(launch_planes(type, dy, lddy, sw + n0, P, pitch, p.planes, (int)M, (int)n, st));
+    if (rc != GEMMQ_OK) return rc;
+    const GradArgs g{W + n0 * ldw, ldw, P, pitch, acc, p.kp, (int)M, (int)n, (int)K, p.planes,
+                     p.splits, n0 > 0};
+    rc = launched(launch_grad(g, st));
+    if (rc != GEMMQ_OK) return rc;
+  }
+  return launched(launch_finish(acc, p.kp, N > 0 ? p.splits : 0, nullptr, nullptr, 0, type, dX,
+                                lddx, (int)M, (int)K, st));
+}
+
+size_t gemmq_loss_i8_workspace(int64_t M, int64_t N, int64_t K) {
+  if (check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0 || !loss_fits((int)M, (int)N, (int)K))
+    return 0;
+  return align_up(8 * M * loss_tiles((int)M, (int)N, (int)K), 256) + align_up(4 * M, 256);
+}
+
+int gemmq_loss_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
+                  const float* sx, const int64_t* target, float* loss, float* lse, int64_t M,
+                  int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (N == 0) return GEMMQ_E_SHAPE;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_i8(W, ldw, sw, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!target || !loss || !lse) return GEMMQ_E_INVALID_ARG;
+  if (!aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4)) return GEMMQ_E_ALIGNMENT;
+  const size_t need = gemmq_loss_i8_workspace(M, N, K);
+  if (need == 0) return GEMMQ_E_SHAPE;
+  rc = check_ws(ws, ws_bytes, need);
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  const Operands op{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
+  const int nt = loss_tiles((int)M, (int)N, (int)K);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  const LossOut o{target, reinterpret_cast<float2*>(b),
+                  reinterpret_cast<float*>(b + align_up(8 * M * nt, 256)), nt};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  clear_pending();
+  rc = launched(launch_loss(op, o, st));
+  if (rc != GEMMQ_OK) return rc;
+  return launched(launch_loss_join(o, loss, lse, (int)M, (int)N, st));
+}
+
+size_t gemmq_loss_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
+  return N < 1 ? 0 : gemmq_linear_i8_grad_workspace(type, M, N, K);
+}
+
+int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq,
+                       int64_t ldq, const float* sx, const int64_t* target, const float* lse,
+                       const float* dloss, int type, void* dX, int64_t lddx, int64_t M, int64_t N,
+                       int64_t K, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(type)) return GEMMQ_E_INVALID_ARG;
+  if (N == 0) return GEMMQ_E_SHAPE;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_i8(W, ldw, sw, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc == GEMMQ_OK) rc = check_rows(type, dX, lddx, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!target || !lse || !dloss) return GEMMQ_E_INVALID_ARG;
+  if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return GEMMQ_E_ALIGNMENT;
+  const GradPlan p = grad_plan(type, M, N, K);
+  if (!grad_shape_ok(M, N, K, p)) return GEMMQ_E_SHAPE;
+  rc = check_ws(ws, ws_bytes, p.bytes());
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint16_t* P = static_cast<uint16_t*>(ws);
+  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.factor_bytes);
+  clear_pending();
+  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
+    const int64_t n = N - n0 < p.piece ? N - n0 : p.piece;
+    const int64_t pitch = (int64_t)align_up(n, 64);
+    const Operands op{W + n0 * ldw, sw + n0, Xq, sx, ldw, ldq, (int)M, (int)n, (int)K};
+    rc = launched(launch_factor(op, FactorOut{target, lse, P, pitch, n0, p.planes}, st));
+    if (rc != GEMMQ_OK) return rc;
+    const GradArgs g{W + n0 * ldw, ldw, P, pitch, acc, p.kp, (int)M, (int)n, (int)K, p.planes,
+                     p.splits, n0 > 0};
+    rc = launched(launch_grad(g, st));
+    if (rc != GEMMQ_OK) return rc;
+  }
+  return launched(launch_finish(acc, p.kp, p.splits, dloss, target, N, type, dX, lddx, (int)M,
+                                (int)K, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,86 @@
+// i8_common.h -- device pieces the int8 kernels share.
+#pragma once
+
+#include "gemm_common.h"
+#include "i8.h"
+
+namespace gemmq {
+namespace i8 {
+
+using gk::rsrc_t;
+using gk::v16f;
+using gk::v16i;
+using gk::v4i;
+
+typedef __bf16 bf16_t;
+
+// f32 -> the type's 16 bits, round to nearest even
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, (bf16_t)v);
+}
+__device__ __forceinline__ uint32_t f16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int type) {
+  if (type == GEMMQ_F32) return static_cast<const float*>(p)[i];
+  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+  if (type == GEMMQ_BF16) return __builtin_bit_cast(float, (uint32_t)b << 16);
+  return (float)__builtin_bit_cast(_Float16, b);
+}
+
+__device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) {
+  if (type == GEMMQ_F32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<uint16_t*>(p)[i] = (uint16_t)(type == GEMMQ_BF16 ? bf16_bits(v) : f16_bits(v));
+}
+
+// four consecutive values of a row from element i: at once where `wide` says that
+// the address allows it and all four are inside, else those of the first `count`
+__device__ __forceinline__ void store4_as(void* p, int64_t i, int type, bool wide, int count,
+                                          float v0, float v1, float v2, float v3) {
+  if (wide && count >= 4) {
+    if (type == GEMMQ_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v0, v1, v2, v3);
+    } else {
+      uint2 b;
+      if (type == GEMMQ_BF16)
+        b = make_uint2(bf16_bits(v0) | bf16_bits(v1) << 16, bf16_bits(v2) | bf16_bits(v3) << 16);
+      else
+        b = make_uint2(f16_bits(v0) | f16_bits(v1) << 16, f16_bits(v2) | f16_bits(v3) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = b;
+    }
+    return;
+  }
+  if (count > 0) store_as(p, i, type, v0);
+  if (count > 1) store_as(p, i + 1, type, v1);
+  if (count > 2) store_as(p, i + 2, type, v2);
+  if (count > 3) store_as(p, i + 3, type, v3);
+}
+
+// The next bf16 of v's expansion, its top 16 bits, and what is left of v: both
+// exact, so three of them hold all 24 bits of an f32 (the last one is rounded,
+// which matters for two).  An infinity or a NaN is its own only part, with the
+// quiet bit set so that a NaN whose set bits are all in the low half stays one.
+__device__ __forceinline__ uint32_t bf16_part(float& v, bool last) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  if ((b & 0x7f800000u) == 0x7f800000u) {
+    v = 0.0f;
+    return (b >> 16) | ((b & 0x7fffffu) ? 0x40u : 0u);
+  }
+  if (last) return bf16_bits(v);
+  v -= __builtin_bit_cast(float, b & 0xffff0000u);
+  return b >> 16;
+}
+
+// Workgroup index -> position in the work list such that each of the eight XCDs
+// (consecutive workgroups go to consecutive XCDs) takes one contiguous stretch
+// of it, and neighbours in the list share an L2.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t total) {
+  const uint32_t xcd = id & 7, at = id >> 3, per = total >> 3, more = total & 7;
+  return xcd * per + (xcd < more ? xcd : more) + at;
+}
+
+}  // namespace i8
+}  // namespace gemmq
