@@ -39,11 +39,10 @@ struct LinearOut {
 };
 
 // Softmax statistics per column tile: (max, sum of exp2(z - max)) of the base-2
-// logits of row m in tile t at part[m * ntiles + t]; zt[m] the target's logit.
+// logits of row m in tile t at part[m * ntiles + t].
 struct LossOut {
   const int64_t* target;
   float2* part;
-  float* zt;
   int ntiles;
 };
 
@@ -67,7 +66,8 @@ int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st);
 int loss_tiles(int M, int N, int K);  // column tiles of the loss launch (LossOut::ntiles)
 bool loss_fits(int M, int N, int K);
 int launch_loss(const Operands& op, const LossOut& out, hipStream_t st);
-int launch_loss_join(const LossOut& o, float* loss, float* lse, int M, int N, hipStream_t st);
+int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* lse,
+                     hipStream_t st);
 bool factor_fits(int M, int N);
 int launch_factor(const Operands& op, const FactorOut& out, hipStream_t st);
 

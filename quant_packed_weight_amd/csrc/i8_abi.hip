@@ -209,7 +209,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
 size_t gemmq_loss_i8_workspace(int64_t M, int64_t N, int64_t K) {
   if (check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0 || !loss_fits((int)M, (int)N, (int)K))
     return 0;
-  return align_up(8 * M * loss_tiles((int)M, (int)N, (int)K), 256) + align_up(4 * M, 256);
+  return align_up(8 * M * loss_tiles((int)M, (int)N, (int)K), 256);
 }
 
 int gemmq_loss_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
@@ -231,14 +231,12 @@ int gemmq_loss_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* X
   if (rc != GEMMQ_OK) return rc;
   const Operands op{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
   const int nt = loss_tiles((int)M, (int)N, (int)K);
-  uint8_t* b = static_cast<uint8_t*>(ws);
-  const LossOut o{target, reinterpret_cast<float2*>(b),
-                  reinterpret_cast<float*>(b + align_up(8 * M * nt, 256)), nt};
+  const LossOut o{target, static_cast<float2*>(ws), nt};
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_pending();
   rc = launched(launch_loss(op, o, st));
   if (rc != GEMMQ_OK) return rc;
-  return launched(launch_loss_join(o, loss, lse, (int)M, (int)N, st));
+  return launched(launch_loss_join(op, o, loss, lse, st));
 }
 
 size_t gemmq_loss_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {

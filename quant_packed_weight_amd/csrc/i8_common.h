@@ -74,6 +74,23 @@ __device__ __forceinline__ uint32_t bf16_part(float& v, bool last) {
   return b >> 16;
 }
 
+// vmcnt(N) where the wave-uniform `most` holds, else vmcnt(0); without a branch
+// that the compiler sees
+template <int N>
+__device__ __forceinline__ void wait_vm_if(bool most) {
+  static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit field");
+  if constexpr (N == 0) {
+    gk::wait_vm<0>();
+  } else {
+    const uint32_t t = __builtin_amdgcn_readfirstlane((uint32_t)most);
+    asm volatile(
+        "s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%1)\n\ts_branch 2f\n"
+        "1:\ts_waitcnt vmcnt(0)\n2:" ::"s"(t),
+        "i"(N)
+        : "memory", "scc");
+  }
+}
+
 // Workgroup index -> position in the work list such that each of the eight XCDs
 // (consecutive workgroups go to consecutive XCDs) takes one contiguous stretch
 // of it, and neighbours in the list share an L2.

@@ -4,10 +4,10 @@
 // of its gradient.
 //
 // One workgroup computes a tile of BN channels by BM tokens, K in steps of 128
-// bytes, both operands staged in LDS by direct buffer->LDS loads, two steps
-// deep.  W is the MFMA's row operand, so a lane ends with one token and four
-// consecutive channels per register quad: rows of Y are stored four values at a
-// time, and the softmax sums of a token are in-lane sums.
+// bytes, both operands staged in LDS by direct buffer->LDS loads.  W is the
+// MFMA's row operand, so a lane ends with one token and four consecutive channels
+// per register quad: rows of Y are stored four values at a time, and the softmax
+// sums of a token are in-lane sums.
 #include "i8_common.h"
 
 namespace gemmq {
@@ -17,9 +17,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // LDS image of a step: rows of 128 bytes, eight 16-byte chunks each, chunk c of
-// row r in slot c ^ (r & 7).  The eight rows that eight consecutive lanes read
-// the same chunk of then lie in eight different slots, i.e. in different banks.
+// row r in slot c ^ ((r >> 1) & 7).  Sixteen rows whose numbers differ in their
+// low four bits then have the same chunk in sixteen different 16-byte columns of
+// the 256 bytes that the 64 banks span: no conflict among sixteen lanes of a
+// fragment's read (with c ^ (r & 7), eight columns, the reads took twice as long).
 constexpr int kStep = 128;
+
+__device__ __forceinline__ int slot(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
 enum Epilogue { kLinear, kLoss, kFactor };
 
@@ -28,8 +32,19 @@ struct TileArgs {
   LinearOut lin;
   LossOut loss;
   FactorOut fac;
-  uint32_t mtiles;
+  uint32_t mtiles, ntiles, group;
 };
+
+// Work list order: `group` tiles along the tokens by all tiles along the channels,
+// then the next group.  The tiles that one XCD works on at a time are then about
+// as many tokens as channels, and its L2 loads the fewest rows for them.
+__device__ __forceinline__ void tile_of(const TileArgs& a, uint32_t id, uint32_t& tm,
+                                        uint32_t& tn) {
+  const uint32_t full = a.group * a.ntiles, g = id / full, r = id % full;
+  const uint32_t width = min(a.group, a.mtiles - g * a.group);
+  tm = g * a.group + r % width;
+  tn = r / width;
+}
 
 template <int BN, int BM>
 struct Stage {
@@ -43,7 +58,7 @@ struct Stage {
 template <int ROWS, int NW>
 struct RowLoader {
   static constexpr int kIssues = ROWS / 8 / NW;
-  static_assert(ROWS % (8 * NW) == 0, "every wave issues the same number of loads");
+  static_assert(ROWS % (8 * NW) == 0 && NW % 2 == 0, "each wave issues the same loads");
   rsrc_t rs;
   uint32_t voff[kIssues];
   int last;  // offset of the 16-byte chunk that holds column K - 1
@@ -53,7 +68,9 @@ struct RowLoader {
                                        int K, int wave, int lane) {
     const int valid = (int)min((int64_t)ROWS, rows - row0);
     rs = gk::make_rsrc(base + row0 * ld, (uint32_t)(valid * ld));
-    chunk = 16 * ((lane & 7) ^ (lane >> 3));
+    // the eight rows of an instruction start at a multiple of eight, of sixteen
+    // for even waves (NW is even): the slot of a lane's chunk is the same in all
+    chunk = 16 * slot(8 * (wave & 1) + (lane >> 3), lane & 7);
     last = (K - 1) / 16 * 16;
 #pragma unroll
     for (int j = 0; j < kIssues; ++j) {
@@ -61,16 +78,20 @@ struct RowLoader {
       voff[j] = (uint32_t)(min(r, valid - 1) * ld) + chunk;
     }
   }
-  __device__ __forceinline__ void issue(int k0, uint32_t lds, int wave) const {
-    const int over = min(0, last - (k0 + chunk));  // <= 0, and chunk + over >= 0
-#pragma unroll
-    for (int j = 0; j < kIssues; ++j)
-      gk::dma16(rs, voff[j] + (uint32_t)over, (uint32_t)k0, lds + 1024 * (wave + NW * j));
+  // how far the chunk of the step at column k0 moves back to lie before column K
+  // (<= 0, and chunk + over >= 0)
+  __device__ __forceinline__ uint32_t over(int k0) const {
+    return (uint32_t)min(0, last - (k0 + chunk));
+  }
+  // load j, where the wave-uniform `take` is not zero
+  __device__ __forceinline__ void issue(int j, uint32_t take, int k0, uint32_t back, uint32_t lds,
+                                        int wave) const {
+    gk::dma16_if(take, rs, voff[j] + back, (uint32_t)k0, lds + 1024 * (wave + NW * j));
   }
 };
 
 __device__ __forceinline__ v4i frag(const uint8_t* tile, int row, int chunk) {
-  return *reinterpret_cast<const v4i*>(tile + row * kStep + 16 * (chunk ^ (row & 7)));
+  return *reinterpret_cast<const v4i*>(tile + row * kStep + 16 * slot(row, chunk));
 }
 
 // The activations' bytes from column K on, zeroed in LDS for the step at k0:
@@ -80,7 +101,7 @@ __device__ __forceinline__ void clear_tail(uint8_t* x, int k0, int K, int t) {
   for (int i = t; i < BM * 8; i += THREADS) {
     const int row = i >> 3, c = i & 7, keep = K - (k0 + 16 * c);
     if (keep >= 16) continue;
-    uint32_t* p = reinterpret_cast<uint32_t*>(x + row * kStep + 16 * (c ^ (row & 7)));
+    uint32_t* p = reinterpret_cast<uint32_t*>(x + row * kStep + 16 * slot(row, c));
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int b = keep - 4 * w;
@@ -89,20 +110,29 @@ __device__ __forceinline__ void clear_tail(uint8_t* x, int k0, int K, int t) {
   }
 }
 
-template <int BN, int BM, int WN, int WM, int EPI>
-__global__ __launch_bounds__(64 * WN * WM) void tile_kernel(TileArgs a) {
+// (max, sum) of one part of a row, the sum taken relative to the row's maximum
+__device__ __forceinline__ float join_term(float2 p, float top) {
+  // a part without columns is (-inf, 0)
+  return p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - top);
+}
+
+template <int BN, int BM, int WN, int WM, int DEPTH, int EPI>
+__global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   constexpr int NW = WN * WM, T = 64 * NW;
   constexpr int TN = BN / WN / 32, TM = BM / WM / 32;
   using S = Stage<BN, BM>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S::kBytes];
-  __shared__ float swl[BN];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
+  __shared__ __attribute__((aligned(16))) float swl[BN];
+  __shared__ __attribute__((aligned(16))) float bias[EPI == kLinear ? BN : 4];
   __shared__ float2 red[EPI == kLoss ? WN * BM : 1];
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wn = wave % WN, wm = wave / WN;
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
-  const int64_t m0 = (int64_t)(id % a.mtiles) * BM, n0 = (int64_t)(id / a.mtiles) * BN;
+  uint32_t tm, tn;
+  tile_of(a, id, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const Operands& op = a.op;
 
   RowLoader<BN, NW> lw;
@@ -111,7 +141,11 @@ __global__ __launch_bounds__(64 * WN * WM) void tile_kernel(TileArgs a) {
   lx.init(op.X, op.ldx, m0, op.M, op.K, wave, lane);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
-  for (int i = t; i < BN; i += T) swl[i] = n0 + i < op.N ? op.sw[n0 + i] : 0.0f;
+  for (int i = t; i < BN; i += T) {
+    const bool in = n0 + i < op.N;
+    swl[i] = in ? op.sw[n0 + i] : 0.0f;
+    if constexpr (EPI == kLinear) bias[i] = in && a.lin.bias ? a.lin.bias[n0 + i] : 0.0f;
+  }
 
   v16i acc[TN][TM];
 #pragma unroll
@@ -122,39 +156,95 @@ __global__ __launch_bounds__(64 * WN * WM) void tile_kernel(TileArgs a) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
   const int steps = (op.K + kStep - 1) / kStep;
-  lw.issue(0, lds0 + S::kW, wave);
-  lx.issue(0, lds0 + S::kX, wave);
+  constexpr int kLw = RowLoader<BN, NW>::kIssues, kLoads = kLw + RowLoader<BM, NW>::kIssues;
+  // load j of this wave's kLoads for a step
+  auto load = [&](int j, uint32_t take, int k0, uint32_t back, uint32_t to) {
+    if (j < kLw)
+      lw.issue(j, take, k0, back, to + S::kW, wave);
+    else
+      lx.issue(j - kLw, take, k0, back, to + S::kX, wave);
+  };
+
+  // Fragments of a quarter step (32 bytes of K): two sets, one read while the
+  // matrix cores work on the other.
+  v4i wf[2][TN], xf[2][TM];
+  constexpr int kReads = TN + TM, kProducts = TN * TM;
+  auto read = [&](const uint8_t* stage, int q, int r) {
+    if (r < TN)
+      wf[q & 1][r] = frag(stage + S::kW, (wn * TN + r) * 32 + (lane & 31), 2 * q + (lane >> 5));
+    else
+      xf[q & 1][r - TN] =
+          frag(stage + S::kX, (wm * TM + r - TN) * 32 + (lane & 31), 2 * q + (lane >> 5));
+  };
+  // The products of quarter q, with the reads of the next quarter over the first
+  // half of them and, in quarter 3, the loads of a later step over all: each is
+  // issued while an MFMA runs.  A burst of either would leave the matrix cores
+  // idle behind it.  Everything in one loop body, with the branches around the
+  // loads inside their asm: a second copy of the products makes the compiler move
+  // all accumulators between the two.
+  constexpr int kPerProduct = (2 * kReads + kProducts - 1) / kProducts;
+  auto quarter = [&](int q, const uint8_t* from, uint32_t take, int k0, uint32_t back,
+                     uint32_t to) {
+#pragma unroll
+    for (int p = 0; p < kProducts; ++p) {
+      acc[p / TM][p % TM] =
+          gk::mfma_i8(wf[q & 1][p / TM], xf[q & 1][p % TM], acc[p / TM][p % TM]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = p * kPerProduct; r < (p + 1) * kPerProduct && r < kReads; ++r)
+        read(from, (q + 1) & 3, r);
+      if (q == 3) {
+#pragma unroll
+        for (int j = p * kLoads / kProducts; j < (p + 1) * kLoads / kProducts; ++j)
+          load(j, take, k0, back, to);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s) {
+    const uint32_t back = lw.over(s * kStep);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      load(j, s < steps, s * kStep, back, lds0 + s * S::kBytes);
+  }
+  wait_vm_if<(DEPTH - 1) * kLoads>(steps >= DEPTH);
+  gk::lds_barrier();
+  if (steps == 1 && op.K % kStep) {
+    clear_tail<BM, T>(lds + S::kX, 0, op.K, t);
+    gk::lds_barrier();
+  }
+#pragma unroll
+  for (int r = 0; r < kReads; ++r) read(lds, 0, r);
+
+  // Past the barrier in step s the next step is in LDS (the loads of DEPTH - 2
+  // later ones may be under way) and every wave has read all of this one, so that
+  // its buffer takes the step DEPTH further on.  The last step reads a buffer that
+  // it does not use.
+  int buf = 0;
   for (int s = 0; s < steps; ++s) {
-    uint8_t* cur = lds + (s & 1) * S::kBytes;
-    gk::wait_vm<0>();
-    gk::lds_barrier();  // this step is in LDS, and the other buffer is read
-    if (s + 1 < steps) {
-      const uint32_t nxt = lds0 + ((s + 1) & 1) * S::kBytes;
-      lw.issue((s + 1) * kStep, nxt + S::kW, wave);
-      lx.issue((s + 1) * kStep, nxt + S::kX, wave);
-    } else if (op.K % kStep) {
-      clear_tail<BM, T>(cur + S::kX, s * kStep, op.K, t);
+    const int nbuf = buf == DEPTH - 1 ? 0 : buf + 1;
+    const uint8_t* cur = lds + buf * S::kBytes;
+    uint8_t* next = lds + nbuf * S::kBytes;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) quarter(q, cur, 0, 0, 0, 0);
+    wait_vm_if<(DEPTH - 2) * kLoads>(s + DEPTH - 1 < steps);
+    gk::lds_barrier();
+    if (s + 2 == steps && op.K % kStep) {
+      clear_tail<BM, T>(next + S::kX, (s + 1) * kStep, op.K, t);
       gk::lds_barrier();
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v4i wf[TN], xf[TM];
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-        wf[i] = frag(cur + S::kW, (wn * TN + i) * 32 + (lane & 31), 2 * q + (lane >> 5));
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        xf[j] = frag(cur + S::kX, (wm * TM + j) * 32 + (lane & 31), 2 * q + (lane >> 5));
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = gk::mfma_i8(wf[i], xf[j], acc[i][j]);
-    }
+    const int k0 = (s + DEPTH) * kStep;
+    quarter(3, next, s + DEPTH < steps, k0, lw.over(k0), lds0 + buf * S::kBytes);
+    buf = nbuf;
   }
+  gk::lds_barrier();  // no wave still reads what the epilogue may write
 
   // Lane l holds token 32 (wm TM + j) + (l & 31) and, in registers 4 g .. 4 g + 3
   // of tile i, channels 32 (wn TN + i) + 8 g + 4 (l >> 5) + 0..3.
-  const int h = lane >> 5;
+  const int h = lane >> 5, nw = wn * TN * 32 + 4 * h;
+  const bool edge = n0 + BN > op.N;  // some of the tile's channels do not exist
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int ml = (wm * TM + j) * 32 + (lane & 31);
@@ -163,80 +253,128 @@ __global__ __launch_bounds__(64 * WN * WM) void tile_kernel(TileArgs a) {
     const float sx = inside ? op.sx[m] : 0.0f;
     if constexpr (EPI == kLinear) {
       if (!inside) continue;
+      const bool wide = a.lin.wide && !edge;
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int nl = (wn * TN + i) * 32 + 8 * g + 4 * h;
+          const int nl = nw + 32 * i + 8 * g;
+          const float4 sw = *reinterpret_cast<const float4*>(swl + nl);
+          const float4 b = *reinterpret_cast<const float4*>(bias + nl);
+          const v16i& c = acc[i][j];
+          const float v0 = fmaf((float)c[4 * g] * sx, sw.x, b.x);
+          const float v1 = fmaf((float)c[4 * g + 1] * sx, sw.y, b.y);
+          const float v2 = fmaf((float)c[4 * g + 2] * sx, sw.z, b.z);
+          const float v3 = fmaf((float)c[4 * g + 3] * sx, sw.w, b.w);
           const int64_t n = n0 + nl;
-          const int count = (int)min((int64_t)4, op.N - n);
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = (float)acc[i][j][4 * g + e] * sx * swl[nl + e];
-            if (a.lin.bias && e < count) v[e] += a.lin.bias[n + e];
-          }
-          store4_as(a.lin.Y, m * a.lin.ldy + n, a.lin.type, a.lin.wide, count, v[0], v[1], v[2],
-                    v[3]);
+          store4_as(a.lin.Y, m * a.lin.ldy + n, a.lin.type, wide,
+                    edge ? (int)min((int64_t)4, op.N - n) : 4, v0, v1, v2, v3);
         }
-    } else if constexpr (EPI == kLoss) {
-      // base-2 logits: exp(z) = 2^(z log2 e), the factor folded into sx
-      const float s2 = sx * kLog2e;
-      const int64_t tg = inside ? a.loss.target[m] : -1;
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int nl = (wn * TN + i) * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
-          const float z = (float)acc[i][j][r] * s2 * swl[nl];
-          if (n0 + nl == tg) a.loss.zt[m] = z;
-          // a NaN (a row whose scale is NaN) has to survive: it is not dropped by >
-          if (n0 + nl < op.N) top = z > top || z != z ? z : top;
-        }
-      {
-        const float o = __shfl_xor(top, 32, 64);
-        top = o > top || o != o ? o : top;
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int nl = (wn * TN + i) * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
-          const float z = (float)acc[i][j][r] * s2 * swl[nl];
-          if (n0 + nl < op.N) sum += __builtin_amdgcn_exp2f(z - top);
-        }
-      sum += __shfl_xor(sum, 32, 64);
-      if (h == 0) red[wn * BM + ml] = make_float2(top, sum);
     } else {
-      const int64_t tg = inside ? a.fac.target[m] - a.fac.n0 : -1;
-      const float s2 = sx * kLog2e, l2 = inside ? a.fac.lse[m] * kLog2e : 0.0f;
-      if (!inside) continue;
+      // base-2 logits, exp(z) = 2^(z log2 e): v = sw I, z2 = s2 v with s2 = sx log2 e.
+      // A negative scale is moved to v, so that the largest v has the largest logit.
+      float s2 = sx * kLog2e;
+      const float sign = s2 < 0.0f ? -1.0f : 1.0f;
+      s2 *= sign;
+      float v[TN][16];
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int nl = (wn * TN + i) * 32 + 8 * g + 4 * h;
-          if (n0 + nl >= a.fac.pitch) continue;  // the pitch is a multiple of 4
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float z = (float)acc[i][j][4 * g + e] * s2 * swl[nl + e];
-            float p = __builtin_amdgcn_exp2f(z - l2);
-            if (n0 + nl + e == tg) p -= 1.0f;
-            v[e] = n0 + nl + e < op.N ? p * swl[nl + e] : 0.0f;
-          }
-          uint16_t* out = a.fac.P + m * a.fac.pitch + n0 + nl;
-          for (int p = 0; p < a.fac.planes; ++p) {
-            const bool last = p + 1 == a.fac.planes;
-            uint32_t b[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b[e] = bf16_part(v[e], last);
-            *reinterpret_cast<uint2*>(out + p * op.M * a.fac.pitch) =
-                make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-          }
+          const float4 sw = *reinterpret_cast<const float4*>(swl + nw + 32 * i + 8 * g);
+          v[i][4 * g] = (float)acc[i][j][4 * g] * sw.x;
+          v[i][4 * g + 1] = (float)acc[i][j][4 * g + 1] * sw.y;
+          v[i][4 * g + 2] = (float)acc[i][j][4 * g + 2] * sw.z;
+          v[i][4 * g + 3] = (float)acc[i][j][4 * g + 3] * sw.w;
         }
+      if (__any(sign < 0.0f)) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[i][r] *= sign;
+      }
+      if constexpr (EPI == kLoss) {
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (n0 + nw + 32 * i + 8 * (r >> 2) + (r & 3) >= op.N) v[i][r] = -__builtin_inff();
+        }
+        // A NaN is dropped by the maximum and kept by the sum.  A wave whose
+        // columns all lie past N takes 0 as its maximum, and has the sum 0.
+        float top = v[0][0];
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, v[i][r]);
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float z = top == -__builtin_inff() ? 0.0f : top * s2;
+        float sum = 0.0f;
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (n0 + nw + 32 * i + 8 * (r >> 2) + (r & 3) < op.N)
+                sum += __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -z));
+        } else {
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              part[r & 3] += __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -z));
+          sum = (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        sum += __shfl_xor(sum, 32, 64);
+        if (h == 0) red[wn * BM + ml] = make_float2(top == -__builtin_inff() ? top : z, sum);
+      } else {
+        if (!inside) continue;
+        const float l2 = a.fac.lse[m] * kLog2e;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            v[i][r] = __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -l2));
+        const int64_t tg = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
+        if (tg >= 0 && tg < TN * 32) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (tg == 32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) v[i][r] -= 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int nl = nw + 32 * i + 8 * g;
+            if (edge && n0 + nl >= a.fac.pitch) continue;  // the pitch is a multiple of 4
+            const float4 sw = *reinterpret_cast<const float4*>(swl + nl);
+            float f[4] = {v[i][4 * g] * sw.x, v[i][4 * g + 1] * sw.y, v[i][4 * g + 2] * sw.z,
+                          v[i][4 * g + 3] * sw.w};
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n0 + nl + e >= op.N) f[e] = 0.0f;
+            }
+            uint16_t* out = a.fac.P + m * a.fac.pitch + n0 + nl;
+            if (a.fac.planes == 1) {
+              *reinterpret_cast<uint2*>(out) = make_uint2(bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
+                                                          bf16_bits(f[2]) | bf16_bits(f[3]) << 16);
+              continue;
+            }
+            for (int p = 0; p < a.fac.planes; ++p) {
+              const bool last = p + 1 == a.fac.planes;
+              uint32_t b[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = bf16_part(f[e], last);
+              *reinterpret_cast<uint2*>(out + p * op.M * a.fac.pitch) =
+                  make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            }
+          }
+      }
     }
   }
   if constexpr (EPI == kLoss) {
@@ -245,73 +383,125 @@ __global__ __launch_bounds__(64 * WN * WM) void tile_kernel(TileArgs a) {
       if (m0 + ml >= op.M) break;
       float top = red[ml].x;
 #pragma unroll
-      for (int w = 1; w < WN; ++w) {
-        const float o = red[w * BM + ml].x;
-        top = o > top || o != o ? o : top;
-      }
+      for (int w = 1; w < WN; ++w) top = fmaxf(top, red[w * BM + ml].x);
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WN; ++w) {
-        const float2 p = red[w * BM + ml];
-        // a wave with no valid column has (-inf, 0)
-        sum += p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - top);
-      }
+      for (int w = 0; w < WN; ++w) sum += join_term(red[w * BM + ml], top);
       a.loss.part[(m0 + ml) * a.loss.ntiles + n0 / BN] = make_float2(top, sum);
     }
   }
 }
 
-// The tiles of each row joined by log-sum-exp, one wave per row.
-__global__ __launch_bounds__(256) void loss_join_kernel(LossOut o, float* loss, float* lse, int M,
-                                                        int64_t N) {
+// The tiles of each row joined by log-sum-exp, and the target's logit from its
+// own row of the weights (the same exact sum as in the tile that held it): one
+// wave per row.
+__global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, float* loss,
+                                                        float* lse) {
   const int lane = threadIdx.x & 63;
   const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (m >= M) return;
+  if (m >= op.M) return;
   const float2* p = o.part + m * o.ntiles;
+  const int64_t tg = o.target[m];
+  const bool hit = tg >= 0 && tg < op.N;
+  int dot = 0;
+  if (hit) {
+    const int8_t *x = op.X + m * op.ldx, *w = op.W + tg * op.ldw;
+    for (int k = 16 * lane; k < op.K; k += 1024) {
+      v4i a = *reinterpret_cast<const v4i*>(x + k);
+      const v4i b = *reinterpret_cast<const v4i*>(w + k);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int keep = op.K - k - 4 * c;  // bytes of this word before column K
+        if (keep < 4) a[c] = keep <= 0 ? 0 : a[c] & ((1 << (8 * keep)) - 1);
+        dot = __builtin_amdgcn_sdot4(a[c], b[c], dot, false);
+      }
+    }
+  }
   float top = -__builtin_inff();
-  for (int i = lane; i < o.ntiles; i += 64) {
-    const float z = p[i].x;
-    top = z > top || z != z ? z : top;
-  }
-  for (int d = 1; d < 64; d *= 2) {
-    const float z = __shfl_xor(top, d, 64);
-    top = z > top || z != z ? z : top;
-  }
+  for (int i = lane; i < o.ntiles; i += 64) top = fmaxf(top, p[i].x);
+  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
   float sum = 0.0f;
-  for (int i = lane; i < o.ntiles; i += 64) sum += p[i].y * __builtin_amdgcn_exp2f(p[i].x - top);
-  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+  for (int i = lane; i < o.ntiles; i += 64) sum += join_term(p[i], top);
+  for (int d = 1; d < 64; d *= 2) {
+    sum += __shfl_xor(sum, d, 64);
+    dot += __shfl_xor(dot, d, 64);
+  }
   if (lane == 0) {
     const float l2 = top + __builtin_log2f(sum);
-    const int64_t tg = o.target[m];
+    const float z = hit ? (float)dot * op.sw[tg] * (op.sx[m] * kLog2e) : __builtin_nanf("");
     lse[m] = l2 * kLn2;
-    loss[m] = tg < 0 ? 0.0f : tg >= N ? __builtin_nanf("") : (l2 - o.zt[m]) * kLn2;
+    loss[m] = tg < 0 ? 0.0f : (l2 - z) * kLn2;
   }
 }
 
-constexpr int kBN = 128;
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int kCUs = 256;
 
-int64_t tiles(int M, int N, int bm) { return ceil_div(M, bm) * ceil_div(N, kBN); }
-int pick_bm(int M) { return M <= 32 ? 32 : 128; }
+// The tiles, and how many of their workgroups a compute unit holds (by LDS).
+struct Tile {
+  int bn, bm, resident;
+};
+constexpr Tile kTiles[] = {{256, 256, 1}, {128, 256, 1}, {128, 128, 2}, {128, 64, 3}, {64, 64, 3}};
+constexpr int kTileCount = 5;
+
+int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div(N, c.bn); }
+
+// The tile with the least estimated time.  What the K loop waits for is its loads:
+// per compute unit 44, 52 and 62 bytes a nanosecond with one, two and three
+// workgroups on it; a step has a round trip of its own in it, which small tiles do
+// not get below; and an output costs 0.08 ns of epilogue.  Measured against it (us,
+// M N K; tiles as in kTiles): 2048 4096 12288 140 / 111 / 115 / 164 / -, 512 12288
+// 4096 53 / 37 / 37 / 37 / -, 333 4099 2048 34 / 22 / 14 / 10.8 / 11.0, 128 4096
+// 4096 45 / 30 / 19 / 15.9 / 14.2.
+int pick_tile(int M, int N, int K) {
+  const double steps = (double)ceil_div(K, kStep);
+  const double rate[4] = {0.0, 44.0, 52.0, 62.0};
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < kTileCount; ++i) {
+    const Tile& c = kTiles[i];
+    const int64_t n = tiles(c, M, N);
+    int64_t r = ceil_div(n, kCUs);
+    if (r > c.resident) r = c.resident;
+    const double rounds = (double)ceil_div(n, kCUs * r);
+    double step = (double)r * (c.bn + c.bm) * kStep / rate[r];
+    if (step < 400.0) step = 400.0;
+    const double t = rounds * (steps * step + 0.08 * (double)r * c.bn * c.bm);
+    if (i == 0 || t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  return best;
+}
+
+bool tiles_fit(int M, int N) { return tiles(kTiles[kTileCount - 1], M, N) <= kMaxGrid; }
 
 template <int EPI>
 int launch_tiles(TileArgs& a, hipStream_t st) {
-  const int bm = pick_bm(a.op.M);
-  const int64_t n = tiles(a.op.M, a.op.N, bm);
+  const int pick = pick_tile(a.op.M, a.op.N, a.op.K);
+  const Tile& c = kTiles[pick];
+  const int64_t n = tiles(c, a.op.M, a.op.N);
   if (n > kMaxGrid) return -1;
-  a.mtiles = (uint32_t)ceil_div(a.op.M, bm);
-  if (bm == 32)
-    tile_kernel<kBN, 32, 4, 1, EPI><<<(uint32_t)n, 256, 0, st>>>(a);
-  else
-    tile_kernel<kBN, 128, 2, 2, EPI><<<(uint32_t)n, 256, 0, st>>>(a);
+  a.mtiles = (uint32_t)ceil_div(a.op.M, c.bm);
+  a.ntiles = (uint32_t)ceil_div(a.op.N, c.bn);
+  a.group = 1024 / c.bm;
+  const dim3 grid((uint32_t)n);
+  switch (pick) {
+    case 0: tile_kernel<256, 256, 2, 4, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 1: tile_kernel<128, 256, 2, 4, 3, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 2: tile_kernel<128, 128, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 3: tile_kernel<128, 64, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
+    default: tile_kernel<64, 64, 2, 2, 3, EPI><<<grid, 256, 0, st>>>(a); break;
+  }
   return 0;
 }
 
 }  // namespace
 
-bool linear_fits(int M, int N) { return tiles(M, N, pick_bm(M)) <= kMaxGrid; }
-bool loss_fits(int M, int N, int) { return linear_fits(M, N); }
-bool factor_fits(int M, int N) { return linear_fits(M, N); }
+bool linear_fits(int M, int N) { return tiles_fit(M, N); }
+bool loss_fits(int M, int N, int) { return tiles_fit(M, N); }
+bool factor_fits(int M, int N) { return tiles_fit(M, N); }
 
 int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st) {
   TileArgs a{};
@@ -320,7 +510,9 @@ int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st) {
   return launch_tiles<kLinear>(a, st);
 }
 
-int loss_tiles(int, int N, int) { return (int)ceil_div(N, kBN); }
+int loss_tiles(int M, int N, int K) {
+  return (int)ceil_div(N, kTiles[pick_tile(M, N, K)].bn);
+}
 
 int launch_loss(const Operands& op, const LossOut& out, hipStream_t st) {
   TileArgs a{};
@@ -329,8 +521,9 @@ int launch_loss(const Operands& op, const LossOut& out, hipStream_t st) {
   return launch_tiles<kLoss>(a, st);
 }
 
-int launch_loss_join(const LossOut& o, float* loss, float* lse, int M, int N, hipStream_t st) {
-  loss_join_kernel<<<(uint32_t)ceil_div(M, 4), 256, 0, st>>>(o, loss, lse, M, N);
+int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* lse,
+                     hipStream_t st) {
+  loss_join_kernel<<<(uint32_t)ceil_div(op.M, 4), 256, 0, st>>>(op, o, loss, lse);
   return 0;
 }
 

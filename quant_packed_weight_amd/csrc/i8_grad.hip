@@ -2,9 +2,11 @@
 // A[m, n] W[n, k]: int8 weights, exact in bf16, against a factor A given as one
 // to three bf16 matrices whose sum it is; and the kernels before and after it.
 //
-// W is read as it lies, rows of N along the reduction, so its fragments are
-// transposed on the way from LDS to registers.  W^T is the MFMA's row operand: a
-// lane ends with one token and four consecutive k per register quad.
+// W is read as it lies, rows of N along the reduction: the transposing LDS read
+// hands each lane the eight consecutive n of its own k, which are converted to
+// bf16 in registers (int8 is exact there), so LDS and the loads hold one byte per
+// weight.  W^T is the MFMA's row operand: a lane ends with one token and four
+// consecutive k per register quad.
 #include "i8_common.h"
 
 namespace gemmq {
@@ -12,22 +14,49 @@ namespace i8 {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
-constexpr int kRed = 64;   // n per step: rows of 64 bytes of W's tile, 128 bytes of A's
-constexpr int kBK = 128;   // k per workgroup
+constexpr int kRed = 64;  // n per step: kRed rows of W's tile, 128 bytes of A's rows
 
 __device__ __forceinline__ v16f mfma_bf16(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-template <int BM, int WK, int WM>
-__global__ __launch_bounds__(64 * WK * WM) void grad_kernel(GradArgs a, uint32_t ktiles,
-                                                            uint32_t mtiles) {
+// eight int8 to bf16, exactly
+__device__ __forceinline__ v8bf widen(v2i w) {
+  v8bf r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = (__bf16)(float)(int8_t)(w[e >> 2] >> (8 * (e & 3)));
+  return r;
+}
+
+template <int BK, int BM>
+struct GradStage {
+  static constexpr int kW = 0, kA = kRed * BK, kBytes = kRed * BK + BM * 2 * kRed;
+};
+
+// W's LDS image: rows of BK bytes, chunk c of row n in slot c ^ 2 (n & 7): the
+// eight rows by two chunks that 32 lanes of a transposing read take lie in 16
+// different columns of 256 bytes.  (BK >= 256; rows of 128 bytes lie two to that
+// span, and take c ^ 2 ((n >> 1) & 3) instead.)
+template <int BK>
+__device__ __forceinline__ int wslot(int n, int chunk) {
+  return BK >= 256 ? chunk ^ ((n & 7) << 1) : chunk ^ (((n >> 1) & 3) << 1);
+}
+// A's image: as the int8 product's operands (i8_gemm.hip)
+__device__ __forceinline__ int aslot(int m, int chunk) { return chunk ^ ((m >> 1) & 7); }
+
+template <int BK, int BM, int WK, int WM, int DEPTH>
+__global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint32_t ktiles,
+                                                               uint32_t mtiles) {
   constexpr int NW = WK * WM;
-  constexpr int TK = kBK / WK / 32, TM = BM / WM / 32;
-  constexpr int kStageBytes = kRed * kBK + BM * 2 * kRed;
-  static_assert(kRed % (8 * NW) == 0 && BM % (8 * NW) == 0, "whole loads per wave");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+  constexpr int TK = BK / WK / 32, TM = BM / WM / 32;
+  using S = GradStage<BK, BM>;
+  constexpr int kRowsPer = 1024 / BK;  // rows of W per load
+  constexpr int kLw = kRed / kRowsPer / NW, kLa = BM / 8 / NW, kLoads = kLw + kLa;
+  static_assert(kLw * kRowsPer * NW == kRed && kLa * 8 * NW == BM && NW % 2 == 0,
+                "every wave issues the same loads");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -35,38 +64,54 @@ __global__ __launch_bounds__(64 * WK * WM) void grad_kernel(GradArgs a, uint32_t
   uint32_t id = xcd_order(blockIdx.x, gridDim.x);
   const int64_t m0 = (int64_t)(id % mtiles) * BM;
   id /= mtiles;
-  const int k0 = (int)(id % ktiles) * kBK, split = (int)(id / ktiles);
+  const int k0 = (int)(id % ktiles) * BK, split = (int)(id / ktiles);
 
-  // this split's share of the steps; a step has one load of W and A per plane
+  // this split's share of the steps of kRed rows; every plane goes over it
   const int steps = (a.N + kRed - 1) / kRed;
   const int per = steps / a.splits, more = steps % a.splits;
   const int first = split * per + min(split, more), count = per + (split < more ? 1 : 0);
+  const int its = count * a.planes;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int r8 = lane >> 3, chunk = 16 * ((lane & 7) ^ r8);
-  // chunks of W past column K repeat the last one: their columns are dropped
-  const int col = min(k0 + chunk, (a.K - 1) / 16 * 16);
   const int mvalid = (int)min((int64_t)BM, a.M - m0);
   const uint32_t arow = (uint32_t)(2 * a.pitch);
-
-  auto issue = [&](int it, uint32_t dst) {
-    const int step = first + it / a.planes, plane = it % a.planes;
-    const int64_t n = (int64_t)step * kRed;
-    const int nvalid = (int)min((int64_t)kRed, a.N - n);
-    const rsrc_t rw = gk::make_rsrc(a.W + n * a.ldw, (uint32_t)(nvalid * a.ldw));
-    // rows of W past the last one repeat it: the factor is zero there
+  int wrow[kLw];
+  uint32_t wcol[kLw], aoff[kLa];
 #pragma unroll
-    for (int j = 0; j < kRed / 8 / NW; ++j) {
-      const int r = min(8 * (wave + NW * j) + r8, nvalid - 1);
-      gk::dma16(rw, (uint32_t)(r * a.ldw) + col, 0, dst + 1024 * (wave + NW * j));
+  for (int j = 0; j < kLw; ++j) {
+    const int r = kRowsPer * (wave + NW * j) + lane / (BK / 16);
+    wrow[j] = r;
+    // chunks past column K repeat the last one: their columns are dropped
+    wcol[j] = (uint32_t)min(k0 + 16 * wslot<BK>(r, lane % (BK / 16)), (a.K - 1) / 16 * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < kLa; ++j) {
+    const int r = 8 * (wave + NW * j) + (lane >> 3);
+    // rows past the last token repeat it: their results are dropped
+    aoff[j] = (uint32_t)min(r, mvalid - 1) * arow + 16 * aslot(r, lane & 7);
+  }
+  // iteration `it` reads step first + it / planes of plane it % planes; `ahead`
+  // is the one that is loaded next
+  int astep = first, aplane = 0;
+  auto load = [&](int j, uint32_t take, uint32_t to) {
+    const int64_t n = (int64_t)min(astep, steps - 1) * kRed;
+    if (j < kLw) {
+      // rows of W past the last one repeat it: the factor is zero there
+      const int nvalid = (int)min((int64_t)kRed, a.N - n);
+      const rsrc_t rs = gk::make_rsrc(a.W + n * a.ldw, (uint32_t)(nvalid * a.ldw));
+      gk::dma16_if(take, rs, (uint32_t)(min(wrow[j], nvalid - 1) * (int)a.ldw) + wcol[j], 0,
+                   to + S::kW + 1024 * (wave + NW * j));
+    } else {
+      const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)aplane * a.M + m0) * a.pitch,
+                                      (uint32_t)mvalid * arow);
+      gk::dma16_if(take, rs, aoff[j - kLw], (uint32_t)(2 * n),
+                   to + S::kA + 1024 * (wave + NW * (j - kLw)));
     }
-    const rsrc_t ra = gk::make_rsrc(a.P + ((int64_t)plane * a.M + m0) * a.pitch,
-                                    (uint32_t)(mvalid * (int64_t)arow));
-#pragma unroll
-    for (int j = 0; j < BM / 8 / NW; ++j) {
-      const int r = min(8 * (wave + NW * j) + r8, mvalid - 1);
-      gk::dma16(ra, r * arow + (uint32_t)(2 * n) + chunk, 0,
-                dst + kRed * kBK + 1024 * (wave + NW * j));
+  };
+  auto advance = [&] {
+    if (++aplane == a.planes) {
+      aplane = 0;
+      ++astep;
     }
   };
 
@@ -78,39 +123,73 @@ __global__ __launch_bounds__(64 * WK * WM) void grad_kernel(GradArgs a, uint32_t
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const int its = count * a.planes;
-  if (its > 0) issue(0, lds0);
-  for (int it = 0; it < its; ++it) {
-    const uint8_t* cw = lds + (it & 1) * kStageBytes;
-    const uint8_t* ca = cw + kRed * kBK;
-    gk::wait_vm<0>();
-    gk::lds_barrier();
-    if (it + 1 < its) issue(it + 1, lds0 + ((it + 1) & 1) * kStageBytes);
+  // Two sets of fragments of a quarter step (16 n), as in the int8 product.  The
+  // transposing read: of each 16 lanes, lanes 2 r and 2 r + 1 give the addresses
+  // of the two halves of 16 k of row r, and lane i takes k i of the eight rows.
+  v2i wraw[2][TK];
+  v8bf af[2][TM];
+  constexpr int kReads = TK + TM, kProducts = TK * TM;
+  constexpr int kPerProduct = (2 * kReads + kProducts - 1) / kProducts;
+  const int h = lane >> 5;
+  auto read = [&](int stage, int q, int r) {
+    if (r < TK) {
+      const int n = 16 * q + 8 * h + ((lane & 15) >> 1);
+      const int c = 2 * (wk * TK + r) + ((lane >> 4) & 1);
+      const uint8_t* p = lds + stage * S::kBytes + S::kW + n * BK + 16 * wslot<BK>(n, c) +
+                         8 * (lane & 1);
+      wraw[q & 1][r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) v2i*)p);
+    } else {
+      const int m = (wm * TM + r - TK) * 32 + (lane & 31);
+      af[q & 1][r - TK] = *reinterpret_cast<const v8bf*>(
+          lds + stage * S::kBytes + S::kA + m * 2 * kRed + 16 * aslot(m, 2 * q + h));
+    }
+  };
+  auto quarter = [&](int q, int from, uint32_t take, uint32_t to) {
 #pragma unroll
-    for (int q = 0; q < kRed / 16; ++q) {
-      v8bf wf[TK], af[TM];
-#pragma unroll
-      for (int i = 0; i < TK; ++i) {
-        const int k = (wk * TK + i) * 32 + (lane & 31);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int n = 16 * q + 8 * (lane >> 5) + e;
-          wf[i][e] = (__bf16)(float)(int8_t)cw[n * kBK + 16 * ((k >> 4) ^ (n & 7)) + (k & 15)];
-        }
-      }
+    for (int i = 0; i < TK; ++i) {
+      const v8bf w = widen(wraw[q & 1][i]);
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const int m = (wm * TM + j) * 32 + (lane & 31), c = 2 * q + (lane >> 5);
-        af[j] = *reinterpret_cast<const v8bf*>(ca + m * 128 + 16 * (c ^ (m & 7)));
+        const int p = i * TM + j;
+        acc[i][j] = mfma_bf16(w, af[q & 1][j], acc[i][j]);
+        if (j == TM - 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = p * kPerProduct; r < (p + 1) * kPerProduct && r < kReads; ++r)
+          read(from, (q + 1) & 3, r);
+        if (q == 3) {
+#pragma unroll
+          for (int l = p * kLoads / kProducts; l < (p + 1) * kLoads / kProducts; ++l)
+            load(l, take, to);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < TK; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = mfma_bf16(wf[i], af[j], acc[i][j]);
     }
+  };
+
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load(j, s < its, lds0 + s * S::kBytes);
+    advance();
+  }
+  if (its > 0) {
+    wait_vm_if<(DEPTH - 1) * kLoads>(its >= DEPTH);
+    gk::lds_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(0, 0, r);
+  }
+  int buf = 0;
+  for (int it = 0; it < its; ++it) {
+    const int nbuf = buf == DEPTH - 1 ? 0 : buf + 1;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) quarter(q, buf, 0, 0);
+    wait_vm_if<(DEPTH - 2) * kLoads>(it + DEPTH - 1 < its);
+    gk::lds_barrier();
+    quarter(3, nbuf, it + DEPTH < its, lds0 + buf * S::kBytes);
+    advance();
+    buf = nbuf;
   }
 
-  const int h = lane >> 5;
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int64_t m = m0 + (wm * TM + j) * 32 + (lane & 31);
@@ -175,31 +254,40 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* acc, int64_t k
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
-int pick_bm(int M) { return M <= 32 ? 32 : 128; }
+
+struct Tile {
+  int bk, bm;
+};
+Tile pick_tile(int M) { return M <= 32 ? Tile{128, 32} : M <= 128 ? Tile{128, 128} : Tile{256, 256}; }
+
+int64_t tiles(int M, int K) {
+  const Tile c = pick_tile(M);
+  return ceil_div(M, c.bm) * ceil_div(K, c.bk);
+}
 
 }  // namespace
 
 int grad_splits(int M, int N, int K, int) {
-  const int64_t tiles = ceil_div(M, pick_bm(M)) * ceil_div(K, kBK);
   const int64_t steps = ceil_div(N, kRed);
-  int64_t s = ceil_div(512, tiles);
+  int64_t s = ceil_div(256, tiles(M, K));
   if (s > steps / 4) s = steps / 4;
   return s < 1 ? 1 : (int)s;
 }
 
 bool grad_fits(int M, int K, int splits) {
-  return ceil_div(M, pick_bm(M)) * ceil_div(K, kBK) * splits <= kMaxGrid &&
-         ceil_div((int64_t)M * K, 256) <= kMaxGrid;
+  return tiles(M, K) * splits <= kMaxGrid && ceil_div((int64_t)M * K, 256) <= kMaxGrid;
 }
 
 int launch_grad(const GradArgs& a, hipStream_t st) {
-  const int bm = pick_bm(a.M);
-  const int64_t mt = ceil_div(a.M, bm), kt = ceil_div(a.K, kBK), n = mt * kt * a.splits;
+  const Tile c = pick_tile(a.M);
+  const int64_t mt = ceil_div(a.M, c.bm), kt = ceil_div(a.K, c.bk), n = mt * kt * a.splits;
   if (n > kMaxGrid) return -1;
-  if (bm == 32)
-    grad_kernel<32, 4, 1><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
+  if (c.bm == 32)
+    grad_kernel<128, 32, 4, 1, 3><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
+  else if (c.bm == 128)
+    grad_kernel<128, 128, 2, 2, 3><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
   else
-    grad_kernel<128, 2, 2><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
+    grad_kernel<256, 256, 4, 2, 3><<<(uint32_t)n, 512, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
   return 0;
 }
 
