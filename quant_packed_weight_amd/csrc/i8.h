@@ -14,6 +14,11 @@ namespace i8 {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t type_bytes(int type) { return type == GEMMQ_F32 ? 4 : 2; }
 
+// whether every row of a matrix can be read 16 bytes at a time from its first value
+inline bool wide_rows(const void* p, int64_t ld, int type) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * type_bytes(type) % 16 == 0;
+}
+
 // bf16 numbers that carry one value of `type` in the gradient's products
 // (8 significant bits each): all of a bf16, f16's 11 bits, all of an f32.
 inline int planes_of(int type) { return type == GEMMQ_BF16 ? 1 : type == GEMMQ_F16 ? 2 : 3; }
@@ -60,16 +65,25 @@ struct FactorOut {
 int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
                     int K, hipStream_t st);
 
-// i8_gemm.hip: each with its own check of the grid
-bool linear_fits(int M, int N);
+// i8_gemm.hip: the product by tiles in LDS, or by i8_skinny.hip's stream of W where
+// that is faster; each with its own check of the grid
+bool product_fits(int M, int N, int K);
 int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st);
 int loss_tiles(int M, int N, int K);  // column tiles of the loss launch (LossOut::ntiles)
-bool loss_fits(int M, int N, int K);
 int launch_loss(const Operands& op, const LossOut& out, hipStream_t st);
 int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* lse,
                      hipStream_t st);
-bool factor_fits(int M, int N);
 int launch_factor(const Operands& op, const FactorOut& out, hipStream_t st);
+
+// i8_skinny.hip, M <= kSkinnyMaxM
+constexpr int kSkinnyMaxM = 64, kSkinnyChannels = 16;  // channels per workgroup
+int launch_skinny(const Operands& op, const LinearOut& out, hipStream_t st);
+int launch_skinny(const Operands& op, const LossOut& out, hipStream_t st);
+int launch_skinny(const Operands& op, const FactorOut& out, hipStream_t st);
+// the layer in one launch: X quantized by every workgroup, one writes op.X and op.sx
+bool fuses(int M, int N, int K);
+int launch_fused(int xtype, const void* X, int64_t ldx, const Operands& op, const LinearOut& out,
+                 hipStream_t st);
 
 // i8_grad.hip: acc[s][m][k] (+)= sum over the s-th range of n of
 // (sum of planes)[m, n] * W[n, k], the ranges covering the piece's columns.

@@ -78,7 +78,7 @@ GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K) {
 }
 
 bool grad_shape_ok(int64_t M, int64_t N, int64_t K, const GradPlan& p) {
-  return grad_fits((int)M, (int)K, p.splits) && factor_fits((int)M, (int)p.piece) &&
+  return grad_fits((int)M, (int)K, p.splits) && product_fits((int)M, (int)p.piece, (int)K) &&
          ceil_div(M * (p.piece / 4), 256) <= 0x7fffffff && N >= 0;
 }
 
@@ -116,7 +116,7 @@ int check_product(const int8_t* W, int64_t ldw, const float* sw, const int8_t* X
   if (rc == GEMMQ_OK) rc = check_rows(ytype, Y, ldy, N);
   if (rc != GEMMQ_OK) return rc;
   if (bias && !aligned(bias, 4)) return GEMMQ_E_ALIGNMENT;
-  if (!linear_fits((int)M, (int)N)) return GEMMQ_E_SHAPE;
+  if (!product_fits((int)M, (int)N, (int)K)) return GEMMQ_E_SHAPE;
   op = Operands{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
   out = LinearOut{bias, Y, ldy, ytype,
                   ldy % 4 == 0 && aligned(Y, (uintptr_t)(4 * type_bytes(ytype)))};
@@ -160,6 +160,8 @@ int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, co
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_pending();
+  if (N > 0 && fuses((int)M, (int)N, (int)K))
+    return launched(launch_fused(xtype, X, ldx, op, out, st));
   rc = launched(launch_quantize(xtype, X, ldx, Xq, ldq, sx, (int)M, (int)K, st));
   if (rc != GEMMQ_OK || N == 0) return rc;
   return launched(launch_linear(op, out, st));
@@ -207,7 +209,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
 }
 
 size_t gemmq_loss_i8_workspace(int64_t M, int64_t N, int64_t K) {
-  if (check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0 || !loss_fits((int)M, (int)N, (int)K))
+  if (check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0 || !product_fits((int)M, (int)N, (int)K))
     return 0;
   return align_up(8 * M * loss_tiles((int)M, (int)N, (int)K), 256);
 }

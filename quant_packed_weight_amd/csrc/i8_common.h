@@ -14,6 +14,11 @@ using gk::v4i;
 
 typedef __bf16 bf16_t;
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// what a product's kernel does with its sums
+enum Epilogue { kLinear, kLoss, kFactor };
+
 // f32 -> the type's 16 bits, round to nearest even
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (bf16_t)v);
@@ -88,6 +93,88 @@ __device__ __forceinline__ void wait_vm_if(bool most) {
         "1:\ts_waitcnt vmcnt(0)\n2:" ::"s"(t),
         "i"(N)
         : "memory", "scc");
+  }
+}
+
+// f[0..3] as `planes` matrices of bf16 parts, `plane` elements apart
+__device__ __forceinline__ void store_planes(uint16_t* p, int64_t plane, int planes, float (&f)[4]) {
+  if (planes == 1) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
+                                              bf16_bits(f[2]) | bf16_bits(f[3]) << 16);
+    return;
+  }
+  for (int i = 0; i < planes; ++i) {
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = bf16_part(f[e], i + 1 == planes);
+    *reinterpret_cast<uint2*>(p + i * plane) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  }
+}
+
+// the first `keep` bytes of v, the others zero
+__device__ __forceinline__ v4i keep_bytes(v4i v, int keep) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int b = keep - 4 * w;
+    v[w] = b >= 4 ? v[w] : b <= 0 ? 0 : v[w] & ((1 << (8 * b)) - 1);
+  }
+  return v;
+}
+
+// ---- the row quantizer's arithmetic (gemmq_quantize_i8)
+
+// |x| as an unsigned integer: ordered as the values, infinity above every finite
+// one and NaN above infinity, so that a maximum shows either.
+__device__ __forceinline__ uint32_t abs_bits(float x) {
+  return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+}
+// a row's scale from its largest abs_bits: NaN where the row is not finite
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  return top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
+}
+// x / s to the nearest integer, ties to even, within [-127, 127]; 0 where s is 0
+// or NaN
+__device__ __forceinline__ int quantized(float x, float s) {
+  const float q = s > 0.0f ? rintf(x / s) : 0.0f;
+  return (int)fminf(fmaxf(q, -127.0f), 127.0f);
+}
+
+// V consecutive values of a row from element i as f32, zero from element `end`
+// of the row on (`left` values are left before it); at once where the row allows
+// 16-byte loads and all are there
+template <int TYPE, int V>
+__device__ __forceinline__ void load_values(const void* p, int64_t i, int64_t left, bool wide,
+                                            float (&v)[V]) {
+  static_assert(V == (TYPE == GEMMQ_F32 ? 4 : 8), "16 bytes");
+  if (wide && left >= V) {
+    if constexpr (TYPE == GEMMQ_F32) {
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = (u[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+        v[e] = TYPE == GEMMQ_BF16 ? __builtin_bit_cast(float, b << 16)
+                                  : (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = e < left ? load_as_f32(p, i + e, TYPE) : 0.0f;
+}
+
+// V quantized values as bytes
+template <int V>
+__device__ __forceinline__ void quantize_values(const float (&v)[V], float s,
+                                                uint32_t (&q)[V / 4]) {
+#pragma unroll
+  for (int w = 0; w < V / 4; ++w) {
+    q[w] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[w] |= ((uint32_t)quantized(v[4 * w + e], s) & 0xffu) << (8 * e);
   }
 }
 

@@ -14,8 +14,6 @@ namespace gemmq {
 namespace i8 {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
 // LDS image of a step: rows of 128 bytes, eight 16-byte chunks each, chunk c of
 // row r in slot c ^ ((r >> 1) & 7).  Sixteen rows whose numbers differ in their
 // low four bits then have the same chunk in sixteen different 16-byte columns of
@@ -24,8 +22,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStep = 128;
 
 __device__ __forceinline__ int slot(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
-
-enum Epilogue { kLinear, kLoss, kFactor };
 
 struct TileArgs {
   Operands op;
@@ -359,20 +355,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
               for (int e = 0; e < 4; ++e)
                 if (n0 + nl + e >= op.N) f[e] = 0.0f;
             }
-            uint16_t* out = a.fac.P + m * a.fac.pitch + n0 + nl;
-            if (a.fac.planes == 1) {
-              *reinterpret_cast<uint2*>(out) = make_uint2(bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
-                                                          bf16_bits(f[2]) | bf16_bits(f[3]) << 16);
-              continue;
-            }
-            for (int p = 0; p < a.fac.planes; ++p) {
-              const bool last = p + 1 == a.fac.planes;
-              uint32_t b[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) b[e] = bf16_part(f[e], last);
-              *reinterpret_cast<uint2*>(out + p * op.M * a.fac.pitch) =
-                  make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-            }
+            store_planes(a.fac.P + m * a.fac.pitch + n0 + nl, (int64_t)op.M * a.fac.pitch,
+                         a.fac.planes, f);
           }
       }
     }
@@ -394,41 +378,49 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
 
 // The tiles of each row joined by log-sum-exp, and the target's logit from its
 // own row of the weights (the same exact sum as in the tile that held it): one
-// wave per row.
+// workgroup per row.
 __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, float* loss,
                                                         float* lse) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (m >= op.M) return;
+  __shared__ float tops[4], sums[4];
+  __shared__ int dots[4];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t m = blockIdx.x;
   const float2* p = o.part + m * o.ntiles;
   const int64_t tg = o.target[m];
   const bool hit = tg >= 0 && tg < op.N;
   int dot = 0;
   if (hit) {
     const int8_t *x = op.X + m * op.ldx, *w = op.W + tg * op.ldw;
-    for (int k = 16 * lane; k < op.K; k += 1024) {
-      v4i a = *reinterpret_cast<const v4i*>(x + k);
+    for (int k = 16 * t; k < op.K; k += 4096) {
+      const v4i a = keep_bytes(*reinterpret_cast<const v4i*>(x + k), op.K - k);
       const v4i b = *reinterpret_cast<const v4i*>(w + k);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int keep = op.K - k - 4 * c;  // bytes of this word before column K
-        if (keep < 4) a[c] = keep <= 0 ? 0 : a[c] & ((1 << (8 * keep)) - 1);
-        dot = __builtin_amdgcn_sdot4(a[c], b[c], dot, false);
-      }
+      for (int c = 0; c < 4; ++c) dot = __builtin_amdgcn_sdot4(a[c], b[c], dot, false);
     }
   }
   float top = -__builtin_inff();
-  for (int i = lane; i < o.ntiles; i += 64) top = fmaxf(top, p[i].x);
-  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
-  float sum = 0.0f;
-  for (int i = lane; i < o.ntiles; i += 64) sum += join_term(p[i], top);
+  for (int i = t; i < o.ntiles; i += 256) top = fmaxf(top, p[i].x);
+#pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    sum += __shfl_xor(sum, d, 64);
+    top = fmaxf(top, __shfl_xor(top, d, 64));
     dot += __shfl_xor(dot, d, 64);
   }
   if (lane == 0) {
-    const float l2 = top + __builtin_log2f(sum);
-    const float z = hit ? (float)dot * op.sw[tg] * (op.sx[m] * kLog2e) : __builtin_nanf("");
+    tops[wave] = top;
+    dots[wave] = dot;
+  }
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  float sum = 0.0f;
+  for (int i = t; i < o.ntiles; i += 256) sum += join_term(p[i], top);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  if (t == 0) {
+    const float l2 = top + __builtin_log2f((sums[0] + sums[1]) + (sums[2] + sums[3]));
+    const int d = (dots[0] + dots[1]) + (dots[2] + dots[3]);
+    const float z = hit ? (float)d * op.sw[tg] * (op.sx[m] * kLog2e) : __builtin_nanf("");
     lse[m] = l2 * kLn2;
     loss[m] = tg < 0 ? 0.0f : (l2 - z) * kLn2;
   }
@@ -441,8 +433,9 @@ constexpr int kCUs = 256;
 struct Tile {
   int bn, bm, resident;
 };
-constexpr Tile kTiles[] = {{256, 256, 1}, {128, 256, 1}, {128, 128, 2}, {128, 64, 3}, {64, 64, 3}};
-constexpr int kTileCount = 5;
+constexpr Tile kTiles[] = {{256, 256, 1}, {128, 256, 1}, {128, 128, 2}, {128, 64, 3}, {64, 64, 3},
+                           {128, 32, 2},  {64, 32, 3}};
+constexpr int kTileCount = 7;
 
 int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div(N, c.bn); }
 
@@ -450,15 +443,19 @@ int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div
 // per compute unit 44, 52 and 62 bytes a nanosecond with one, two and three
 // workgroups on it; a step has a round trip of its own in it, which small tiles do
 // not get below; and an output costs 0.08 ns of epilogue.  Measured against it (us,
-// M N K; tiles as in kTiles): 2048 4096 12288 140 / 111 / 115 / 164 / -, 512 12288
-// 4096 53 / 37 / 37 / 37 / -, 333 4099 2048 34 / 22 / 14 / 10.8 / 11.0, 128 4096
-// 4096 45 / 30 / 19 / 15.9 / 14.2.
+// M N K; tiles in the order of kTiles): 2048 4096 12288 140 / 111 / 115 / 164 / -,
+// 512 12288 4096 53 / 37 / 37 / 37 / -, 333 4099 2048 34 / 22 / 14 / 10.8 / 11.0,
+// 128 4096 4096 45 / 30 / 19 / 15.9 / 14.2.  Up to 32 tokens one row of tiles is
+// all there is, and W's stream decides: 128 channels where the chip is full many
+// times over (M = 8, 151936 x 2048 57 us, 64 channels 59), 64 otherwise (M = 16,
+// 12288 x 4096 17 us, 128 channels 19).
 int pick_tile(int M, int N, int K) {
+  if (M <= 32) return N > 65536 ? 5 : 6;
   const double steps = (double)ceil_div(K, kStep);
   const double rate[4] = {0.0, 44.0, 52.0, 62.0};
   int best = 0;
   double least = 0.0;
-  for (int i = 0; i < kTileCount; ++i) {
+  for (int i = 0; i < 5; ++i) {
     const Tile& c = kTiles[i];
     const int64_t n = tiles(c, M, N);
     int64_t r = ceil_div(n, kCUs);
@@ -475,7 +472,15 @@ int pick_tile(int M, int N, int K) {
   return best;
 }
 
-bool tiles_fit(int M, int N) { return tiles(kTiles[kTileCount - 1], M, N) <= kMaxGrid; }
+// Few tokens: the stream into registers, whose waves share a workgroup's K, where
+// the tiles would be too few to fill the chip (us, stream / tiles: M = 8, 4096 x
+// 4096 5.9 / 14; M = 16, 12288 x 4096 16 / 17; M = 64, 4096 x 4096 12.7 / 14).
+// `linear` at M <= 4 also beyond (151936 x 2048 at M = 1 53 / 58, M = 4 57 / 59);
+// the loss would have more partial sums to join there.
+bool skinny(int M, int N, bool linear) {
+  if (M <= 4 && linear) return true;
+  return N <= (M <= 16 ? 16384 : M <= 32 ? 8192 : M <= kSkinnyMaxM ? 6144 : 0);
+}
 
 template <int EPI>
 int launch_tiles(TileArgs& a, hipStream_t st) {
@@ -492,18 +497,21 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
     case 1: tile_kernel<128, 256, 2, 4, 3, EPI><<<grid, 512, 0, st>>>(a); break;
     case 2: tile_kernel<128, 128, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
     case 3: tile_kernel<128, 64, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
-    default: tile_kernel<64, 64, 2, 2, 3, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 4: tile_kernel<64, 64, 2, 2, 3, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 5: tile_kernel<128, 32, 4, 1, 3, EPI><<<grid, 256, 0, st>>>(a); break;
+    default: tile_kernel<64, 32, 2, 1, 4, EPI><<<grid, 128, 0, st>>>(a); break;
   }
   return 0;
 }
 
 }  // namespace
 
-bool linear_fits(int M, int N) { return tiles_fit(M, N); }
-bool loss_fits(int M, int N, int) { return tiles_fit(M, N); }
-bool factor_fits(int M, int N) { return tiles_fit(M, N); }
+bool product_fits(int M, int N, int K) {
+  return tiles(kTiles[pick_tile(M, N, K)], M, N) <= kMaxGrid;
+}
 
 int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st) {
+  if (skinny(op.M, op.N, true)) return launch_skinny(op, out, st);
   TileArgs a{};
   a.op = op;
   a.lin = out;
@@ -511,10 +519,12 @@ int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st) {
 }
 
 int loss_tiles(int M, int N, int K) {
-  return (int)ceil_div(N, kTiles[pick_tile(M, N, K)].bn);
+  const int width = skinny(M, N, false) ? kSkinnyChannels : kTiles[pick_tile(M, N, K)].bn;
+  return (int)ceil_div(N, width);
 }
 
 int launch_loss(const Operands& op, const LossOut& out, hipStream_t st) {
+  if (skinny(op.M, op.N, false)) return launch_skinny(op, out, st);
   TileArgs a{};
   a.op = op;
   a.loss = out;
@@ -523,11 +533,12 @@ int launch_loss(const Operands& op, const LossOut& out, hipStream_t st) {
 
 int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* lse,
                      hipStream_t st) {
-  loss_join_kernel<<<(uint32_t)ceil_div(op.M, 4), 256, 0, st>>>(op, o, loss, lse);
+  loss_join_kernel<<<(uint32_t)op.M, 256, 0, st>>>(op, o, loss, lse);
   return 0;
 }
 
 int launch_factor(const Operands& op, const FactorOut& out, hipStream_t st) {
+  if (skinny(op.M, op.N, false)) return launch_skinny(op, out, st);
   TileArgs a{};
   a.op = op;
   a.fac = out;

@@ -6,33 +6,63 @@ namespace gemmq {
 namespace i8 {
 namespace {
 
-// |x| as an unsigned integer: ordered as the values, infinity above every finite
-// one and NaN above infinity, so that the maximum shows either.
-__device__ __forceinline__ uint32_t abs_bits(float x) {
-  return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
-}
+// One workgroup per row; a thread keeps up to kHeld 16-byte loads of it in
+// registers between the two passes (rows of up to 8192 f32 or 16384 bf16 and f16
+// values are read once), and reads what is beyond them again.
+constexpr int kHeld = 8;
 
-// One workgroup per row, two passes over it (the second from cache).
 template <int TYPE>
-__global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ldx, int8_t* Q,
-                                                       int64_t ldq, float* s, int K) {
-  __shared__ uint32_t top[4];
-  const int64_t m = blockIdx.x;
+__global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ldx, bool wide,
+                                                       int8_t* Q, int64_t ldq, float* s, int K) {
+  constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8, kSpan = 256 * V;
+  __shared__ uint32_t tops[4];
+  const int64_t m = blockIdx.x, x0 = m * ldx;
   const int t = threadIdx.x;
-  const int64_t x0 = m * ldx;
-  uint32_t a = 0;
-  for (int k = t; k < K; k += 256) a = max(a, abs_bits(load_as_f32(X, x0 + k, TYPE)));
-  for (int d = 1; d < 64; d *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, d, 64));
-  if ((t & 63) == 0) top[t >> 6] = a;
+  float held[kHeld][V];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k = kSpan * i + V * t;
+    if (kSpan * i < K) load_values<TYPE, V>(X, x0 + k, K - k, wide, held[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (kSpan * i < K) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) top = max(top, abs_bits(held[i][e]));
+    }
+  for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
+    float v[V];
+    load_values<TYPE, V>(X, x0 + k, K - k, wide, v);
+#pragma unroll
+    for (int e = 0; e < V; ++e) top = max(top, abs_bits(v[e]));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
-  a = max(max(top[0], top[1]), max(top[2], top[3]));
-  const bool finite = a < 0x7f800000u;
-  const float d = __builtin_bit_cast(float, a) / 127.0f;
-  if (t == 0) s[m] = finite ? d : __builtin_nanf("");
-  const bool live = finite && d > 0.0f;
-  for (int k = t; k < K; k += 256) {
-    const float q = live ? rintf(load_as_f32(X, x0 + k, TYPE) / d) : 0.0f;
-    Q[m * ldq + k] = (int8_t)fminf(fmaxf(q, -127.0f), 127.0f);
+  const float sc = scale_of(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+  if (t == 0) s[m] = sc;
+  auto store = [&](int k, const float (&v)[V]) {
+    uint32_t q[V / 4];
+    quantize_values<V>(v, sc, q);
+    int8_t* to = Q + m * ldq + k;
+    if (k + V <= K) {
+#pragma unroll
+      for (int w = 0; w < V / 4; ++w) reinterpret_cast<uint32_t*>(to)[w] = q[w];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (k + e < K) to[e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (kSpan * i < K) store(kSpan * i + V * t, held[i]);
+  for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
+    float v[V];
+    load_values<TYPE, V>(X, x0 + k, K - k, wide, v);
+    store(k, v);
   }
 }
 
@@ -41,12 +71,13 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
 int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
                     int K, hipStream_t st) {
   const dim3 g((uint32_t)M);
+  const bool wide = wide_rows(X, ldx, type);
   if (type == GEMMQ_F32)
-    quantize_kernel<GEMMQ_F32><<<g, 256, 0, st>>>(X, ldx, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_F32><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
   else if (type == GEMMQ_BF16)
-    quantize_kernel<GEMMQ_BF16><<<g, 256, 0, st>>>(X, ldx, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_BF16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
   else
-    quantize_kernel<GEMMQ_F16><<<g, 256, 0, st>>>(X, ldx, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_F16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
   return 0;
 }
 
