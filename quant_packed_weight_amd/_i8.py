@@ -134,8 +134,9 @@ def _elsewhere(device, stream):
 
 
 def _here(device):
-    """The current stream of the current device, as the C side takes it."""
-    return _torch.cuda.current_stream(device).cuda_stream or None
+    """The current stream of the current device, as the C side takes it (the same
+    handle as torch.cuda.current_stream's, without building a Stream for it)."""
+    return _torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
 def _new_i8(rows, cols, device):

@@ -40,7 +40,8 @@ struct LinearOut {
   void* Y;
   int64_t ldy;
   int type;
-  bool wide;  // four consecutive values of a row may be stored at once
+  bool wide;   // four consecutive values of a row may be stored at once
+  bool lines;  // of 16 bits, and eight may
 };
 
 // Softmax statistics per column tile: (max, sum of exp2(z - max)) of the base-2
@@ -85,30 +86,46 @@ bool fuses(int M, int N, int K);
 int launch_fused(int xtype, const void* X, int64_t ldx, const Operands& op, const LinearOut& out,
                  hipStream_t st);
 
-// i8_grad.hip: acc[s][m][k] (+)= sum over the s-th range of n of
-// (sum of planes)[m, n] * W[n, k], the ranges covering the piece's columns.
+// i8_grad.hip: v[m, k] = sum over n of (sum of planes)[m, n] * W[n, k], by ranges
+// of n: range s gives acc[s][m][k] (+)= its sum, which launch_finish adds up, or,
+// where there is one range and one piece (acc null), the result itself.
+struct GradOut {
+  // dX[m] = v[m] * g[m] (g null: 1), zero where target[m] < 0 and NaN where it is
+  // nvocab or more (target null: neither)
+  const float* g;
+  const int64_t* target;
+  int64_t nvocab;
+  int type;
+  void* dX;
+  int64_t lddx;
+  bool wide;  // four consecutive values of a row may be stored at once
+};
 struct GradArgs {
   const int8_t* W;     // the piece's first row
   int64_t ldw;
   const uint16_t* P;   // planes of [M, pitch]
   int64_t pitch;       // a multiple of 64
-  float* acc;          // [splits][M][kp]
+  float* acc;          // [splits][M][kp], or null
   int64_t kp;          // pitch of a row of acc, a multiple of 4, >= K
-  int M, N, K, planes, splits;
+  int M, N, K, planes;
+  int tile, splits;    // of grad_split
   bool add;            // add to what acc holds (a later piece)
+  GradOut out;
 };
-int grad_splits(int M, int N, int K, int planes);
-bool grad_fits(int M, int K, int splits);
+struct GradSplit {
+  int tile, splits;
+};
+// the tile and the ranges for pieces of N columns; `whole`: there is one piece
+GradSplit grad_split(int M, int N, int K, int planes, bool whole);
+bool grad_fits(const GradSplit& s, int M, int K);
 int launch_grad(const GradArgs& a, hipStream_t st);
 
 // planes of dY * sw for columns [n0, n0 + N) of dY; columns up to the pitch zero
 int launch_planes(int type, const void* dY, int64_t lddy, const float* sw, uint16_t* P,
                   int64_t pitch, int planes, int M, int N, hipStream_t st);
 
-// dX = g[m] * sum over splits of acc (g null: 1); rows with target[m] < 0 zero,
-// with target[m] >= nvocab NaN
-int launch_finish(const float* acc, int64_t kp, int splits, const float* g, const int64_t* target,
-                  int64_t nvocab, int type, void* dX, int64_t lddx, int M, int K, hipStream_t st);
+int launch_finish(const float* acc, int64_t kp, int splits, const GradOut& out, int M, int K,
+                  hipStream_t st);
 
 }  // namespace i8
 }  // namespace gemmq

@@ -51,12 +51,14 @@ size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 // (it then stays in the 256 MB last-level cache between the launch that writes
 // it and the one that reads it, and bounds the workspace), or of kMinPiece
 // columns where the rows alone are more.
-constexpr int64_t kFactorBytes = (int64_t)128 << 20;
+constexpr int64_t kFactorBytes = (int64_t)384 << 20;
 constexpr int64_t kMinPiece = 1024;
 
 struct GradPlan {
-  int planes, splits;
+  int planes;
+  GradSplit split;
   int64_t piece, kp;
+  bool direct;  // one piece and one range: no partial sums
   size_t factor_bytes, acc_bytes;
   size_t bytes() const { return factor_bytes + acc_bytes; }
 };
@@ -71,15 +73,50 @@ GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K) {
   const int64_t pieces = ceil_div(n64, most);
   p.piece = pieces == 1 ? n64 : (int64_t)align_up(ceil_div(n64, pieces), 256);
   p.kp = (int64_t)align_up(K, 4);
-  p.splits = grad_splits((int)M, (int)p.piece, (int)K, p.planes);
+  p.split = grad_split((int)M, (int)p.piece, (int)K, p.planes, pieces == 1);
+  p.direct = pieces == 1 && p.split.splits == 1;
   p.factor_bytes = align_up(2 * p.planes * M * p.piece, 256);
-  p.acc_bytes = align_up(4 * p.splits * M * p.kp, 256);
+  p.acc_bytes = p.direct ? 0 : align_up(4 * p.split.splits * M * p.kp, 256);
   return p;
 }
 
-bool grad_shape_ok(int64_t M, int64_t N, int64_t K, const GradPlan& p) {
-  return grad_fits((int)M, (int)K, p.splits) && product_fits((int)M, (int)p.piece, (int)K) &&
-         ceil_div(M * (p.piece / 4), 256) <= 0x7fffffff && N >= 0;
+bool grad_shape_ok(int64_t M, int64_t K, const GradPlan& p) {
+  return grad_fits(p.split, (int)M, (int)K) && product_fits((int)M, (int)p.piece, (int)K);
+}
+
+// The pieces of a gradient: `factor` enqueues the factor of columns [n0, n0 + n)
+// at a pitch into the workspace, and the product with W's rows follows it.
+template <class Factor>
+int run_grad(const GradPlan& p, const int8_t* W, int64_t ldw, const GradOut& out, int64_t M,
+             int64_t N, int64_t K, void* ws, hipStream_t st, Factor factor) {
+  uint16_t* P = static_cast<uint16_t*>(ws);
+  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.factor_bytes);
+  clear_pending();
+  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
+    const int64_t n = N - n0 < p.piece ? N - n0 : p.piece;
+    const int64_t pitch = (int64_t)align_up(n, 64);
+    int rc = launched(factor(n0, n, P, pitch));
+    if (rc != GEMMQ_OK) return rc;
+    const GradArgs g{W + n0 * ldw, ldw,      P,
+                     pitch,        p.direct ? nullptr : acc, p.kp,
+                     (int)M,       (int)n,   (int)K,
+                     p.planes,     p.split.tile, p.split.splits,
+                     n0 > 0,       out};
+    rc = launched(launch_grad(g, st));
+    if (rc != GEMMQ_OK) return rc;
+  }
+  if (p.direct && N > 0) return GEMMQ_OK;
+  return launched(
+      launch_finish(acc, p.kp, N > 0 ? p.split.splits : 0, out, (int)M, (int)K, st));
+}
+
+GradOut grad_out(int type, void* dX, int64_t lddx) {
+  GradOut o{};
+  o.type = type;
+  o.dX = dX;
+  o.lddx = lddx;
+  o.wide = lddx % 4 == 0 && aligned(dX, (uintptr_t)(4 * type_bytes(type)));
+  return o;
 }
 
 }  // namespace
@@ -119,7 +156,8 @@ int check_product(const int8_t* W, int64_t ldw, const float* sw, const int8_t* X
   if (!product_fits((int)M, (int)N, (int)K)) return GEMMQ_E_SHAPE;
   op = Operands{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
   out = LinearOut{bias, Y, ldy, ytype,
-                  ldy % 4 == 0 && aligned(Y, (uintptr_t)(4 * type_bytes(ytype)))};
+                  ldy % 4 == 0 && aligned(Y, (uintptr_t)(4 * type_bytes(ytype))),
+                  type_bytes(ytype) == 2 && wide_rows(Y, ldy, ytype)};
   return GEMMQ_OK;
 }
 
@@ -170,7 +208,7 @@ int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, co
 size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
   if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0) return 0;
   const GradPlan p = grad_plan(type, M, N, K);
-  return grad_shape_ok(M, N, K, p) ? p.bytes() : 0;
+  return grad_shape_ok(M, K, p) ? p.bytes() : 0;
 }
 
 int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type, const void* dY,
@@ -185,27 +223,17 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
   if (rc == GEMMQ_OK && N > 0) rc = check_rows(type, dY, lddy, N);
   if (rc != GEMMQ_OK) return rc;
   const GradPlan p = grad_plan(type, M, N, K);
-  if (!grad_shape_ok(M, N, K, p)) return GEMMQ_E_SHAPE;
+  if (!grad_shape_ok(M, K, p)) return GEMMQ_E_SHAPE;
   rc = check_ws(ws, ws_bytes, p.bytes());
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  uint16_t* P = static_cast<uint16_t*>(ws);
-  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.factor_bytes);
-  clear_pending();
-  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
-    const int64_t n = N - n0 < p.piece ? N - n0 : p.piece;
-    const int64_t pitch = (int64_t)align_up(n, 64);
-    const uint8_t* dy = static_cast<const uint8_t*>(dY) + n0 * type_bytes(type);
-    rc = launched(launch_planes(type, dy, lddy, sw + n0, P, pitch, p.planes, (int)M, (int)n, st));
-    if (rc != GEMMQ_OK) return rc;
-    const GradArgs g{W + n0 * ldw, ldw, P, pitch, acc, p.kp, (int)M, (int)n, (int)K, p.planes,
-                     p.splits, n0 > 0};
-    rc = launched(launch_grad(g, st));
-    if (rc != GEMMQ_OK) return rc;
-  }
-  return launched(launch_finish(acc, p.kp, N > 0 ? p.splits : 0, nullptr, nullptr, 0, type, dX,
-                                lddx, (int)M, (int)K, st));
+  return run_grad(p, W, ldw, grad_out(type, dX, lddx), M, N, K, ws, st,
+                  [&](int64_t n0, int64_t n, uint16_t* P, int64_t pitch) {
+                    const uint8_t* dy = static_cast<const uint8_t*>(dY) + n0 * type_bytes(type);
+                    return launch_planes(type, dy, lddy, sw + n0, P, pitch, p.planes, (int)M,
+                                         (int)n, st);
+                  });
 }
 
 size_t gemmq_loss_i8_workspace(int64_t M, int64_t N, int64_t K) {
@@ -261,27 +289,21 @@ int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8
   if (!target || !lse || !dloss) return GEMMQ_E_INVALID_ARG;
   if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return GEMMQ_E_ALIGNMENT;
   const GradPlan p = grad_plan(type, M, N, K);
-  if (!grad_shape_ok(M, N, K, p)) return GEMMQ_E_SHAPE;
+  if (!grad_shape_ok(M, K, p)) return GEMMQ_E_SHAPE;
   rc = check_ws(ws, ws_bytes, p.bytes());
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  uint16_t* P = static_cast<uint16_t*>(ws);
-  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.factor_bytes);
-  clear_pending();
-  for (int64_t n0 = 0; n0 < N; n0 += p.piece) {
-    const int64_t n = N - n0 < p.piece ? N - n0 : p.piece;
-    const int64_t pitch = (int64_t)align_up(n, 64);
-    const Operands op{W + n0 * ldw, sw + n0, Xq, sx, ldw, ldq, (int)M, (int)n, (int)K};
-    rc = launched(launch_factor(op, FactorOut{target, lse, P, pitch, n0, p.planes}, st));
-    if (rc != GEMMQ_OK) return rc;
-    const GradArgs g{W + n0 * ldw, ldw, P, pitch, acc, p.kp, (int)M, (int)n, (int)K, p.planes,
-                     p.splits, n0 > 0};
-    rc = launched(launch_grad(g, st));
-    if (rc != GEMMQ_OK) return rc;
-  }
-  return launched(launch_finish(acc, p.kp, p.splits, dloss, target, N, type, dX, lddx, (int)M,
-                                (int)K, st));
+  GradOut out = grad_out(type, dX, lddx);
+  out.g = dloss;
+  out.target = target;
+  out.nvocab = N;
+  return run_grad(p, W, ldw, out, M, N, K, ws, st,
+                  [&](int64_t n0, int64_t n, uint16_t* P, int64_t pitch) {
+                    const Operands op{W + n0 * ldw, sw + n0, Xq,     sx,    ldw,
+                                      ldq,          (int)M,  (int)n, (int)K};
+                    return launch_factor(op, FactorOut{target, lse, P, pitch, n0, p.planes}, st);
+                  });
 }
 
 }  // extern "C"

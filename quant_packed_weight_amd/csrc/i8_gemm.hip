@@ -241,6 +241,20 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   // of tile i, channels 32 (wn TN + i) + 8 g + 4 (l >> 5) + 0..3.
   const int h = lane >> 5, nw = wn * TN * 32 + 4 * h;
   const bool edge = n0 + BN > op.N;  // some of the tile's channels do not exist
+  // 16-bit results go through LDS, so that rows are written in whole lines: four
+  // values of a token at a time from registers, at 32 tokens an instruction, made
+  // the factor of M = 1024 by 151936 rows 600 us, of which the K loop is 300.
+  // Their image: BN / 8 chunks of 16 bytes a row, chunk c of row m in slot c ^ (m
+  // mod BN / 8).
+  constexpr int kChunks = BN / 8;
+  static_assert(BM * BN * 2 <= DEPTH * S::kBytes, "the results fit the steps' buffers");
+  bool staged = false;
+  if constexpr (EPI == kLinear) staged = a.lin.type != GEMMQ_F32;
+  if constexpr (EPI == kFactor) staged = a.fac.planes == 1;
+  auto put = [&](int ml, int nl, uint32_t lo, uint32_t hi) {
+    *reinterpret_cast<uint2*>(lds + (ml * kChunks + ((nl >> 3) ^ (ml & (kChunks - 1)))) * 16 +
+                              8 * h) = make_uint2(lo, hi);
+  };
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int ml = (wm * TM + j) * 32 + (lane & 31);
@@ -263,8 +277,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
           const float v2 = fmaf((float)c[4 * g + 2] * sx, sw.z, b.z);
           const float v3 = fmaf((float)c[4 * g + 3] * sx, sw.w, b.w);
           const int64_t n = n0 + nl;
-          store4_as(a.lin.Y, m * a.lin.ldy + n, a.lin.type, wide,
-                    edge ? (int)min((int64_t)4, op.N - n) : 4, v0, v1, v2, v3);
+          if (staged) {
+            if (a.lin.type == GEMMQ_BF16)
+              put(ml, nl, bf16_bits(v0) | bf16_bits(v1) << 16, bf16_bits(v2) | bf16_bits(v3) << 16);
+            else
+              put(ml, nl, f16_bits(v0) | f16_bits(v1) << 16, f16_bits(v2) | f16_bits(v3) << 16);
+          } else {
+            store4_as(a.lin.Y, m * a.lin.ldy + n, a.lin.type, wide,
+                      edge ? (int)min((int64_t)4, op.N - n) : 4, v0, v1, v2, v3);
+          }
         }
     } else {
       // base-2 logits, exp(z) = 2^(z log2 e): v = sw I, z2 = s2 v with s2 = sx log2 e.
@@ -346,7 +367,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const int nl = nw + 32 * i + 8 * g;
-            if (edge && n0 + nl >= a.fac.pitch) continue;  // the pitch is a multiple of 4
             const float4 sw = *reinterpret_cast<const float4*>(swl + nl);
             float f[4] = {v[i][4 * g] * sw.x, v[i][4 * g + 1] * sw.y, v[i][4 * g + 2] * sw.z,
                           v[i][4 * g + 3] * sw.w};
@@ -355,9 +375,52 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
               for (int e = 0; e < 4; ++e)
                 if (n0 + nl + e >= op.N) f[e] = 0.0f;
             }
-            store_planes(a.fac.P + m * a.fac.pitch + n0 + nl, (int64_t)op.M * a.fac.pitch,
-                         a.fac.planes, f);
+            if (staged)
+              put(ml, nl, bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
+                  bf16_bits(f[2]) | bf16_bits(f[3]) << 16);
+            else if (n0 + nl < a.fac.pitch)  // a multiple of 4
+              store_planes(a.fac.P + m * a.fac.pitch + n0 + nl, (int64_t)op.M * a.fac.pitch,
+                           a.fac.planes, f);
           }
+      }
+    }
+  }
+  if constexpr (EPI != kLoss) {
+    if (staged) {
+      uint16_t* out;
+      int64_t pitch, width;  // the width of a row that is written
+      if constexpr (EPI == kLinear) {
+        out = static_cast<uint16_t*>(a.lin.Y), pitch = a.lin.ldy, width = op.N;
+      } else {
+        out = a.fac.P, pitch = a.fac.pitch, width = a.fac.pitch;
+      }
+      __syncthreads();
+      bool lines = true;
+      if constexpr (EPI == kLinear) lines = a.lin.lines;
+      if (lines) {
+        for (int i = t; i < BM * kChunks; i += T) {
+          const int ml = i / kChunks, c = i % kChunks;
+          const int64_t n = n0 + 8 * c;
+          if (m0 + ml >= op.M || n >= width) continue;
+          const v4i v = *reinterpret_cast<const v4i*>(
+              lds + (ml * kChunks + (c ^ (ml & (kChunks - 1)))) * 16);
+          uint16_t* to = out + (m0 + ml) * pitch + n;
+          if (n + 8 <= width) {
+            *reinterpret_cast<v4i*>(to) = v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (n + e < width) to[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      } else {
+        // rows off 16 bytes: neighbouring lanes still write neighbouring values
+        for (int i = t; i < BM * BN; i += T) {
+          const int ml = i / BN, nl = i % BN;
+          if (m0 + ml >= op.M || n0 + nl >= width) continue;
+          out[(m0 + ml) * pitch + n0 + nl] = *reinterpret_cast<const uint16_t*>(
+              lds + (ml * kChunks + ((nl >> 3) ^ (ml & (kChunks - 1)))) * 16 + 2 * (nl & 7));
+        }
       }
     }
   }

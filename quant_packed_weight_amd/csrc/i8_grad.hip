@@ -22,12 +22,34 @@ __device__ __forceinline__ v16f mfma_bf16(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// eight int8 to bf16, exactly
-__device__ __forceinline__ v8bf widen(v2i w) {
-  v8bf r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = (__bf16)(float)(int8_t)(w[e >> 2] >> (8 * (e & 3)));
-  return r;
+// two int8 of w (bytes 2 i and 2 i + 1) to bf16, exactly.  The conversion takes the
+// byte out of its word itself (written as source, the odd bytes cost a shift each).
+template <int i>
+__device__ __forceinline__ uint32_t widen2(int w) {
+  float lo, hi;
+  if constexpr (i == 0) {
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
+        : "=v"(lo) : "v"(w));
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
+        : "=v"(hi) : "v"(w));
+  } else {
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
+        : "=v"(lo) : "v"(w));
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
+        : "=v"(hi) : "v"(w));
+  }
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf r = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, r);
+}
+// part e (0..3) of a fragment of eight
+__device__ __forceinline__ uint32_t widen_part(v2i w, int e) {
+  switch (e) {
+    case 0: return widen2<0>(w[0]);
+    case 1: return widen2<1>(w[0]);
+    case 2: return widen2<0>(w[1]);
+    default: return widen2<1>(w[1]);
+  }
 }
 
 template <int BK, int BM>
@@ -45,6 +67,21 @@ __device__ __forceinline__ int wslot(int n, int chunk) {
 }
 // A's image: as the int8 product's operands (i8_gemm.hip)
 __device__ __forceinline__ int aslot(int m, int chunk) { return chunk ^ ((m >> 1) & 7); }
+
+// four values of row m of the result, from column k on
+__device__ __forceinline__ void put_result(const GradOut& o, int64_t m, int k, int K, float4 v) {
+  if (o.g) {
+    const float f = o.g[m];
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+  }
+  if (o.target) {
+    const int64_t tg = o.target[m];
+    const float nan = __builtin_nanf("");
+    if (tg < 0) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (tg >= o.nvocab) v = make_float4(nan, nan, nan, nan);
+  }
+  store4_as(o.dX, m * o.lddx + k, o.type, o.wide, K - k, v.x, v.y, v.z, v.w);
+}
 
 template <int BK, int BM, int WK, int WM, int DEPTH>
 __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint32_t ktiles,
@@ -145,15 +182,25 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
           lds + stage * S::kBytes + S::kA + m * 2 * kRed + 16 * aslot(m, 2 * q + h));
     }
   };
+  // The products of a quarter, and between them the reads of the next one, the
+  // loads of a later step, and the conversion of the fragment that the next TM
+  // products take (the next quarter's first in the last of this): a conversion
+  // ahead of its products would leave the matrix cores idle.
+  v4i wf[2];
+  auto convert = [&](int set, v2i raw, int j) {
+#pragma unroll
+    for (int e = 4 * j / TM; e < 4 * (j + 1) / TM; ++e)
+      wf[set][e] = (int)widen_part(raw, e);
+  };
   auto quarter = [&](int q, int from, uint32_t take, uint32_t to) {
 #pragma unroll
     for (int i = 0; i < TK; ++i) {
-      const v8bf w = widen(wraw[q & 1][i]);
+      const int set = (q * TK + i) & 1;
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         const int p = i * TM + j;
-        acc[i][j] = mfma_bf16(w, af[q & 1][j], acc[i][j]);
-        if (j == TM - 1) __builtin_amdgcn_sched_barrier(0);
+        acc[i][j] = mfma_bf16(__builtin_bit_cast(v8bf, wf[set]), af[q & 1][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r = p * kPerProduct; r < (p + 1) * kPerProduct && r < kReads; ++r)
           read(from, (q + 1) & 3, r);
@@ -162,6 +209,9 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
           for (int l = p * kLoads / kProducts; l < (p + 1) * kLoads / kProducts; ++l)
             load(l, take, to);
         }
+        convert(set ^ 1, i + 1 < TK ? wraw[q & 1][i + 1 < TK ? i + 1 : 0] : wraw[(q + 1) & 1][0],
+                j);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -177,6 +227,8 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     gk::lds_barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, 0, r);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) convert(0, wraw[0][0], j);
   }
   int buf = 0;
   for (int it = 0; it < its; ++it) {
@@ -194,16 +246,19 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   for (int j = 0; j < TM; ++j) {
     const int64_t m = m0 + (wm * TM + j) * 32 + (lane & 31);
     if (m >= a.M) continue;
-    float* out = a.acc + ((int64_t)split * a.M + m) * a.kp;
 #pragma unroll
     for (int i = 0; i < TK; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int k = k0 + (wk * TK + i) * 32 + 8 * g + 4 * h;
-        if (k >= a.kp) continue;
         float4 v = make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                                acc[i][j][4 * g + 3]);
-        float4* p = reinterpret_cast<float4*>(out + k);
+        if (!a.acc) {
+          if (k < a.K) put_result(a.out, m, k, a.K, v);
+          continue;
+        }
+        if (k >= a.kp) continue;
+        float4* p = reinterpret_cast<float4*>(a.acc + ((int64_t)split * a.M + m) * a.kp + k);
         if (a.add) {
           const float4 o = *p;
           v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
@@ -214,96 +269,187 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
 }
 
 // A[m, n] = dY[m, n] * sw[n] as `planes` bf16 matrices, zero from column N to
-// the pitch.  One thread per four columns.
-__global__ __launch_bounds__(256) void planes_kernel(int type, const void* dY, int64_t lddy,
+// the pitch.  A workgroup takes 2048 columns of ROWS rows, a thread eight of each:
+// four rows where there are many (2048 x 12288 bf16: 21 us, one row 54), one
+// where few would leave the chip idle (77 x 1037 f32: 5 us, four rows 9).
+template <int TYPE, int ROWS>
+__global__ __launch_bounds__(256) void planes_kernel(const void* dY, int64_t lddy, bool wide,
                                                      const float* sw, uint16_t* P, int64_t pitch,
                                                      int planes, int M, int N) {
-  const int64_t q = pitch / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = i / q;
-  if (m >= M) return;
-  const int64_t n = 4 * (i % q);
-  float v[4];
+  const int64_t m0 = (blockIdx.y + (int64_t)gridDim.y * blockIdx.z) * ROWS;
+  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (n >= pitch) return;  // the pitch is a multiple of 64
+  float f[8], v[ROWS][8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    v[e] = n + e < N ? load_as_f32(dY, m * lddy + n + e, type) * sw[n + e] : 0.0f;
-  for (int p = 0; p < planes; ++p) {
-    uint32_t b[4];
+  for (int e = 0; e < 8; ++e) f[e] = n + e < N ? sw[n + e] : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = bf16_part(v[e], p + 1 == planes);
-    *reinterpret_cast<uint2*>(P + ((int64_t)p * M + m) * pitch + n) =
-        make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t at = min(m0 + r, (int64_t)M - 1) * lddy + n;
+    if constexpr (TYPE == GEMMQ_F32) {
+      float a[4], b[4];
+      load_values<TYPE, 4>(dY, at, N - n, wide, a);
+      load_values<TYPE, 4>(dY, at + 4, N - n - 4, wide, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[r][e] = a[e], v[r][e + 4] = b[e];
+    } else {
+      load_values<TYPE, 8>(dY, at, N - n, wide, v[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (m0 + r >= M) return;
+    uint16_t* to = P + (m0 + r) * pitch + n;
+    // columns from N on are zero, not the product of what is read there with zero
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[r][e] = n + e < N ? v[r][e] * f[e] : 0.0f;
+    if (TYPE == GEMMQ_BF16) {
+      *reinterpret_cast<uint4*>(to) =
+          make_uint4(bf16_bits(v[r][0]) | bf16_bits(v[r][1]) << 16,
+                     bf16_bits(v[r][2]) | bf16_bits(v[r][3]) << 16,
+                     bf16_bits(v[r][4]) | bf16_bits(v[r][5]) << 16,
+                     bf16_bits(v[r][6]) | bf16_bits(v[r][7]) << 16);
+      continue;
+    }
+    for (int p = 0; p < planes; ++p) {
+      uint32_t b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        b[e] = bf16_part(v[r][2 * e], p + 1 == planes);
+        b[e] |= bf16_part(v[r][2 * e + 1], p + 1 == planes) << 16;
+      }
+      *reinterpret_cast<uint4*>(to + (int64_t)p * M * pitch) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
   }
 }
 
+// The ranges' sums added up, always in the same order: a thread takes four
+// columns of a row and one of GROUPS stretches of the ranges, eight of them at a
+// time, and the stretches are added through LDS.
+template <int GROUPS>
 __global__ __launch_bounds__(256) void finish_kernel(const float* acc, int64_t kp, int splits,
-                                                     const float* g, const int64_t* target,
-                                                     int64_t nvocab, int type, void* dX,
-                                                     int64_t lddx, int M, int K) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = i / K;
-  if (m >= M) return;
-  const int64_t k = i % K;
-  float v = 0.0f;
-  for (int s = 0; s < splits; ++s) v += acc[((int64_t)s * M + m) * kp + k];
-  if (g) v *= g[m];
-  if (target) {
-    const int64_t tg = target[m];
-    v = tg < 0 ? 0.0f : tg >= nvocab ? __builtin_nanf("") : v;
+                                                     GradOut out, int M, int K) {
+  constexpr int kQuads = 256 / GROUPS;
+  __shared__ float4 part[GROUPS > 1 ? 256 : 1];
+  const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+  if (m >= M) return;  // all of the workgroup
+  const int quad = threadIdx.x % kQuads, group = threadIdx.x / kQuads;
+  const int k = (blockIdx.x * kQuads + quad) * 4;
+  const int per = (splits + GROUPS - 1) / GROUPS;
+  const int first = group * per, end = min(first + per, splits);
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (k < K) {
+    for (int s = first; s < end; s += 8) {
+      float4 w[8];
+      // a row of acc is whole to its pitch, a multiple of 4
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e] = *reinterpret_cast<const float4*>(acc + ((int64_t)min(s + e, end - 1) * M + m) * kp +
+                                                k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (s + e < end) v = make_float4(v.x + w[e].x, v.y + w[e].y, v.z + w[e].z, v.w + w[e].w);
+    }
   }
-  store_as(dX, m * lddx + k, type, v);
+  if constexpr (GROUPS > 1) {
+    part[threadIdx.x] = v;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) {
+      const float4 w = part[g * kQuads + quad];
+      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+  }
+  if (k < K) put_result(out, m, k, K, v);
+}
+
+// rows over the grid's second and third dimensions
+dim3 rows_grid(int64_t x, int64_t M) {
+  const int64_t y = M < 32768 ? M : 32768;
+  return dim3((uint32_t)x, (uint32_t)y, (uint32_t)ceil_div(M, y));
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 
 struct Tile {
-  int bk, bm;
+  int bk, bm, grid;  // grid: workgroups that fill the chip
+  double us;         // of a step, measured
 };
-Tile pick_tile(int M) { return M <= 32 ? Tile{128, 32} : M <= 128 ? Tile{128, 128} : Tile{256, 256}; }
+constexpr Tile kTiles[] = {{256, 256, 256, 1.9}, {128, 256, 256, 1.15}, {128, 128, 512, 0.9},
+                           {128, 64, 512, 0.7},  {128, 32, 512, 0.6}};
 
-int64_t tiles(int M, int K) {
-  const Tile c = pick_tile(M);
-  return ceil_div(M, c.bm) * ceil_div(K, c.bk);
-}
+int64_t tiles(const Tile& c, int M, int K) { return ceil_div(M, c.bm) * ceil_div(K, c.bk); }
 
 }  // namespace
 
-int grad_splits(int M, int N, int K, int) {
-  const int64_t steps = ceil_div(N, kRed);
-  int64_t s = ceil_div(256, tiles(M, K));
-  if (s > steps / 4) s = steps / 4;
-  return s < 1 ? 1 : (int)s;
+// Up to 128 tokens the lowest tile that holds them; beyond, the one of the two
+// with the least estimated time, the partial sums' passage through memory (4.5
+// TB/s) and the launch that adds them counted: M = 2048, N = 12288, K = 4096 takes
+// 222 us in 128 x 256 tiles as one range, and 190 in 256 x 256 as two, which 14
+// then add up; M = 1024, N = 50688, K = 2048 216 in four ranges and 181 in eight.
+// A range has at least one step.
+GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
+  const int64_t steps = ceil_div(N < 1 ? 1 : N, kRed);
+  const int from = M <= 32 ? 4 : M <= 64 ? 3 : M <= 128 ? 2 : 0, to = M <= 128 ? from : 1;
+  GradSplit best{from, 1};
+  double least = -1.0;
+  for (int i = from; i <= to; ++i) {
+    const int64_t n = tiles(kTiles[i], M, K);
+    int64_t s = n < kTiles[i].grid ? kTiles[i].grid / n : 1;
+    if (s > steps) s = steps;
+    double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * planes * kTiles[i].us;
+    if (s > 1 || !whole) t += 4.0 + (double)s * M * K * 8e-6 / 4.5;
+    if (least < 0.0 || t < least) {
+      best = GradSplit{i, (int)s};
+      least = t;
+    }
+  }
+  return best;
 }
 
-bool grad_fits(int M, int K, int splits) {
-  return tiles(M, K) * splits <= kMaxGrid && ceil_div((int64_t)M * K, 256) <= kMaxGrid;
+bool grad_fits(const GradSplit& s, int M, int K) {
+  return tiles(kTiles[s.tile], M, K) * s.splits <= kMaxGrid;
 }
 
 int launch_grad(const GradArgs& a, hipStream_t st) {
-  const Tile c = pick_tile(a.M);
-  const int64_t mt = ceil_div(a.M, c.bm), kt = ceil_div(a.K, c.bk), n = mt * kt * a.splits;
+  const Tile& c = kTiles[a.tile];
+  const uint32_t mt = (uint32_t)ceil_div(a.M, c.bm), kt = (uint32_t)ceil_div(a.K, c.bk);
+  const int64_t n = (int64_t)mt * kt * a.splits;
   if (n > kMaxGrid) return -1;
-  if (c.bm == 32)
-    grad_kernel<128, 32, 4, 1, 3><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
-  else if (c.bm == 128)
-    grad_kernel<128, 128, 2, 2, 3><<<(uint32_t)n, 256, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
-  else
-    grad_kernel<256, 256, 4, 2, 3><<<(uint32_t)n, 512, 0, st>>>(a, (uint32_t)kt, (uint32_t)mt);
+  const dim3 grid((uint32_t)n);
+  switch (a.tile) {
+    case 0: grad_kernel<256, 256, 4, 2, 3><<<grid, 512, 0, st>>>(a, kt, mt); break;
+    case 1: grad_kernel<128, 256, 2, 4, 3><<<grid, 512, 0, st>>>(a, kt, mt); break;
+    case 2: grad_kernel<128, 128, 2, 2, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
+    case 3: grad_kernel<128, 64, 2, 2, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
+    default: grad_kernel<128, 32, 4, 1, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
+  }
   return 0;
 }
 
 int launch_planes(int type, const void* dY, int64_t lddy, const float* sw, uint16_t* P,
                   int64_t pitch, int planes, int M, int N, hipStream_t st) {
-  const int64_t n = ceil_div(M * (pitch / 4), 256);
-  if (n > kMaxGrid) return -1;
-  planes_kernel<<<(uint32_t)n, 256, 0, st>>>(type, dY, lddy, sw, P, pitch, planes, M, N);
+  const bool many = M * pitch >= (int64_t)1 << 22, wide = wide_rows(dY, lddy, type);
+  const dim3 grid = rows_grid(ceil_div(pitch, 2048), many ? ceil_div(M, 4) : M);
+  const auto run = [&](auto kernel) {
+    kernel<<<grid, 256, 0, st>>>(dY, lddy, wide, sw, P, pitch, planes, M, N);
+  };
+  if (type == GEMMQ_F32)
+    many ? run(planes_kernel<GEMMQ_F32, 4>) : run(planes_kernel<GEMMQ_F32, 1>);
+  else if (type == GEMMQ_BF16)
+    many ? run(planes_kernel<GEMMQ_BF16, 4>) : run(planes_kernel<GEMMQ_BF16, 1>);
+  else
+    many ? run(planes_kernel<GEMMQ_F16, 4>) : run(planes_kernel<GEMMQ_F16, 1>);
   return 0;
 }
 
-int launch_finish(const float* acc, int64_t kp, int splits, const float* g, const int64_t* target,
-                  int64_t nvocab, int type, void* dX, int64_t lddx, int M, int K,
+int launch_finish(const float* acc, int64_t kp, int splits, const GradOut& out, int M, int K,
                   hipStream_t st) {
-  finish_kernel<<<(uint32_t)ceil_div((int64_t)M * K, 256), 256, 0, st>>>(
-      acc, kp, splits, g, target, nvocab, type, dX, lddx, M, K);
+  // many ranges (few rows: the chip is otherwise idle) are read by four threads a column
+  if (splits >= 16)
+    finish_kernel<4><<<rows_grid(ceil_div(K, 256), M), 256, 0, st>>>(acc, kp, splits, out, M, K);
+  else
+    finish_kernel<1><<<rows_grid(ceil_div(K, 1024), M), 256, 0, st>>>(acc, kp, splits, out, M, K);
   return 0;
 }
 
