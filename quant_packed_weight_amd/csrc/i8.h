@@ -77,7 +77,7 @@ int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* l
 int launch_factor(const Operands& op, const FactorOut& out, hipStream_t st);
 
 // i8_skinny.hip, M <= kSkinnyMaxM
-constexpr int kSkinnyMaxM = 64, kSkinnyChannels = 16;  // channels per workgroup
+constexpr int kSkinnyMaxM = 16, kSkinnyChannels = 16;  // channels per workgroup
 int launch_skinny(const Operands& op, const LinearOut& out, hipStream_t st);
 int launch_skinny(const Operands& op, const LossOut& out, hipStream_t st);
 int launch_skinny(const Operands& op, const FactorOut& out, hipStream_t st);

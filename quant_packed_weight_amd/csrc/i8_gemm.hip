@@ -97,12 +97,8 @@ __device__ __forceinline__ void clear_tail(uint8_t* x, int k0, int K, int t) {
   for (int i = t; i < BM * 8; i += THREADS) {
     const int row = i >> 3, c = i & 7, keep = K - (k0 + 16 * c);
     if (keep >= 16) continue;
-    uint32_t* p = reinterpret_cast<uint32_t*>(x + row * kStep + 16 * slot(row, c));
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int b = keep - 4 * w;
-      p[w] = b <= 0 ? 0u : b >= 4 ? p[w] : p[w] & ((1u << (8 * b)) - 1u);
-    }
+    v4i* p = reinterpret_cast<v4i*>(x + row * kStep + 16 * slot(row, c));
+    *p = keep <= 0 ? (v4i){0, 0, 0, 0} : keep_bytes(*p, keep);
   }
 }
 
@@ -112,18 +108,23 @@ __device__ __forceinline__ float join_term(float2 p, float top) {
   return p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - top);
 }
 
-template <int BN, int BM, int WN, int WM, int DEPTH, int EPI>
-__global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
-  constexpr int NW = WN * WM, T = 64 * NW;
+// GROUPS groups of WN x WM waves compute the tile, group g the steps g, g + GROUPS,
+// ... of K in buffers of its own; their sums are added at the end.  More than one
+// where the tiles leave the chip idle: a step is then mostly a round trip to LDS
+// and back, and the groups' overlap.
+template <int BN, int BM, int WN, int WM, int DEPTH, int GROUPS, int EPI>
+__global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs a) {
+  constexpr int NW = WN * WM, T = 64 * NW * GROUPS;
   constexpr int TN = BN / WN / 32, TM = BM / WM / 32;
   using S = Stage<BN, BM>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[GROUPS * DEPTH * S::kBytes];
   __shared__ __attribute__((aligned(16))) float swl[BN];
   __shared__ __attribute__((aligned(16))) float bias[EPI == kLinear ? BN : 4];
   __shared__ float2 red[EPI == kLoss ? WN * BM : 1];
 
   const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((t >> 6) % NW);
+  const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane((t >> 6) / NW);
   const int wn = wave % WN, wm = wave / WN;
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
   uint32_t tm, tn;
@@ -135,7 +136,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   RowLoader<BM, NW> lx;
   lw.init(op.W, op.ldw, n0, op.N, op.K, wave, lane);
   lx.init(op.X, op.ldx, m0, op.M, op.K, wave, lane);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  uint8_t* mine = lds + group * DEPTH * S::kBytes;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)mine;
 
   for (int i = t; i < BN; i += T) {
     const bool in = n0 + i < op.N;
@@ -151,7 +153,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  const int steps = (op.K + kStep - 1) / kStep;
   constexpr int kLw = RowLoader<BN, NW>::kIssues, kLoads = kLw + RowLoader<BM, NW>::kIssues;
   // load j of this wave's kLoads for a step
   auto load = [&](int j, uint32_t take, int k0, uint32_t back, uint32_t to) {
@@ -198,21 +199,31 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
     }
   };
 
+  // local step s of the group is step s GROUPS + group of K; every group goes
+  // through `steps` of them, some through one past the end, which adds zero
+  const int all = (op.K + kStep - 1) / kStep;
+  const int steps = (all + GROUPS - 1) / GROUPS, own = (all - group + GROUPS - 1) / GROUPS;
+  auto column = [&](int s) { return (s * GROUPS + group) * kStep; };
+  // the last local step's columns from K on are cleared, by its own group
+  auto clear_last = [&](uint8_t* stage) {
+    if (op.K % kStep || all % GROUPS) {
+      clear_tail<BM, 64 * NW>(stage + S::kX, column(steps - 1), op.K, t % (64 * NW));
+      gk::lds_barrier();
+    }
+  };
+
 #pragma unroll
   for (int s = 0; s < DEPTH; ++s) {
-    const uint32_t back = lw.over(s * kStep);
+    const uint32_t back = lw.over(column(s));
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      load(j, s < steps, s * kStep, back, lds0 + s * S::kBytes);
+      load(j, s < own, column(s), back, lds0 + s * S::kBytes);
   }
-  wait_vm_if<(DEPTH - 1) * kLoads>(steps >= DEPTH);
+  wait_vm_if<(DEPTH - 1) * kLoads>(own >= DEPTH);
   gk::lds_barrier();
-  if (steps == 1 && op.K % kStep) {
-    clear_tail<BM, T>(lds + S::kX, 0, op.K, t);
-    gk::lds_barrier();
-  }
+  if (steps == 1) clear_last(mine);
 #pragma unroll
-  for (int r = 0; r < kReads; ++r) read(lds, 0, r);
+  for (int r = 0; r < kReads; ++r) read(mine, 0, r);
 
   // Past the barrier in step s the next step is in LDS (the loads of DEPTH - 2
   // later ones may be under way) and every wave has read all of this one, so that
@@ -221,21 +232,52 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   int buf = 0;
   for (int s = 0; s < steps; ++s) {
     const int nbuf = buf == DEPTH - 1 ? 0 : buf + 1;
-    const uint8_t* cur = lds + buf * S::kBytes;
-    uint8_t* next = lds + nbuf * S::kBytes;
+    const uint8_t* cur = mine + buf * S::kBytes;
+    uint8_t* next = mine + nbuf * S::kBytes;
 #pragma unroll
     for (int q = 0; q < 3; ++q) quarter(q, cur, 0, 0, 0, 0);
-    wait_vm_if<(DEPTH - 2) * kLoads>(s + DEPTH - 1 < steps);
+    wait_vm_if<(DEPTH - 2) * kLoads>(s + DEPTH - 1 < own);
     gk::lds_barrier();
-    if (s + 2 == steps && op.K % kStep) {
-      clear_tail<BM, T>(next + S::kX, (s + 1) * kStep, op.K, t);
-      gk::lds_barrier();
-    }
-    const int k0 = (s + DEPTH) * kStep;
-    quarter(3, next, s + DEPTH < steps, k0, lw.over(k0), lds0 + buf * S::kBytes);
+    if (s + 2 == steps) clear_last(next);
+    const int k0 = column(s + DEPTH);
+    quarter(3, next, s + DEPTH < own, k0, lw.over(k0), lds0 + buf * S::kBytes);
     buf = nbuf;
   }
-  gk::lds_barrier();  // no wave still reads what the epilogue may write
+  gk::lds_barrier();  // no wave still reads what follows writes
+
+  if constexpr (GROUPS > 1) {
+    constexpr int kAt = BM * BN * 2;  // behind the results' image
+    static_assert(kAt + (GROUPS - 1) * BM * BN * 4 <= GROUPS * DEPTH * S::kBytes, "the sums fit");
+    v4i* sums = reinterpret_cast<v4i*>(lds + kAt);
+    auto at = [&](int g, int i, int j, int r) {
+      return ((((g - 1) * NW + wave) * TN + i) * TM + j) * 256 + r * 64 + lane;
+    };
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sums[at(group, i, j, r)] = (v4i){acc[i][j][4 * r], acc[i][j][4 * r + 1],
+                                             acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < GROUPS; ++g)
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const v4i o = sums[at(g, i, j, r)];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * r + e] += o[e];
+            }
+    }
+  }
 
   // Lane l holds token 32 (wm TM + j) + (l & 31) and, in registers 4 g .. 4 g + 3
   // of tile i, channels 32 (wn TN + i) + 8 g + 4 (l >> 5) + 0..3.
@@ -247,7 +289,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   // Their image: BN / 8 chunks of 16 bytes a row, chunk c of row m in slot c ^ (m
   // mod BN / 8).
   constexpr int kChunks = BN / 8;
-  static_assert(BM * BN * 2 <= DEPTH * S::kBytes, "the results fit the steps' buffers");
+  static_assert(BM * BN * 2 <= GROUPS * DEPTH * S::kBytes, "the results fit the steps' buffers");
   bool staged = false;
   if constexpr (EPI == kLinear) staged = a.lin.type != GEMMQ_F32;
   if constexpr (EPI == kFactor) staged = a.fac.planes == 1;
@@ -257,6 +299,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void tile_kernel(TileArgs a) {
   };
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
+    if (group > 0) break;
     const int ml = (wm * TM + j) * 32 + (lane & 31);
     const int64_t m = m0 + ml;
     const bool inside = m < op.M;
@@ -492,41 +535,47 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr int kCUs = 256;
 
-// The tiles, and how many of their workgroups a compute unit holds (by LDS).
+// The tiles, their groups of waves, and how many of their workgroups a compute
+// unit holds (by LDS).
 struct Tile {
-  int bn, bm, resident;
+  int bn, bm, groups, resident;
 };
-constexpr Tile kTiles[] = {{256, 256, 1}, {128, 256, 1}, {128, 128, 2}, {128, 64, 3}, {64, 64, 3},
-                           {128, 32, 2},  {64, 32, 3}};
-constexpr int kTileCount = 7;
+constexpr Tile kTiles[] = {{256, 256, 1, 1}, {128, 256, 1, 1}, {128, 128, 1, 2}, {128, 64, 1, 3},
+                           {64, 64, 1, 3},   {128, 64, 2, 1},  {64, 64, 2, 2},   {64, 32, 4, 1},
+                           {64, 32, 1, 3},   {128, 32, 1, 2}};
+constexpr int kTileCount = 9;  // of those that pick_tile compares
+constexpr int kWideTile = 9;
 
 int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div(N, c.bn); }
 
 // The tile with the least estimated time.  What the K loop waits for is its loads:
-// per compute unit 44, 52 and 62 bytes a nanosecond with one, two and three
-// workgroups on it; a step has a round trip of its own in it, which small tiles do
-// not get below; and an output costs 0.08 ns of epilogue.  Measured against it (us,
-// M N K; tiles in the order of kTiles): 2048 4096 12288 140 / 111 / 115 / 164 / -,
-// 512 12288 4096 53 / 37 / 37 / 37 / -, 333 4099 2048 34 / 22 / 14 / 10.8 / 11.0,
-// 128 4096 4096 45 / 30 / 19 / 15.9 / 14.2.  Up to 32 tokens one row of tiles is
-// all there is, and W's stream decides: 128 channels where the chip is full many
-// times over (M = 8, 151936 x 2048 57 us, 64 channels 59), 64 otherwise (M = 16,
-// 12288 x 4096 17 us, 128 channels 19).
+// per compute unit 44, 52 and 62 bytes a nanosecond with one, two and more groups
+// of waves on it; a step has a round trip of 0.42 us in it that small tiles do not
+// get below; a workgroup costs 2 us around its loop, and an output 0.08 ns.
+// Measured against it (us; tiles in the order of kTiles):
+//   M 2048 N 4096 K 12288  137 / 106 / 107 / 164 / 192 / - / - / - / -
+//   M 512 N 12288 K 4096   50 / 37 / 37 / 36 / 45 / - / - / - / -
+//   M 512 N 4096 K 4096    - / - / 24 / 22 / 20 / 16 / 17 / 31 / 30
+//   M 128 N 4096 K 4096    - / - / 21 / 17 / 14 / 14 / 11 / 9 / 15
+//   M 64 N 4096 K 4096     - / - / 20 / 16 / 14 / 14 / 11 / 8 / 14
+// Up to 32 tokens of a vocabulary W's stream decides, and 128 channels a workgroup
+// are ahead of 64 (M = 8, 151936 x 2048 57 us against 59).
 int pick_tile(int M, int N, int K) {
-  if (M <= 32) return N > 65536 ? 5 : 6;
-  const double steps = (double)ceil_div(K, kStep);
-  const double rate[4] = {0.0, 44.0, 52.0, 62.0};
+  if (M <= 32 && N > 65536) return kWideTile;
+  const int64_t steps = ceil_div(K, kStep);
   int best = 0;
   double least = 0.0;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < kTileCount; ++i) {
     const Tile& c = kTiles[i];
     const int64_t n = tiles(c, M, N);
     int64_t r = ceil_div(n, kCUs);
     if (r > c.resident) r = c.resident;
+    const int64_t on = r * c.groups;
     const double rounds = (double)ceil_div(n, kCUs * r);
-    double step = (double)r * (c.bn + c.bm) * kStep / rate[r];
-    if (step < 400.0) step = 400.0;
-    const double t = rounds * (steps * step + 0.08 * (double)r * c.bn * c.bm);
+    double step = (double)on * (c.bn + c.bm) * kStep / (on == 1 ? 44.0 : on == 2 ? 52.0 : 62.0);
+    if (step < 420.0) step = 420.0;
+    const double t = rounds * ((double)ceil_div(steps, c.groups) * step + 2000.0 +
+                               0.08 * (double)r * c.bn * c.bm);
     if (i == 0 || t < least) {
       best = i;
       least = t;
@@ -535,14 +584,13 @@ int pick_tile(int M, int N, int K) {
   return best;
 }
 
-// Few tokens: the stream into registers, whose waves share a workgroup's K, where
-// the tiles would be too few to fill the chip (us, stream / tiles: M = 8, 4096 x
-// 4096 5.9 / 14; M = 16, 12288 x 4096 16 / 17; M = 64, 4096 x 4096 12.7 / 14).
-// `linear` at M <= 4 also beyond (151936 x 2048 at M = 1 53 / 58, M = 4 57 / 59);
-// the loss would have more partial sums to join there.
+// Up to 16 tokens: the stream into registers, whose waves share a workgroup's K,
+// where the tiles would be too few to fill the chip (us, stream / tiles: M = 8,
+// 4096 x 4096 5.9 / 8; M = 16, 12288 x 4096 13 / 16).  `linear` at M <= 4 also
+// beyond (151936 x 2048 at M = 1 53 / 58, M = 4 57 / 59); the loss would have
+// more partial sums to join there.
 bool skinny(int M, int N, bool linear) {
-  if (M <= 4 && linear) return true;
-  return N <= (M <= 16 ? 16384 : M <= 32 ? 8192 : M <= kSkinnyMaxM ? 6144 : 0);
+  return M <= kSkinnyMaxM && (N <= 16384 || (M <= 4 && linear));
 }
 
 template <int EPI>
@@ -556,13 +604,16 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
   a.group = 1024 / c.bm;
   const dim3 grid((uint32_t)n);
   switch (pick) {
-    case 0: tile_kernel<256, 256, 2, 4, 2, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 1: tile_kernel<128, 256, 2, 4, 3, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 2: tile_kernel<128, 128, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 3: tile_kernel<128, 64, 2, 2, 2, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 4: tile_kernel<64, 64, 2, 2, 3, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 5: tile_kernel<128, 32, 4, 1, 3, EPI><<<grid, 256, 0, st>>>(a); break;
-    default: tile_kernel<64, 32, 2, 1, 4, EPI><<<grid, 128, 0, st>>>(a); break;
+    case 0: tile_kernel<256, 256, 2, 4, 2, 1, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 1: tile_kernel<128, 256, 2, 4, 3, 1, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 2: tile_kernel<128, 128, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 3: tile_kernel<128, 64, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 4: tile_kernel<64, 64, 2, 2, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 5: tile_kernel<128, 64, 2, 2, 3, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 6: tile_kernel<64, 64, 2, 2, 2, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 7: tile_kernel<64, 32, 2, 1, 3, 4, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 8: tile_kernel<64, 32, 2, 1, 4, 1, EPI><<<grid, 128, 0, st>>>(a); break;
+    default: tile_kernel<128, 32, 4, 1, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
   }
   return 0;
 }

@@ -1,4 +1,4 @@
-// i8_skinny.hip -- the int8 product for few tokens (M <= 64): a stream of W
+// i8_skinny.hip -- the int8 product for few tokens (M <= 16): a stream of W
 // straight into registers, with the same three epilogues as i8_gemm.hip and, for
 // the linear layer at decode sizes, the quantizer in the same launch.
 //
@@ -77,12 +77,12 @@ __device__ __forceinline__ void quantize_rows(const SkinnyArgs& a, int span, uin
   __syncthreads();
 }
 
-template <int MT, int KS, int DEPTH, int EPI, bool FUSED>
+template <int KS, int DEPTH, int EPI, bool FUSED>
 __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
   constexpr int T = 64 * KS;
-  __shared__ __attribute__((aligned(16))) v4i sums[KS * MT * 64];
+  __shared__ __attribute__((aligned(16))) v4i sums[KS * 64];
   __shared__ __attribute__((aligned(16))) uint8_t xl[FUSED ? kFusedBytes : 16];
-  __shared__ float xs[16 * MT];
+  __shared__ float xs[16];
   __shared__ uint32_t tops[FUSED ? kFusedRows : 1][16];
 
   const int t = threadIdx.x, lane = t & 63;
@@ -95,26 +95,19 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
 
   // rows past the last channel or token repeat it, bytes past column K the last 16
   const int8_t* wp = op.W + min(n0 + row, (int64_t)op.N - 1) * op.ldw;
-  const int8_t* xp[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) xp[j] = op.X + min(16 * j + row, op.M - 1) * op.ldx;
+  const int8_t* xp = op.X + min(row, op.M - 1) * op.ldx;
 
-  v4i wf[DEPTH][2], xf[FUSED ? 1 : DEPTH][2][MT];
+  v4i wf[DEPTH][2], xf[FUSED ? 1 : DEPTH][2];
   auto load = [&](int u, int i) {
     const int k0 = min(wave + KS * i, pieces - 1) * kPiece;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int k = min(k0 + 64 * half + part, last);
       wf[u][half] = *reinterpret_cast<const v4i*>(wp + k);
-      if constexpr (!FUSED) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) xf[u][half][j] = *reinterpret_cast<const v4i*>(xp[j] + k);
-      }
+      if constexpr (!FUSED) xf[u][half] = *reinterpret_cast<const v4i*>(xp + k);
     }
   };
-  v4i acc[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) acc[j] = (v4i){0, 0, 0, 0};
+  v4i acc = {0, 0, 0, 0};
   const int span = pieces * kPiece;
   auto multiply = [&](int u, int i) {
     const int piece = wave + KS * i;
@@ -122,24 +115,16 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
       if (piece >= pieces) return;
 #pragma unroll
       for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-          xf[0][half][j] = *reinterpret_cast<const v4i*>(
-              xl + min(16 * j + row, op.M - 1) * span + piece * kPiece + 64 * half + part);
+        xf[0][half] = *reinterpret_cast<const v4i*>(xl + min(row, op.M - 1) * span +
+                                                    piece * kPiece + 64 * half + part);
     } else if (piece * kPiece + kPiece > op.K) {
       // the activations are zero from column K on, and in a piece past the last one
 #pragma unroll
       for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-          xf[u][half][j] =
-              keep_bytes(xf[u][half][j], op.K - (piece * kPiece + 64 * half + part));
+        xf[u][half] = keep_bytes(xf[u][half], op.K - (piece * kPiece + 64 * half + part));
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        acc[j] = mfma16(wf[u][half], xf[FUSED ? 0 : u][half][j], acc[j]);
+    for (int half = 0; half < 2; ++half) acc = mfma16(wf[u][half], xf[FUSED ? 0 : u][half], acc);
   };
 
   const int rounds = (pieces + KS - 1) / KS;
@@ -167,7 +152,7 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
       if (t < op.M) const_cast<float*>(op.sx)[t] = xs[t];
     }
   } else {
-    for (int m = t; m < 16 * MT; m += T) xs[m] = m < op.M ? op.sx[m] : 0.0f;
+    if (t < 16) xs[t] = t < op.M ? op.sx[t] : 0.0f;
   }
   // a group of DEPTH rounds at a time: the loads of the next group are issued as
   // this one's registers come free; rounds past the last piece add zero
@@ -184,16 +169,15 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
     }
   }
 
-#pragma unroll
-  for (int j = 0; j < MT; ++j) sums[(wave * MT + j) * 64 + lane] = acc[j];
+  sums[wave * 64 + lane] = acc;
   __syncthreads();
 
-  // one wave per 16 tokens: lane l holds token l & 15 and channels 4 (l >> 4) + 0..3
-  if (wave >= MT) return;
-  v4i s = sums[wave * 64 + lane];
+  // lane l holds token l & 15 and channels 4 (l >> 4) + 0..3
+  if (wave > 0) return;
+  v4i s = sums[lane];
 #pragma unroll
-  for (int w = 1; w < KS; ++w) s += sums[(w * MT + wave) * 64 + lane];
-  const int m = 16 * wave + row;
+  for (int w = 1; w < KS; ++w) s += sums[w * 64 + lane];
+  const int m = row;
   const int64_t n = n0 + 4 * (lane >> 4);
   const bool inside = m < op.M;
   const int count = (int)min((int64_t)4, op.N - n);  // channels of these four that exist
@@ -255,14 +239,10 @@ int launch(SkinnyArgs& a, hipStream_t st) {
   // 5.2 us, four waves 5.7), four with twice the loads each where there are many
   // (151936 x 2048 at M = 4: 57 us, eight waves 61).
   const bool many = n > 2048;
-  if (a.op.M > 32)
-    skinny_kernel<4, 8, 1, EPI, false><<<grid, 512, 0, st>>>(a);
-  else if (a.op.M > 16)
-    skinny_kernel<2, 8, 2, EPI, false><<<grid, 512, 0, st>>>(a);
-  else if (many)
-    skinny_kernel<1, 4, 4, EPI, false><<<grid, 256, 0, st>>>(a);
+  if (many)
+    skinny_kernel<4, 4, EPI, false><<<grid, 256, 0, st>>>(a);
   else
-    skinny_kernel<1, 8, 2, EPI, false><<<grid, 512, 0, st>>>(a);
+    skinny_kernel<8, 2, EPI, false><<<grid, 512, 0, st>>>(a);
   return 0;
 }
 
@@ -310,11 +290,11 @@ int launch_fused(int xtype, const void* X, int64_t ldx, const Operands& op, cons
   // workgroups, the less that matters: M = 1, 16, 8 and 4 waves, N = K = 4096 6.6 /
   // 6.9 / 7.6 us, 12288 x 4096 16.2 / 13.4 / 14.6, 151936 x 2048 132 / 89 / 54.
   if (n <= 512)
-    skinny_kernel<1, 16, 2, kLinear, true><<<grid, 1024, 0, st>>>(a);
+    skinny_kernel<16, 2, kLinear, true><<<grid, 1024, 0, st>>>(a);
   else if (n <= 2048)
-    skinny_kernel<1, 8, 4, kLinear, true><<<grid, 512, 0, st>>>(a);
+    skinny_kernel<8, 4, kLinear, true><<<grid, 512, 0, st>>>(a);
   else
-    skinny_kernel<1, 4, 4, kLinear, true><<<grid, 256, 0, st>>>(a);
+    skinny_kernel<4, 4, kLinear, true><<<grid, 256, 0, st>>>(a);
   return 0;
 }
 
