@@ -8,8 +8,7 @@
 // but no sum across lanes is needed.  A workgroup takes 16 channels, its waves
 // alternate 128-byte pieces of K and add their sums through LDS.  Bound by the
 // read of W; the activations' reads from L2, as many bytes as W's for each 16
-// tokens, are why more tokens go to tiles in LDS where those fill the chip
-// (i8_gemm.hip).  Against 32 or 64 channels a workgroup (fewer such reads, fewer
+// tokens, are why more tokens go to tiles in LDS (i8_gemm.hip).  Against 32 or 64 channels a workgroup (fewer such reads, fewer
 // workgroups): N = K = 4096 at M = 8 5.9 / 8.1 / 12.4 us, 151936 x 2048 at M = 1
 // 53 / 54 / 59.
 #include "i8_common.h"
@@ -235,12 +234,18 @@ int launch(SkinnyArgs& a, hipStream_t st) {
   const int64_t n = ceil_div(EPI == kFactor ? a.fac.pitch : a.op.N, kSkinnyChannels);
   if (n > 0x7fffffff) return -1;
   const dim3 grid((uint32_t)n);
-  // Eight waves share the channels' K where there are few workgroups (N = K = 4096:
-  // 5.2 us, four waves 5.7), four with twice the loads each where there are many
-  // (151936 x 2048 at M = 4: 57 us, eight waves 61).
-  const bool many = n > 2048;
-  if (many)
-    skinny_kernel<4, 4, EPI, false><<<grid, 256, 0, st>>>(a);
+  // The more workgroups, the fewer waves need to share a channel's K (us, eight
+  // waves / four: M = 8, 4096 x 4096 5.9 / 6.2, 12288 x 4096 14.4 / 13.5; M = 16,
+  // 16384 x 2048 12.9 / 11.5), and beyond 2048, which only the linear layer has,
+  // the more loads each may hold (151936 x 2048 at M = 4: 57, eight waves 61).
+  if constexpr (EPI == kLinear) {
+    if (n > 2048) {
+      skinny_kernel<4, 4, EPI, false><<<grid, 256, 0, st>>>(a);
+      return 0;
+    }
+  }
+  if (n > 512)
+    skinny_kernel<4, 2, EPI, false><<<grid, 256, 0, st>>>(a);
   else
     skinny_kernel<8, 2, EPI, false><<<grid, 512, 0, st>>>(a);
   return 0;

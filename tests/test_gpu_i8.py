@@ -132,9 +132,17 @@ SHAPES = [(1, 1, 1), (1, 4096, 4096), (1, 37, 100), (2, 16, 16), (3, 129, 127), 
           (33, 130, 300), (48, 640, 1111), (64, 512, 2048), (65, 257, 128), (100, 31, 4100),
           (127, 128, 129), (128, 1024, 512), (129, 513, 640), (255, 255, 255), (256, 256, 256),
           (257, 4099, 1025), (333, 777, 96), (512, 1536, 2048), (1000, 264, 136)]
+# larger ones: every tile and every split of K that the library chooses from
+WIDE = [(1, 40000, 1030), (1, 300, 16384), (1, 130, 20000), (2, 16400, 300), (2, 5000, 8192),
+        (2, 100, 8200), (3, 20000, 256), (4, 70000, 129), (5, 16384, 700), (6, 16400, 400),
+        (16, 70000, 130), (20, 70001, 260), (20, 4100, 1100), (32, 9000, 1000), (30, 40000, 300),
+        (48, 4096, 4100), (64, 70000, 100), (90, 5000, 900), (128, 4096, 640), (300, 4100, 1300),
+        (513, 2052, 2200), (512, 12300, 300), (700, 2000, 600), (1030, 6200, 200),
+        (2048, 4100, 500), (2050, 8200, 130), (4100, 4200, 200), (530, 13500, 40), (780, 7760, 36),
+        (641, 4430, 40), (99, 12340, 36), (33, 8420, 40), (66, 11700, 140), (36, 8230, 140)]
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + WIDE)
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_gemm(M, N, K, dtype):
     g = gen(M * 31 + N * 17 + K)
@@ -196,7 +204,9 @@ def test_rows_do_not_depend_on_their_neighbours():
 # ------------------------------------------------------------------ linear
 @pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (1, 100, 77), (2, 64, 4096), (5, 321, 333),
                                    (16, 256, 12288), (33, 100, 512), (130, 260, 515),
-                                   (300, 512, 640)])
+                                   (300, 512, 640), (1, 9000, 100), (1, 40000, 515), (1, 64, 16384),
+                                   (1, 64, 16400), (2, 10000, 257), (2, 17000, 130), (2, 40, 8192),
+                                   (2, 40, 8300), (3, 100, 100)])
 @pytest.mark.parametrize("xt", TYPES, ids=IDS)
 @pytest.mark.parametrize("yt", TYPES, ids=IDS)
 def test_linear_is_quantize_then_gemm(M, N, K, xt, yt):
@@ -239,7 +249,9 @@ def split_error(dtype):
 GRADS = [(1, 1, 1), (1, 64, 64), (1, 1000, 300), (2, 63, 130), (5, 65, 33), (8, 4096, 1024),
          (16, 127, 128), (17, 129, 1), (31, 640, 515), (32, 512, 512), (33, 200, 129),
          (64, 1111, 640), (77, 1037, 515), (128, 128, 128), (129, 2000, 255), (200, 50, 1000),
-         (256, 1024, 512), (300, 333, 777), (513, 640, 264)]
+         (256, 1024, 512), (300, 333, 777), (513, 640, 264), (16, 20000, 200), (40, 9000, 600),
+         (100, 30000, 130), (700, 3001, 2050), (2050, 130, 4100), (1500, 70, 5000), (4, 64, 100000),
+         (1400, 3001, 70)]
 
 
 @pytest.mark.parametrize("M,N,K", GRADS)
@@ -336,7 +348,10 @@ def logit_error(z):
 
 LOSSES = [(1, 1, 1), (1, 1000, 64), (1, 32003, 515), (2, 127, 100), (5, 128, 128), (8, 4097, 1024),
           (16, 129, 33), (17, 1000, 200), (32, 3000, 256), (33, 255, 129), (64, 5000, 300),
-          (128, 256, 512), (130, 1111, 640), (257, 2050, 255), (500, 513, 64)]
+          (128, 256, 512), (130, 1111, 640), (257, 2050, 255), (500, 513, 64), (3, 16390, 200),
+          (12, 16384, 600), (20, 70001, 260), (48, 4096, 1000), (100, 20000, 130), (300, 9000, 300),
+          (600, 12300, 140), (2050, 8200, 130), (530, 13500, 40), (780, 7760, 36), (641, 4430, 40),
+          (66, 11700, 140), (36, 8230, 140)]
 
 
 @pytest.mark.parametrize("M,N,K", LOSSES)
@@ -492,6 +507,48 @@ def test_loss_grad_against_differences(M, N, K):
     mag = (dx.double().abs() * xq.double().abs()).sum(1)
     tol = (e * s64) ** 2 / 6 * 8 * top ** 3 + 2.0 ** -12 * mag + 1e-9 * top + 40 * U * (top * s64 + 1) * top
     assert bool(((slope - num).abs() <= tol).all())
+
+
+# ------------------------------------------------------------------ far offsets
+def test_offsets_past_32_bits():
+    # weights of 4.6 GB: byte offsets of the last rows pass 2^32
+    N, K, tail = 140000, 32768, 200
+    g = gen(6)
+    w = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    w[-tail:] = i8(tail, K, g)
+    sw = torch.ones(N, device="cuda")
+    for M in (1, 3, 20, 200):
+        xq, sx = i8(M, K, g), scales(M, g, 1e-6)
+        s, z = product(w[-tail:], sw[-tail:], xq, sx)
+        y = gq.gemm_i8(w, sw, xq, sx)
+        assert not bool(y[:, :-tail].any())
+        assert bool(((y[:, -tail:].double() - z).abs() <= 4 * U * z.abs()).all())
+        t = torch.full((M,), N - 1, device="cuda")
+        loss, lse = gq.loss_i8(w, sw, xq, sx, t)
+        ref = torch.logsumexp(torch.cat([z, torch.full_like(z[:, :1], math.log(N - tail))], 1), 1)
+        tol = 3 * logit_error(z) + 320 * U + 3 * U * ref.abs()
+        assert bool(((lse.double() - ref).abs() <= tol).all())
+        assert bool(((loss.double() - (ref - z[:, -1])).abs() <= 2 * tol).all())
+        # only the last rows have weights: their part of the gradient is all of it
+        dy = torch.randn((M, N), generator=g, device="cuda")
+        dx = gq.linear_i8_grad(w, sw, dy)
+        d = dy[:, -tail:].double()
+        ref = d @ w[-tail:].double()
+        mag = d.abs() @ w[-tail:].double().abs()
+        # the zero products add nothing, but their additions may be in any place
+        assert bool(((dx.double() - ref).abs() <= (3 * tail + 70) * U * mag).all())
+        del dy, dx, y
+
+
+def test_results_past_32_bits():
+    # 2.6 10^9 results: element offsets pass 2^31, and in bytes 2^32
+    M, N, K = 40000, 65536, 64
+    g = gen(12)
+    w, sw, xq, sx = i8(N, K, g), scales(N, g, 0.01), i8(M, K, g), scales(M, g, 0.01)
+    y = gq.gemm_i8(w, sw, xq, sx, out_dtype=torch.bfloat16)
+    rows = torch.tensor([0, 1, 127, 128, 20000, 32767, 32768, M - 129, M - 1], device="cuda")
+    _, ref = product(w, sw, xq[rows], sx[rows])
+    assert bool(((y[rows].double() - ref).abs() <= (2.0 ** -8 + 8 * U) * ref.abs()).all())
 
 
 # ------------------------------------------------------------------ together
