@@ -132,49 +132,78 @@ __device__ __forceinline__ uint32_t abs_bits(float x) {
 __device__ __forceinline__ float scale_of(uint32_t top) {
   return top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
 }
-// x / s to the nearest integer, ties to even, within [-127, 127]; 0 where s is 0
-// or NaN
-__device__ __forceinline__ int quantized(float x, float s) {
-  const float q = s > 0.0f ? rintf(x / s) : 0.0f;
-  return (int)fminf(fmaxf(q, -127.0f), 127.0f);
+// x / s to the nearest integer, ties to even, within [-127, 127], for a row with a
+// finite s > 0 and inv = 1 / s.  x * inv is within 2^-23 |x / s| < 2 10^-5 of the
+// quotient, and the rounded quotient within 10^-5: unless x * inv lies within 10^-4
+// of a tie (or inv is infinite), all three round to the same integer, and the
+// division, half of the quantizer's arithmetic, is left out.
+__device__ __forceinline__ float quantized(float x, float s, float inv) {
+  const float t = x * inv;
+  float q = rintf(t);
+  if (!(fabsf(t - q) < 0.4999f)) q = rintf(x / s);
+  return __builtin_amdgcn_fmed3f(q, -127.0f, 127.0f);
 }
 
-// V consecutive values of a row from element i as f32, zero from element `end`
-// of the row on (`left` values are left before it); at once where the row allows
-// 16-byte loads and all are there
+// 16 bytes of a row from element i, zero from element `end` of the row on (`left`
+// values are left before it); at once where the row allows 16-byte loads and all
+// are there
+template <int TYPE>
+__device__ __forceinline__ uint4 load_raw(const void* p, int64_t i, int64_t left, bool wide) {
+  constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8;
+  uint32_t u[4] = {0, 0, 0, 0};
+  if constexpr (TYPE == GEMMQ_F32) {
+    const uint32_t* x = static_cast<const uint32_t*>(p) + i;
+    if (wide && left >= V) return *reinterpret_cast<const uint4*>(x);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < left) u[e] = x[e];
+  } else {
+    const uint16_t* x = static_cast<const uint16_t*>(p) + i;
+    if (wide && left >= V) return *reinterpret_cast<const uint4*>(x);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < left) u[e >> 1] |= (uint32_t)x[e] << (16 * (e & 1));
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// the V values of 16 bytes as f32
+template <int TYPE, int V>
+__device__ __forceinline__ void unpack(uint4 w, float (&v)[V]) {
+  static_assert(V == (TYPE == GEMMQ_F32 ? 4 : 8), "16 bytes");
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if constexpr (TYPE == GEMMQ_F32) {
+      v[e] = __builtin_bit_cast(float, u[e]);
+    } else if constexpr (TYPE == GEMMQ_BF16) {
+      v[e] = __builtin_bit_cast(float, e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+    } else {
+      v[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[e >> 1] >> (16 * (e & 1))));
+    }
+  }
+}
+
 template <int TYPE, int V>
 __device__ __forceinline__ void load_values(const void* p, int64_t i, int64_t left, bool wide,
                                             float (&v)[V]) {
-  static_assert(V == (TYPE == GEMMQ_F32 ? 4 : 8), "16 bytes");
-  if (wide && left >= V) {
-    if constexpr (TYPE == GEMMQ_F32) {
-      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = (u[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-        v[e] = TYPE == GEMMQ_BF16 ? __builtin_bit_cast(float, b << 16)
-                                  : (float)__builtin_bit_cast(_Float16, (uint16_t)b);
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) v[e] = e < left ? load_as_f32(p, i + e, TYPE) : 0.0f;
+  unpack<TYPE, V>(load_raw<TYPE>(p, i, left, wide), v);
 }
 
-// V quantized values as bytes
+// V quantized values as bytes, zero in a row whose scale is 0 or NaN
 template <int V>
-__device__ __forceinline__ void quantize_values(const float (&v)[V], float s,
+__device__ __forceinline__ void quantize_values(const float (&v)[V], float s, float inv,
                                                 uint32_t (&q)[V / 4]) {
 #pragma unroll
   for (int w = 0; w < V / 4; ++w) {
-    q[w] = 0;
+    uint32_t b[4];
+    // 1.5 2^23 + q holds q's two's complement in its low bits
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[w] |= ((uint32_t)quantized(v[4 * w + e], s) & 0xffu) << (8 * e);
+    for (int e = 0; e < 4; ++e)
+      b[e] = __builtin_bit_cast(uint32_t, quantized(v[4 * w + e], s, inv) + 12582912.0f);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    q[w] = s > 0.0f ? lo | hi : 0u;
   }
 }
 

@@ -18,18 +18,20 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
   __shared__ uint32_t tops[4];
   const int64_t m = blockIdx.x, x0 = m * ldx;
   const int t = threadIdx.x;
-  float held[kHeld][V];
+  uint4 held[kHeld];
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int k = kSpan * i + V * t;
-    if (kSpan * i < K) load_values<TYPE, V>(X, x0 + k, K - k, wide, held[i]);
+    if (kSpan * i < K) held[i] = load_raw<TYPE>(X, x0 + k, K - k, wide);
   }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (kSpan * i < K) {
+      float v[V];
+      unpack<TYPE, V>(held[i], v);
 #pragma unroll
-      for (int e = 0; e < V; ++e) top = max(top, abs_bits(held[i][e]));
+      for (int e = 0; e < V; ++e) top = max(top, abs_bits(v[e]));
     }
   for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
     float v[V];
@@ -42,10 +44,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
   if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
   const float sc = scale_of(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+  const float inv = 1.0f / sc;
   if (t == 0) s[m] = sc;
   auto store = [&](int k, const float (&v)[V]) {
     uint32_t q[V / 4];
-    quantize_values<V>(v, sc, q);
+    quantize_values<V>(v, sc, inv, q);
     int8_t* to = Q + m * ldq + k;
     if (k + V <= K) {
 #pragma unroll
@@ -58,7 +61,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
   };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
-    if (kSpan * i < K) store(kSpan * i + V * t, held[i]);
+    if (kSpan * i < K) {
+      float v[V];
+      unpack<TYPE, V>(held[i], v);
+      store(kSpan * i + V * t, v);
+    }
   for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
     float v[V];
     load_values<TYPE, V>(X, x0 + k, K - k, wide, v);

@@ -62,12 +62,13 @@ __device__ __forceinline__ void quantize_rows(const SkinnyArgs& a, int span, uin
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) top = max(top, tops[m][w]);
     const float s = scale_of(top);
+    const float inv = 1.0f / s;
     if (t == 0) xs[m] = s;
     for (int k = V * t; k < span; k += V * T) {
       float v[V];
       load_values<TYPE, V>(a.X, m * a.ldx + k, op.K - k, a.xwide, v);
       uint32_t q[V / 4];
-      quantize_values<V>(v, s, q);
+      quantize_values<V>(v, s, inv, q);
 #pragma unroll
       for (int w = 0; w < V / 4; ++w)
         *reinterpret_cast<uint32_t*>(xl + m * span + k + 4 * w) = q[w];

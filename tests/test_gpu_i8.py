@@ -91,6 +91,29 @@ def test_quantize(M, K, dtype, extra):
     assert torch.equal(q2, q) and torch.equal(s2, s)
 
 
+def test_quantize_ties():
+    # values on and one step beside the ties between two integers, at scales of all
+    # sizes: the rounded quotient decides
+    g = gen(15)
+    half = torch.arange(-127, 127, device="cuda").float() + 0.5
+    rows = []
+    for e in range(-120, 118, 7):
+        s = float(2.0 ** e * (1 + torch.rand(1, generator=g, device="cuda")))
+        top = torch.tensor([127.0 * s], device="cuda")
+        v = (half.double() * (top / 127).double()).float()
+        rows.append(torch.cat([top, v, torch.nextafter(v, top), torch.nextafter(v, -top)]))
+    x = torch.stack(rows)
+    q, s = gq.quantize_i8(x)
+    sr = (x.double().abs().amax(1) / 127).float()
+    assert torch.equal(s, sr)
+    assert torch.equal(q.float(), (x.double() / sr.double()[:, None]).float().round().clamp(-127, 127))
+    # the one-launch layer quantizes by the same steps
+    w, sw = i8(48, x.shape[1], g), scales(48, g)
+    for m in range(0, x.shape[0], 5):
+        y = gq.linear_i8(w, sw, x[m:m + 1], out_dtype=torch.float32)
+        assert torch.equal(y, gq.gemm_i8(w, sw, q[m:m + 1], s[m:m + 1]))
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_quantize_extreme_rows(dtype):
     fi = torch.finfo(dtype)
