@@ -283,9 +283,9 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
   // of tile i, channels 32 (wn TN + i) + 8 g + 4 (l >> 5) + 0..3.
   const int h = lane >> 5, nw = wn * TN * 32 + 4 * h;
   const bool edge = n0 + BN > op.N;  // some of the tile's channels do not exist
-  // 16-bit results go through LDS, so that rows are written in whole lines: four
-  // values of a token at a time from registers, at 32 tokens an instruction, made
-  // the factor of M = 1024 by 151936 rows 600 us, of which the K loop is 300.
+  // 16-bit results go through LDS, so that rows are written in whole lines.  Written
+  // from the registers, four values of a token at a time and 32 tokens an
+  // instruction, the factor of M = 1024 by 50688 rows took 200 us instead of 160.
   // Their image: BN / 8 chunks of 16 bytes a row, chunk c of row m in slot c ^ (m
   // mod BN / 8).
   constexpr int kChunks = BN / 8;
