@@ -52,9 +52,10 @@ __device__ __forceinline__ uint32_t widen_part(v2i w, int e) {
   }
 }
 
-template <int BK, int BM>
+template <int BK, int BM, int PLANES>
 struct GradStage {
-  static constexpr int kW = 0, kA = kRed * BK, kBytes = kRed * BK + BM * 2 * kRed;
+  static constexpr int kW = 0, kA = kRed * BK, kPlane = BM * 2 * kRed;
+  static constexpr int kBytes = kA + PLANES * kPlane;
 };
 
 // W's LDS image: rows of BK bytes, chunk c of row n in slot c ^ 2 (n & 7): the
@@ -83,14 +84,17 @@ __device__ __forceinline__ void put_result(const GradOut& o, int64_t m, int k, i
   store4_as(o.dX, m * o.lddx + k, o.type, o.wide, K - k, v.x, v.y, v.z, v.w);
 }
 
-template <int BK, int BM, int WK, int WM, int DEPTH>
+// PLANES planes at a time (1, or all of them): W's tile is then read and converted
+// once for them.
+template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES>
 __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint32_t ktiles,
                                                                uint32_t mtiles) {
   constexpr int NW = WK * WM;
   constexpr int TK = BK / WK / 32, TM = BM / WM / 32;
-  using S = GradStage<BK, BM>;
+  using S = GradStage<BK, BM, PLANES>;
   constexpr int kRowsPer = 1024 / BK;  // rows of W per load
-  constexpr int kLw = kRed / kRowsPer / NW, kLa = BM / 8 / NW, kLoads = kLw + kLa;
+  constexpr int kLw = kRed / kRowsPer / NW, kLa = BM / 8 / NW;
+  constexpr int kLoads = kLw + PLANES * kLa;
   static_assert(kLw * kRowsPer * NW == kRed && kLa * 8 * NW == BM && NW % 2 == 0,
                 "every wave issues the same loads");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
@@ -103,11 +107,11 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   id /= mtiles;
   const int k0 = (int)(id % ktiles) * BK, split = (int)(id / ktiles);
 
-  // this split's share of the steps of kRed rows; every plane goes over it
+  // this split's share of the steps of kRed rows; the planes go over it PLANES at a time
   const int steps = (a.N + kRed - 1) / kRed;
   const int per = steps / a.splits, more = steps % a.splits;
   const int first = split * per + min(split, more), count = per + (split < more ? 1 : 0);
-  const int its = count * a.planes;
+  const int turns = a.planes / PLANES, its = count * turns;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const int mvalid = (int)min((int64_t)BM, a.M - m0);
@@ -127,8 +131,8 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     // rows past the last token repeat it: their results are dropped
     aoff[j] = (uint32_t)min(r, mvalid - 1) * arow + 16 * aslot(r, lane & 7);
   }
-  // iteration `it` reads step first + it / planes of plane it % planes; `ahead`
-  // is the one that is loaded next
+  // iteration `it` reads step first + it / turns, its planes from PLANES (it % turns)
+  // on; astep and aplane are those that are loaded next
   int astep = first, aplane = 0;
   auto load = [&](int j, uint32_t take, uint32_t to) {
     const int64_t n = (int64_t)min(astep, steps - 1) * kRed;
@@ -139,14 +143,16 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
       gk::dma16_if(take, rs, (uint32_t)(min(wrow[j], nvalid - 1) * (int)a.ldw) + wcol[j], 0,
                    to + S::kW + 1024 * (wave + NW * j));
     } else {
-      const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)aplane * a.M + m0) * a.pitch,
+      const int p = (j - kLw) / kLa, l = (j - kLw) % kLa;
+      const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)(aplane + p) * a.M + m0) * a.pitch,
                                       (uint32_t)mvalid * arow);
-      gk::dma16_if(take, rs, aoff[j - kLw], (uint32_t)(2 * n),
-                   to + S::kA + 1024 * (wave + NW * (j - kLw)));
+      gk::dma16_if(take, rs, aoff[l], (uint32_t)(2 * n),
+                   to + S::kA + p * S::kPlane + 1024 * (wave + NW * l));
     }
   };
   auto advance = [&] {
-    if (++aplane == a.planes) {
+    aplane += PLANES;
+    if (aplane == a.planes) {
       aplane = 0;
       ++astep;
     }
@@ -164,8 +170,9 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   // transposing read: of each 16 lanes, lanes 2 r and 2 r + 1 give the addresses
   // of the two halves of 16 k of row r, and lane i takes k i of the eight rows.
   v2i wraw[2][TK];
-  v8bf af[2][TM];
-  constexpr int kReads = TK + TM, kProducts = TK * TM;
+  v8bf af[2][PLANES * TM];
+  constexpr int kU = PLANES * TM;  // products of a fragment of W
+  constexpr int kReads = TK + kU, kProducts = TK * kU;
   constexpr int kPerProduct = (2 * kReads + kProducts - 1) / kProducts;
   const int h = lane >> 5;
   auto read = [&](int stage, int q, int r) {
@@ -177,19 +184,20 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
       wraw[q & 1][r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
           (__attribute__((address_space(3))) v2i*)p);
     } else {
-      const int m = (wm * TM + r - TK) * 32 + (lane & 31);
-      af[q & 1][r - TK] = *reinterpret_cast<const v8bf*>(
-          lds + stage * S::kBytes + S::kA + m * 2 * kRed + 16 * aslot(m, 2 * q + h));
+      const int p = (r - TK) / TM, m = (wm * TM + (r - TK) % TM) * 32 + (lane & 31);
+      af[q & 1][r - TK] = *reinterpret_cast<const v8bf*>(lds + stage * S::kBytes + S::kA +
+                                                         p * S::kPlane + m * 2 * kRed +
+                                                         16 * aslot(m, 2 * q + h));
     }
   };
   // The products of a quarter, and between them the reads of the next one, the
-  // loads of a later step, and the conversion of the fragment that the next TM
+  // loads of a later step, and the conversion of the fragment that the next
   // products take (the next quarter's first in the last of this): a conversion
   // ahead of its products would leave the matrix cores idle.
   v4i wf[2];
-  auto convert = [&](int set, v2i raw, int j) {
+  auto convert = [&](int set, v2i raw, int u) {
 #pragma unroll
-    for (int e = 4 * j / TM; e < 4 * (j + 1) / TM; ++e)
+    for (int e = 4 * u / kU; e < 4 * (u + 1) / kU; ++e)
       wf[set][e] = (int)widen_part(raw, e);
   };
   auto quarter = [&](int q, int from, uint32_t take, uint32_t to) {
@@ -197,9 +205,10 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     for (int i = 0; i < TK; ++i) {
       const int set = (q * TK + i) & 1;
 #pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const int p = i * TM + j;
-        acc[i][j] = mfma_bf16(__builtin_bit_cast(v8bf, wf[set]), af[q & 1][j], acc[i][j]);
+      for (int u = 0; u < kU; ++u) {
+        const int p = i * kU + u;
+        acc[i][u % TM] =
+            mfma_bf16(__builtin_bit_cast(v8bf, wf[set]), af[q & 1][u], acc[i][u % TM]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r = p * kPerProduct; r < (p + 1) * kPerProduct && r < kReads; ++r)
@@ -210,7 +219,7 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
             load(l, take, to);
         }
         convert(set ^ 1, i + 1 < TK ? wraw[q & 1][i + 1 < TK ? i + 1 : 0] : wraw[(q + 1) & 1][0],
-                j);
+                u);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, 0, r);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) convert(0, wraw[0][0], j);
+    for (int u = 0; u < kU; ++u) convert(0, wraw[0][0], u);
   }
   int buf = 0;
   for (int it = 0; it < its; ++it) {
@@ -397,7 +406,9 @@ GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
     const int64_t n = tiles(kTiles[i], M, K);
     int64_t s = n < kTiles[i].grid ? kTiles[i].grid / n : 1;
     if (s > steps) s = steps;
-    double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * planes * kTiles[i].us;
+    // the low tiles take all planes in a step
+    const double each = kTiles[i].us * (i >= 2 ? 0.65 + 0.35 * planes : (double)planes);
+    double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * each;
     if (s > 1 || !whole) t += 4.0 + (double)s * M * K * 8e-6 / 4.5;
     if (least < 0.0 || t < least) {
       best = GradSplit{i, (int)s};
@@ -417,12 +428,24 @@ int launch_grad(const GradArgs& a, hipStream_t st) {
   const int64_t n = (int64_t)mt * kt * a.splits;
   if (n > kMaxGrid) return -1;
   const dim3 grid((uint32_t)n);
+  const auto run = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, st>>>(a, kt, mt); };
   switch (a.tile) {
-    case 0: grad_kernel<256, 256, 4, 2, 3><<<grid, 512, 0, st>>>(a, kt, mt); break;
-    case 1: grad_kernel<128, 256, 2, 4, 3><<<grid, 512, 0, st>>>(a, kt, mt); break;
-    case 2: grad_kernel<128, 128, 2, 2, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
-    case 3: grad_kernel<128, 64, 2, 2, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
-    default: grad_kernel<128, 32, 4, 1, 3><<<grid, 256, 0, st>>>(a, kt, mt); break;
+    case 0: run(grad_kernel<256, 256, 4, 2, 3, 1>, 512); break;
+    case 1: run(grad_kernel<128, 256, 2, 4, 3, 1>, 512); break;
+    case 2:
+      a.planes == 1   ? run(grad_kernel<128, 128, 2, 2, 3, 1>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 3, 2>, 256)
+                      : run(grad_kernel<128, 128, 2, 2, 2, 3>, 256);
+      break;
+    case 3:
+      a.planes == 1   ? run(grad_kernel<128, 64, 2, 2, 3, 1>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 64, 2, 2, 3, 2>, 256)
+                      : run(grad_kernel<128, 64, 2, 2, 2, 3>, 256);
+      break;
+    default:
+      a.planes == 1   ? run(grad_kernel<128, 32, 4, 1, 3, 1>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 32, 4, 1, 3, 2>, 256)
+                      : run(grad_kernel<128, 32, 4, 1, 3, 3>, 256);
   }
   return 0;
 }
