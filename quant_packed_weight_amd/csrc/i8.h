@@ -103,13 +103,14 @@ struct GradOut {
 struct GradArgs {
   const int8_t* W;     // the piece's first row
   int64_t ldw;
-  const uint16_t* P;   // planes of [M, pitch]
-  int64_t pitch;       // a multiple of 64
+  const uint16_t* P;   // planes of [M, pitch]; or, with sw, one matrix of the caller's
+  int64_t pitch;       // a multiple of 64 (of 8, N too, with sw)
   float* acc;          // [splits][M][kp], or null
   int64_t kp;          // pitch of a row of acc, a multiple of 4, >= K
   int M, N, K, planes;
   int tile, splits;    // of grad_split
   bool add;            // add to what acc holds (a later piece)
+  const float* sw;     // not null: W's rows are scaled by it
   GradOut out;
 };
 struct GradSplit {

@@ -22,10 +22,11 @@ __device__ __forceinline__ v16f mfma_bf16(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// two int8 of w (bytes 2 i and 2 i + 1) to bf16, exactly.  The conversion takes the
-// byte out of its word itself (written as source, the odd bytes cost a shift each).
-template <int i>
-__device__ __forceinline__ uint32_t widen2(int w) {
+// two int8 of w (bytes 2 i and 2 i + 1) to bf16, exactly, or times s0 and s1, rounded.
+// The conversion takes the byte out of its word itself (written as source, the odd
+// bytes cost a shift each).
+template <int i, bool SCALED>
+__device__ __forceinline__ uint32_t widen2(int w, float s0, float s1) {
   float lo, hi;
   if constexpr (i == 0) {
     asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
@@ -38,17 +39,22 @@ __device__ __forceinline__ uint32_t widen2(int w) {
     asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
         : "=v"(hi) : "v"(w));
   }
+  if constexpr (SCALED) {
+    lo *= s0;
+    hi *= s1;
+  }
   typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
   const v2bf r = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(uint32_t, r);
 }
-// part e (0..3) of a fragment of eight
-__device__ __forceinline__ uint32_t widen_part(v2i w, int e) {
+// part e (0..3) of a fragment of eight, their scales s
+template <bool SCALED>
+__device__ __forceinline__ uint32_t widen_part(v2i w, const float (&s)[8], int e) {
   switch (e) {
-    case 0: return widen2<0>(w[0]);
-    case 1: return widen2<1>(w[0]);
-    case 2: return widen2<0>(w[1]);
-    default: return widen2<1>(w[1]);
+    case 0: return widen2<0, SCALED>(w[0], s[0], s[1]);
+    case 1: return widen2<1, SCALED>(w[0], s[2], s[3]);
+    case 2: return widen2<0, SCALED>(w[1], s[4], s[5]);
+    default: return widen2<1, SCALED>(w[1], s[6], s[7]);
   }
 }
 
@@ -85,8 +91,9 @@ __device__ __forceinline__ void put_result(const GradOut& o, int64_t m, int k, i
 }
 
 // PLANES planes at a time (1, or all of them): W's tile is then read and converted
-// once for them.
-template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES>
+// once for them.  SCALED: the factor is a bf16 matrix of the caller's, N a multiple
+// of 8, and W's rows are scaled by sw as they are converted.
+template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES, bool SCALED>
 __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint32_t ktiles,
                                                                uint32_t mtiles) {
   constexpr int NW = WK * WM;
@@ -94,10 +101,12 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   using S = GradStage<BK, BM, PLANES>;
   constexpr int kRowsPer = 1024 / BK;  // rows of W per load
   constexpr int kLw = kRed / kRowsPer / NW, kLa = BM / 8 / NW;
-  constexpr int kLoads = kLw + PLANES * kLa;
+  constexpr int kLoads = kLw + PLANES * kLa + (SCALED ? 1 : 0);
   static_assert(kLw * kRowsPer * NW == kRed && kLa * 8 * NW == BM && NW % 2 == 0,
                 "every wave issues the same loads");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
+  // a step's scales, each wave its own copy of them
+  __shared__ __attribute__((aligned(256))) float swl[SCALED ? DEPTH * NW * kRed : 4];
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -114,6 +123,7 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   const int turns = a.planes / PLANES, its = count * turns;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t swl0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)swl;
   const int mvalid = (int)min((int64_t)BM, a.M - m0);
   const uint32_t arow = (uint32_t)(2 * a.pitch);
   int wrow[kLw];
@@ -131,6 +141,8 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     // rows past the last token repeat it: their results are dropped
     aoff[j] = (uint32_t)min(r, mvalid - 1) * arow + 16 * aslot(r, lane & 7);
   }
+  // (NW is even: the slot is the same in all of a wave's loads)
+  const int achunk = 16 * aslot(8 * (wave & 1) + (lane >> 3), lane & 7);
   // iteration `it` reads step first + it / turns, its planes from PLANES (it % turns)
   // on; astep and aplane are those that are loaded next
   int astep = first, aplane = 0;
@@ -142,11 +154,17 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
       const rsrc_t rs = gk::make_rsrc(a.W + n * a.ldw, (uint32_t)(nvalid * a.ldw));
       gk::dma16_if(take, rs, (uint32_t)(min(wrow[j], nvalid - 1) * (int)a.ldw) + wcol[j], 0,
                    to + S::kW + 1024 * (wave + NW * j));
+    } else if (SCALED && j == kLoads - 1) {
+      const rsrc_t rs = gk::make_rsrc(a.sw, (uint32_t)(4 * a.N));
+      gk::dma4_if(take, rs, (uint32_t)(4 * min(n + lane, (int64_t)a.N - 1)), 0,
+                  swl0 + (to - lds0) / S::kBytes * (4 * NW * kRed) + 4 * kRed * wave);
     } else {
       const int p = (j - kLw) / kLa, l = (j - kLw) % kLa;
+      // columns of the caller's matrix past the last eight repeat them (clear_tail)
+      const int over = SCALED ? min(0, 2 * a.N - 16 - (2 * (int)n + achunk)) : 0;
       const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)(aplane + p) * a.M + m0) * a.pitch,
                                       (uint32_t)mvalid * arow);
-      gk::dma16_if(take, rs, aoff[l], (uint32_t)(2 * n),
+      gk::dma16_if(take, rs, aoff[l] + (uint32_t)over, (uint32_t)(2 * n),
                    to + S::kA + p * S::kPlane + 1024 * (wave + NW * l));
     }
   };
@@ -172,11 +190,18 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   v2i wraw[2][TK];
   v8bf af[2][PLANES * TM];
   constexpr int kU = PLANES * TM;  // products of a fragment of W
-  constexpr int kReads = TK + kU, kProducts = TK * kU;
+  constexpr int kReads = TK + kU + (SCALED ? 2 : 0), kProducts = TK * kU;
   constexpr int kPerProduct = (2 * kReads + kProducts - 1) / kProducts;
   const int h = lane >> 5;
+  float sc[2][8];
   auto read = [&](int stage, int q, int r) {
-    if (r < TK) {
+    if (SCALED && r >= TK + kU) {
+      const int x = r - TK - kU;
+      const float4 v = *reinterpret_cast<const float4*>(
+          swl + (stage * NW + wave) * kRed + 16 * q + 8 * h + 4 * x);
+      sc[q & 1][4 * x] = v.x, sc[q & 1][4 * x + 1] = v.y;
+      sc[q & 1][4 * x + 2] = v.z, sc[q & 1][4 * x + 3] = v.w;
+    } else if (r < TK) {
       const int n = 16 * q + 8 * h + ((lane & 15) >> 1);
       const int c = 2 * (wk * TK + r) + ((lane >> 4) & 1);
       const uint8_t* p = lds + stage * S::kBytes + S::kW + n * BK + 16 * wslot<BK>(n, c) +
@@ -195,10 +220,10 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
   // products take (the next quarter's first in the last of this): a conversion
   // ahead of its products would leave the matrix cores idle.
   v4i wf[2];
-  auto convert = [&](int set, v2i raw, int u) {
+  auto convert = [&](int set, int q, int i, int u) {
 #pragma unroll
     for (int e = 4 * u / kU; e < 4 * (u + 1) / kU; ++e)
-      wf[set][e] = (int)widen_part(raw, e);
+      wf[set][e] = (int)widen_part<SCALED>(wraw[q & 1][i], sc[q & 1], e);
   };
   auto quarter = [&](int q, int from, uint32_t take, uint32_t to) {
 #pragma unroll
@@ -218,8 +243,10 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
           for (int l = p * kLoads / kProducts; l < (p + 1) * kLoads / kProducts; ++l)
             load(l, take, to);
         }
-        convert(set ^ 1, i + 1 < TK ? wraw[q & 1][i + 1 < TK ? i + 1 : 0] : wraw[(q + 1) & 1][0],
-                u);
+        if (i + 1 < TK)
+          convert(set ^ 1, q, i + 1 < TK ? i + 1 : 0, u);
+        else
+          convert(set ^ 1, q + 1, 0, u);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -231,13 +258,25 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     for (int j = 0; j < kLoads; ++j) load(j, s < its, lds0 + s * S::kBytes);
     advance();
   }
+  // the factor's columns from N on, in the last step of all
+  const bool tail = SCALED && a.N % kRed && first + count == steps;
+  auto clear_tail = [&](int stage) {
+    for (int i = t; i < BM * 8; i += 64 * NW) {
+      const int row = i >> 3, c = i & 7;
+      if (c >= a.N % kRed / 8)
+        *reinterpret_cast<v4i*>(lds + stage * S::kBytes + S::kA + row * 2 * kRed +
+                                16 * aslot(row, c)) = (v4i){0, 0, 0, 0};
+    }
+    gk::lds_barrier();
+  };
   if (its > 0) {
     wait_vm_if<(DEPTH - 1) * kLoads>(its >= DEPTH);
     gk::lds_barrier();
+    if (tail && its == 1) clear_tail(0);
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, 0, r);
 #pragma unroll
-    for (int u = 0; u < kU; ++u) convert(0, wraw[0][0], u);
+    for (int u = 0; u < kU; ++u) convert(0, 0, 0, u);
   }
   int buf = 0;
   for (int it = 0; it < its; ++it) {
@@ -246,6 +285,7 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint3
     for (int q = 0; q < 3; ++q) quarter(q, buf, 0, 0);
     wait_vm_if<(DEPTH - 2) * kLoads>(it + DEPTH - 1 < its);
     gk::lds_barrier();
+    if (tail && it + 2 == its) clear_tail(nbuf);
     quarter(3, nbuf, it + DEPTH < its, lds0 + buf * S::kBytes);
     advance();
     buf = nbuf;
@@ -409,7 +449,7 @@ GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
     // the low tiles take all planes in a step
     const double each = kTiles[i].us * (i >= 2 ? 0.65 + 0.35 * planes : (double)planes);
     double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * each;
-    if (s > 1 || !whole) t += 4.0 + (double)s * M * K * 8e-6 / 4.5;
+    if (s > 1 || !whole) t += 6.0 + (double)s * M * K * 8e-6 / 4.5;
     if (least < 0.0 || t < least) {
       best = GradSplit{i, (int)s};
       least = t;
@@ -430,22 +470,31 @@ int launch_grad(const GradArgs& a, hipStream_t st) {
   const dim3 grid((uint32_t)n);
   const auto run = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, st>>>(a, kt, mt); };
   switch (a.tile) {
-    case 0: run(grad_kernel<256, 256, 4, 2, 3, 1>, 512); break;
-    case 1: run(grad_kernel<128, 256, 2, 4, 3, 1>, 512); break;
+    case 0:
+      a.sw ? run(grad_kernel<256, 256, 4, 2, 3, 1, true>, 512)
+           : run(grad_kernel<256, 256, 4, 2, 3, 1, false>, 512);
+      break;
+    case 1:
+      a.sw ? run(grad_kernel<128, 256, 2, 4, 3, 1, true>, 512)
+           : run(grad_kernel<128, 256, 2, 4, 3, 1, false>, 512);
+      break;
     case 2:
-      a.planes == 1   ? run(grad_kernel<128, 128, 2, 2, 3, 1>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 3, 2>, 256)
-                      : run(grad_kernel<128, 128, 2, 2, 2, 3>, 256);
+      a.sw            ? run(grad_kernel<128, 128, 2, 2, 3, 1, true>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 128, 2, 2, 3, 1, false>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 3, 2, false>, 256)
+                      : run(grad_kernel<128, 128, 2, 2, 2, 3, false>, 256);
       break;
     case 3:
-      a.planes == 1   ? run(grad_kernel<128, 64, 2, 2, 3, 1>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 64, 2, 2, 3, 2>, 256)
-                      : run(grad_kernel<128, 64, 2, 2, 2, 3>, 256);
+      a.sw            ? run(grad_kernel<128, 64, 2, 2, 3, 1, true>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 64, 2, 2, 3, 1, false>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 64, 2, 2, 3, 2, false>, 256)
+                      : run(grad_kernel<128, 64, 2, 2, 2, 3, false>, 256);
       break;
     default:
-      a.planes == 1   ? run(grad_kernel<128, 32, 4, 1, 3, 1>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 32, 4, 1, 3, 2>, 256)
-                      : run(grad_kernel<128, 32, 4, 1, 3, 3>, 256);
+      a.sw            ? run(grad_kernel<128, 32, 4, 1, 3, 1, true>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 32, 4, 1, 3, 1, false>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 32, 4, 1, 3, 2, false>, 256)
+                      : run(grad_kernel<128, 32, 4, 1, 3, 3, false>, 256);
   }
   return 0;
 }

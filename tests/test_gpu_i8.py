@@ -307,6 +307,40 @@ def test_linear_grad(M, N, K, dtype):
     assert torch.equal(gq.linear_i8_grad(w, sw, dy), dx)
 
 
+@pytest.mark.parametrize("M", [1, 5, 32, 33, 64, 65, 128, 129, 300, 1030])
+@pytest.mark.parametrize("N,K", [(8, 40), (64, 128), (72, 515), (1000, 256), (4104, 300), (640, 2050)])
+def test_linear_grad_of_aligned_rows(M, N, K):
+    # bf16 rows on 16 bytes are read as they lie; what lies behind them is no part of
+    # the result, be it NaN
+    g = gen(M + N + K)
+    w, sw = i8(N, K, g, full=True), scales(N, g, 0.01)
+    wide = torch.full((M, N + 8 * (M % 3)), math.nan, dtype=torch.bfloat16, device="cuda")
+    dy = wide[:, :N]
+    dy.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    out = Guarded(M, K, torch.bfloat16, extra=N % 4)
+    dx = gq.linear_i8_grad(w, sw, dy, out=out.t)
+    torch.cuda.synchronize()
+    out.check()
+    a = dy.double() * sw.double()
+    ref = a @ w.double()
+    mag = a.abs() @ w.double().abs()
+    # one rounding of sw w (or of dy sw) to bf16, N additions in f32, the result's
+    tol = ((2 + N + 64) * U + 2.0 ** -8) * mag
+    tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+    odd = torch.zeros((M, N + 1), dtype=torch.bfloat16, device="cuda")[:, :N]
+    odd.copy_(dy)
+    dx2 = gq.linear_i8_grad(w, sw, odd)
+    assert bool(((dx2.double() - ref).abs() <= tol).all())
+    # rows with NaN and infinities stay apart from the others
+    if M > 4:
+        dy[1, N - 1], dy[2, 0], dy[3, N // 2] = math.nan, math.inf, -math.inf
+        dz = gq.linear_i8_grad(w, sw, dy)
+        assert bool(torch.isnan(dz[1]).all()) and not bool(torch.isfinite(dz[2:4]).any())
+        keep = [0] + list(range(4, M))
+        assert torch.equal(dz[keep], dx[keep])
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_linear_grad_is_the_adjoint(dtype):
     # <dy, w x> = <dx, x> for the layer as a linear map of the dequantized x
