@@ -14,6 +14,15 @@ namespace i8 {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t type_bytes(int type) { return type == GEMMQ_F32 ? 4 : 2; }
 
+// a launch holds fewer than 2^32 threads in a dimension
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (1LL << 32); }
+// x workgroups for each of M rows, the rows over the second and third dimensions
+// (a kernel's row is blockIdx.y + gridDim.y * blockIdx.z, and may lie past M)
+inline dim3 rows_grid(int64_t x, int64_t M) {
+  const int64_t y = M < 32768 ? M : 32768;
+  return dim3((uint32_t)x, (uint32_t)y, (uint32_t)ceil_div(M, y));
+}
+
 // whether every row of a matrix can be read 16 bytes at a time from its first value
 inline bool wide_rows(const void* p, int64_t ld, int type) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * type_bytes(type) % 16 == 0;
@@ -110,7 +119,7 @@ struct GradArgs {
   int M, N, K, planes;
   int tile, splits;    // of grad_split
   bool add;            // add to what acc holds (a later piece)
-  const float* sw;     // not null: W's rows are scaled by it
+  const float* sw;     // not null (M <= 128): W's rows are scaled by it
   GradOut out;
 };
 struct GradSplit {

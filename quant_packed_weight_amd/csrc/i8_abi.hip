@@ -86,12 +86,17 @@ bool grad_shape_ok(int64_t M, int64_t K, const GradPlan& p) {
   return grad_fits(p.split, (int)M, (int)K) && product_fits((int)M, (int)p.piece, (int)K);
 }
 
-// A bf16 dY whose rows allow 16-byte loads is read by the product as it lies, and W
-// scaled by sw instead (a rounding of sw * w to bf16 in the place of one of dy *
-// sw): no factor in the workspace, and a launch less.
-bool reads_dy(int type, const void* dY, int64_t lddy, int64_t N) {
-  return type == GEMMQ_BF16 && N % 8 == 0 && N > 0 && wide_rows(dY, lddy, type) &&
-         lddy <= ((int64_t)1 << 22);
+// Up to 128 tokens a bf16 dY whose rows allow 16-byte loads is read by the product as
+// it lies, and W scaled by sw instead (a rounding of sw * w to bf16 in the place of
+// one of dy * sw): no factor in the workspace, and a launch less (4096 x 4096 at M =
+// 16 15 -> 12 us, M = 128 29 -> 26).  The larger tiles' conversion has no room for
+// the scaling (M = 512, 12288 x 4096 72 us with the factor, 77 so; M = 4096, 4096 x
+// 12288 371 and 399).
+constexpr int64_t kScaledMaxM = 128;
+
+bool reads_dy(int type, const void* dY, int64_t lddy, int64_t M, int64_t N) {
+  return type == GEMMQ_BF16 && M <= kScaledMaxM && N % 8 == 0 && N > 0 &&
+         wide_rows(dY, lddy, type) && lddy <= ((int64_t)1 << 22);
 }
 
 GradPlan direct_plan(int64_t M, int64_t N, int64_t K) {
@@ -232,7 +237,7 @@ size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K)
   const GradPlan p = grad_plan(type, M, N, K);
   if (!grad_shape_ok(M, K, p)) return 0;
   // whichever way dY's rows will allow
-  if (type != GEMMQ_BF16 || N == 0) return p.bytes();
+  if (type != GEMMQ_BF16 || N == 0 || M > kScaledMaxM) return p.bytes();
   const GradPlan d = direct_plan(M, N, K);
   if (!grad_fits(d.split, (int)M, (int)K)) return 0;
   return d.bytes() > p.bytes() ? d.bytes() : p.bytes();
@@ -256,7 +261,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (reads_dy(type, dY, lddy, N)) {
+  if (reads_dy(type, dY, lddy, M, N)) {
     const GradPlan d = direct_plan(M, N, K);
     const GradOut out = grad_out(type, dX, lddx);
     float* acc = d.direct ? nullptr : static_cast<float*>(ws);

@@ -490,7 +490,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
   __shared__ float tops[4], sums[4];
   __shared__ int dots[4];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int64_t m = blockIdx.x;
+  const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+  if (m >= op.M) return;  // all of the workgroup
   const float2* p = o.part + m * o.ntiles;
   const int64_t tg = o.target[m];
   const bool hit = tg >= 0 && tg < op.N;
@@ -532,7 +533,6 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
   }
 }
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr int kCUs = 256;
 
 // The tiles, their groups of waves, and how many of their workgroups a compute
@@ -543,6 +543,7 @@ struct Tile {
 constexpr Tile kTiles[] = {{256, 256, 1, 1}, {128, 256, 1, 1}, {128, 128, 1, 2}, {128, 64, 1, 3},
                            {64, 64, 1, 3},   {128, 64, 2, 1},  {64, 64, 2, 2},   {64, 32, 4, 1},
                            {64, 32, 1, 3},   {128, 32, 1, 2}};
+constexpr int kMaxThreads = 512;
 constexpr int kTileCount = 9;  // of those that pick_tile compares
 constexpr int kWideTile = 9;
 
@@ -598,7 +599,7 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
   const int pick = pick_tile(a.op.M, a.op.N, a.op.K);
   const Tile& c = kTiles[pick];
   const int64_t n = tiles(c, a.op.M, a.op.N);
-  if (n > kMaxGrid) return -1;
+  if (!grid_fits(n, kMaxThreads)) return -1;
   a.mtiles = (uint32_t)ceil_div(a.op.M, c.bm);
   a.ntiles = (uint32_t)ceil_div(a.op.N, c.bn);
   a.group = 1024 / c.bm;
@@ -621,7 +622,7 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
 }  // namespace
 
 bool product_fits(int M, int N, int K) {
-  return tiles(kTiles[pick_tile(M, N, K)], M, N) <= kMaxGrid;
+  return grid_fits(tiles(kTiles[pick_tile(M, N, K)], M, N), kMaxThreads);
 }
 
 int launch_linear(const Operands& op, const LinearOut& out, hipStream_t st) {
@@ -647,7 +648,7 @@ int launch_loss(const Operands& op, const LossOut& out, hipStream_t st) {
 
 int launch_loss_join(const Operands& op, const LossOut& o, float* loss, float* lse,
                      hipStream_t st) {
-  loss_join_kernel<<<(uint32_t)op.M, 256, 0, st>>>(op, o, loss, lse);
+  loss_join_kernel<<<rows_grid(1, op.M), 256, 0, st>>>(op, o, loss, lse);
   return 0;
 }
 

@@ -412,14 +412,6 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* acc, int64_t k
   if (k < K) put_result(out, m, k, K, v);
 }
 
-// rows over the grid's second and third dimensions
-dim3 rows_grid(int64_t x, int64_t M) {
-  const int64_t y = M < 32768 ? M : 32768;
-  return dim3((uint32_t)x, (uint32_t)y, (uint32_t)ceil_div(M, y));
-}
-
-constexpr int64_t kMaxGrid = 0x7fffffff;
-
 struct Tile {
   int bk, bm, grid;  // grid: workgroups that fill the chip
   double us;         // of a step, measured
@@ -444,40 +436,37 @@ GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
   double least = -1.0;
   for (int i = from; i <= to; ++i) {
     const int64_t n = tiles(kTiles[i], M, K);
-    int64_t s = n < kTiles[i].grid ? kTiles[i].grid / n : 1;
-    if (s > steps) s = steps;
+    int64_t most = n < kTiles[i].grid ? kTiles[i].grid / n : 1;
+    if (most > steps) most = steps;
     // the low tiles take all planes in a step
     const double each = kTiles[i].us * (i >= 2 ? 0.65 + 0.35 * planes : (double)planes);
-    double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * each;
-    if (s > 1 || !whole) t += 6.0 + (double)s * M * K * 8e-6 / 4.5;
-    if (least < 0.0 || t < least) {
-      best = GradSplit{i, (int)s};
-      least = t;
+    for (const int64_t s : {(int64_t)1, most}) {
+      double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * each;
+      if (s > 1 || !whole) t += 6.0 + (double)s * M * K * 8e-6 / 4.5;
+      if (least < 0.0 || t < least) {
+        best = GradSplit{i, (int)s};
+        least = t;
+      }
     }
   }
   return best;
 }
 
 bool grad_fits(const GradSplit& s, int M, int K) {
-  return tiles(kTiles[s.tile], M, K) * s.splits <= kMaxGrid;
+  return grid_fits(tiles(kTiles[s.tile], M, K) * s.splits, 512);
 }
 
 int launch_grad(const GradArgs& a, hipStream_t st) {
   const Tile& c = kTiles[a.tile];
   const uint32_t mt = (uint32_t)ceil_div(a.M, c.bm), kt = (uint32_t)ceil_div(a.K, c.bk);
   const int64_t n = (int64_t)mt * kt * a.splits;
-  if (n > kMaxGrid) return -1;
+  if (!grid_fits(n, 512)) return -1;
   const dim3 grid((uint32_t)n);
   const auto run = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, st>>>(a, kt, mt); };
   switch (a.tile) {
-    case 0:
-      a.sw ? run(grad_kernel<256, 256, 4, 2, 3, 1, true>, 512)
-           : run(grad_kernel<256, 256, 4, 2, 3, 1, false>, 512);
-      break;
-    case 1:
-      a.sw ? run(grad_kernel<128, 256, 2, 4, 3, 1, true>, 512)
-           : run(grad_kernel<128, 256, 2, 4, 3, 1, false>, 512);
-      break;
+    // M > 128: never with sw
+    case 0: run(grad_kernel<256, 256, 4, 2, 3, 1, false>, 512); break;
+    case 1: run(grad_kernel<128, 256, 2, 4, 3, 1, false>, 512); break;
     case 2:
       a.sw            ? run(grad_kernel<128, 128, 2, 2, 3, 1, true>, 256)
       : a.planes == 1 ? run(grad_kernel<128, 128, 2, 2, 3, 1, false>, 256)

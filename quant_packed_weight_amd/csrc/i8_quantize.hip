@@ -13,10 +13,11 @@ constexpr int kHeld = 8;
 
 template <int TYPE>
 __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ldx, bool wide,
-                                                       int8_t* Q, int64_t ldq, float* s, int K) {
+                                                       int8_t* Q, int64_t ldq, float* s, int M, int K) {
   constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8, kSpan = 256 * V;
   __shared__ uint32_t tops[4];
-  const int64_t m = blockIdx.x, x0 = m * ldx;
+  const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z, x0 = m * ldx;
+  if (m >= M) return;  // all of the workgroup
   const int t = threadIdx.x;
   uint4 held[kHeld];
   uint32_t top = 0;
@@ -77,14 +78,14 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
 
 int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
                     int K, hipStream_t st) {
-  const dim3 g((uint32_t)M);
+  const dim3 g = rows_grid(1, M);
   const bool wide = wide_rows(X, ldx, type);
   if (type == GEMMQ_F32)
-    quantize_kernel<GEMMQ_F32><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_F32><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
   else if (type == GEMMQ_BF16)
-    quantize_kernel<GEMMQ_BF16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_BF16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
   else
-    quantize_kernel<GEMMQ_F16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, K);
+    quantize_kernel<GEMMQ_F16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
   return 0;
 }
 

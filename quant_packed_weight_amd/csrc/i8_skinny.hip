@@ -8,9 +8,9 @@
 // but no sum across lanes is needed.  A workgroup takes 16 channels, its waves
 // alternate 128-byte pieces of K and add their sums through LDS.  Bound by the
 // read of W; the activations' reads from L2, as many bytes as W's for each 16
-// tokens, are why more tokens go to tiles in LDS (i8_gemm.hip).  Against 32 or 64 channels a workgroup (fewer such reads, fewer
-// workgroups): N = K = 4096 at M = 8 5.9 / 8.1 / 12.4 us, 151936 x 2048 at M = 1
-// 53 / 54 / 59.
+// tokens, are why more tokens go to tiles in LDS (i8_gemm.hip).  16, 32 or 64
+// channels a workgroup (fewer such reads, fewer workgroups): N = K = 4096 at M = 8
+// 5.9 / 8.1 / 12.4 us, 151936 x 2048 at M = 1 53 / 54 / 59.
 #include "i8_common.h"
 
 namespace gemmq {
@@ -233,7 +233,7 @@ template <int EPI>
 int launch(SkinnyArgs& a, hipStream_t st) {
   // the factor's columns up to its pitch are written, zero from N on
   const int64_t n = ceil_div(EPI == kFactor ? a.fac.pitch : a.op.N, kSkinnyChannels);
-  if (n > 0x7fffffff) return -1;
+  if (!grid_fits(n, 1024)) return -1;
   const dim3 grid((uint32_t)n);
   // The more workgroups, the fewer waves need to share a channel's K (us, eight
   // waves / four: M = 8, 4096 x 4096 5.9 / 6.2, 12288 x 4096 14.4 / 13.5; M = 16,
@@ -290,7 +290,7 @@ int launch_fused(int xtype, const void* X, int64_t ldx, const Operands& op, cons
   a.xtype = xtype;
   a.xwide = wide_rows(X, ldx, xtype);
   const int64_t n = ceil_div(op.N, kSkinnyChannels);
-  if (n > 0x7fffffff) return -1;
+  if (!grid_fits(n, 1024)) return -1;
   const dim3 grid((uint32_t)n);
   // The more waves, the sooner the workgroup has its activations; the more
   // workgroups, the less that matters: M = 1, 16, 8 and 4 waves, N = K = 4096 6.6 /

@@ -310,8 +310,8 @@ def test_linear_grad(M, N, K, dtype):
 @pytest.mark.parametrize("M", [1, 5, 32, 33, 64, 65, 128, 129, 300, 1030])
 @pytest.mark.parametrize("N,K", [(8, 40), (64, 128), (72, 515), (1000, 256), (4104, 300), (640, 2050)])
 def test_linear_grad_of_aligned_rows(M, N, K):
-    # bf16 rows on 16 bytes are read as they lie; what lies behind them is no part of
-    # the result, be it NaN
+    # bf16 rows on 16 bytes are read as they lie up to 128 tokens; what lies behind
+    # them is no part of the result, be it NaN
     g = gen(M + N + K)
     w, sw = i8(N, K, g, full=True), scales(N, g, 0.01)
     wide = torch.full((M, N + 8 * (M % 3)), math.nan, dtype=torch.bfloat16, device="cuda")
@@ -606,6 +606,34 @@ def test_results_past_32_bits():
     rows = torch.tensor([0, 1, 127, 128, 20000, 32767, 32768, M - 129, M - 1], device="cuda")
     _, ref = product(w, sw, xq[rows], sx[rows])
     assert bool(((y[rows].double() - ref).abs() <= (2.0 ** -8 + 8 * U) * ref.abs()).all())
+
+
+def test_many_rows():
+    # more rows than a grid dimension of 32768 takes, and not a multiple of it
+    M, K, N = 70001, 48, 40
+    g = gen(13)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    q, s = gq.quantize_i8(x)
+    xd = x.double()
+    sr = (xd.abs().amax(1) / 127).float()
+    assert torch.equal(s, sr)
+    assert torch.equal(q.float(), (xd / sr.double()[:, None]).float().round())
+    w, sw = i8(N, K, g), scales(N, g, 0.01)
+    t = torch.randint(0, N, (M,), generator=g, device="cuda")
+    z, lse_r, loss_r = loss_reference(w, sw, q, s, t)
+    loss, lse = gq.loss_i8(w, sw, q, s, t)
+    tol = 4 * logit_error(z) + 320 * U + 3 * U * lse_r.abs()
+    assert bool(((loss.double() - loss_r).abs() <= tol + 2 * U * loss_r.abs()).all())
+    for dt in (torch.float32, torch.bfloat16):
+        dx = gq.loss_i8_grad(w, sw, q, s, t, lse, torch.ones(M, device="cuda"), out_dtype=dt)
+        f = torch.softmax(z, 1)
+        f[torch.arange(M, device="cuda"), t] -= 1.0
+        ref = (f * sw.double()) @ w.double()
+        assert float((dx.double() - ref).norm() / ref.norm()) <= (2.0 ** -8 if dt != torch.float32 else 2.0 ** -18)
+    dy = torch.randn((M, N), generator=g, device="cuda")
+    dx = gq.linear_i8_grad(w, sw, dy)
+    ref = (dy.double() * sw.double()) @ w.double()
+    assert float((dx.double() - ref).norm() / ref.norm()) <= 2.0 ** -21
 
 
 # ------------------------------------------------------------------ together

@@ -121,6 +121,12 @@ def test_grid_limits_are_refused_before_anything_runs(L):
         a = dict(args, **{k: v for k, v in big.items() if k in args})
         assert getattr(L, "gemmq_" + name)(*a.values(), None) == SHAPE, name
     assert L.gemmq_loss_i8_workspace(gq.I8_MAX_ROWS, gq.I8_MAX_ROWS, 64) == 0
+    # 2^19 x 2^20: 2^23 tiles of 512 threads, one launch's threads pass 2^32
+    a = dict(M=1 << 19, N=1 << 20, ldy=1 << 20)
+    assert L.gemmq_gemm_i8(*dict(GEMM, **a).values(), None) == SHAPE
+    assert L.gemmq_linear_i8(*dict(LINEAR, **a).values(), None) == SHAPE
+    assert L.gemmq_loss_i8_workspace(1 << 19, 1 << 20, 64) == 0
+    assert L.gemmq_loss_i8_workspace(1 << 18, 1 << 20, 64) > 0  # half of that fits
 
 
 def test_workspace_sizes(L):
