@@ -72,14 +72,20 @@ def _type(dtype, name):
     return t
 
 
-def _matrix(t, name, dtype, rows, cols, device):
-    """The row pitch of a [rows, cols] device tensor, in elements."""
-    if t.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+def _refuse(t, name, dtype, shape, index):
+    """Raises for a tensor that is not what the call needs."""
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not on device %s" % (name, t.device, index))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != (rows, cols):
-        raise ValueError("%s must be %s, got %s" % (name, (rows, cols), tuple(t.shape)))
+    raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def _matrix(t, name, dtype, rows, cols, index):
+    """The row pitch of a [rows, cols] tensor on device `index`, in elements."""
+    if (t.get_device() != index or t.shape != (rows, cols)
+            or (dtype is not None and t.dtype != dtype)):
+        _refuse(t, name, dtype, (rows, cols), index)
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s must have consecutive values in its rows" % name)
@@ -87,10 +93,14 @@ def _matrix(t, name, dtype, rows, cols, device):
     return ld if rows > 1 else -(-cols // 4) * 4
 
 
-def _i8_matrix(t, name, rows, cols, device):
+def _i8_matrix(t, name, rows, cols, index):
     """The row pitch of an int8 matrix; its rows lie multiples of 16 bytes apart,
     and each row's bytes up to a multiple of 16 belong to the tensor's memory."""
-    ld = _matrix(t, name, _torch.int8, rows, cols, device)
+    if t.get_device() != index or t.shape != (rows, cols) or t.dtype != _torch.int8:
+        _refuse(t, name, _torch.int8, (rows, cols), index)
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s must have consecutive values in its rows" % name)
     row = -(-cols // 16) * 16
     if rows <= 1:
         ld = max(row, 16)
@@ -102,41 +112,37 @@ def _i8_matrix(t, name, rows, cols, device):
     return ld
 
 
-def _vector(t, name, dtype, n, device):
-    if t.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != (n,):
-        raise ValueError("%s must have shape (%d,), got %s" % (name, n, tuple(t.shape)))
+def _vector(t, name, dtype, n, index):
+    if t.get_device() != index or t.shape != (n,) or t.dtype != dtype:
+        _refuse(t, name, dtype, (n,), index)
     if n > 1 and t.stride(0) != 1:
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _elsewhere(device, stream):
-    """None where a call on tensors of `device` runs on the current stream of the
+def _elsewhere(t, index, stream):
+    """None where a call on tensors of t's device runs on the current stream of the
     current device; else a context in which it does: the tensors' device and
     `stream`, so that what the call allocates belongs to the stream that uses it."""
-    if device.type != "cuda":
+    if stream is None and index >= 0 and _torch._C._cuda_getDevice() == index:
+        return None
+    if index < 0:
         raise TypeError("the tensors must be device tensors")
     if stream is None:
-        if _torch.cuda.current_device() == device.index:
-            return None
-        return _torch.cuda.device(device)
+        return _torch.cuda.device(index)
     if not isinstance(stream, _torch.cuda.Stream):
         h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = (_torch.cuda.ExternalStream(h, device) if h
-                  else _torch.cuda.default_stream(device))
-    if stream.device != device:
-        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+        stream = (_torch.cuda.ExternalStream(h, t.device) if h
+                  else _torch.cuda.default_stream(t.device))
+    if stream.device != t.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
     return _torch.cuda.stream(stream)  # enters the stream's device too
 
 
-def _here(device):
+def _here(index):
     """The current stream of the current device, as the C side takes it (the same
     handle as torch.cuda.current_stream's, without building a Stream for it)."""
-    return _torch._C._cuda_getCurrentRawStream(device.index) or None
+    return _torch._C._cuda_getCurrentRawStream(index) or None
 
 
 def _new_i8(rows, cols, device):
@@ -166,17 +172,17 @@ def quantize_i8(x, out=None, scale=None, stream=None):
     (gemmq_quantize_i8): returns (int8 [M, K], f32 [M]).  Activations per token,
     or weights [N, K] per output channel."""
     L = _fns or lib_i8()
-    dev = x.device
     ty = _type(x.dtype, "x")
-    at = _elsewhere(dev, stream)
+    at = _elsewhere(x, x.get_device(), stream)
     if at is not None:
         with at:
             return quantize_i8(x, out, scale)
     M, K = x.shape
+    dev = x.get_device()
     if out is None:
-        out = _new_i8(M, K, dev)
+        out = _new_i8(M, K, x.device)
     if scale is None:
-        scale = _torch.empty(M, dtype=_torch.float32, device=dev)
+        scale = _torch.empty(M, dtype=_torch.float32, device=x.device)
     _check(L.gemmq_quantize_i8(ty, x.data_ptr(), _matrix(x, "x", None, M, K, dev), out.data_ptr(),
                                _i8_matrix(out, "out", M, K, dev),
                                _vector(scale, "scale", _torch.float32, M, dev), M, K, _here(dev)),
@@ -188,15 +194,15 @@ def gemm_i8(w, sw, xq, sx, bias=None, out=None, out_dtype=None, stream=None):
     """y = (sx xq) (sw w)^T + bias for int8 w [N, K], xq [M, K] and their scales
     (gemmq_gemm_i8): f32, bf16 or f16 [M, N] (`out_dtype`, f32 by default)."""
     L = _fns or lib_i8()
-    dev = w.device
-    at = _elsewhere(dev, stream)
+    dev = w.get_device()
+    at = _elsewhere(w, dev, stream)
     if at is not None:
         with at:
             return gemm_i8(w, sw, xq, sx, bias, out, out_dtype)
     N, K = w.shape
     M = xq.shape[0]
     f32 = _torch.float32
-    out = _result(out, out_dtype, f32, (M, N), dev)
+    out = _result(out, out_dtype, f32, (M, N), w.device)
     _check(L.gemmq_gemm_i8(
         w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", f32, N, dev),
         xq.data_ptr(), _i8_matrix(xq, "xq", M, K, dev), _vector(sx, "sx", f32, M, dev),
@@ -211,19 +217,19 @@ def linear_i8(w, sw, x, bias=None, out=None, out_dtype=None, xq=None, sx=None, s
     token, then gemm_i8 (gemmq_linear_i8).  Returns [M, N] in `out_dtype` (x's by
     default); xq and sx, when given, receive the quantized activations."""
     L = _fns or lib_i8()
-    dev = w.device
-    at = _elsewhere(dev, stream)
+    dev = w.get_device()
+    at = _elsewhere(w, dev, stream)
     if at is not None:
         with at:
             return linear_i8(w, sw, x, bias, out, out_dtype, xq, sx)
     N, K = w.shape
     M = x.shape[0]
     f32 = _torch.float32
-    out = _result(out, out_dtype, x.dtype, (M, N), dev)
+    out = _result(out, out_dtype, x.dtype, (M, N), w.device)
     if xq is None:
-        xq = _new_i8(M, K, dev)
+        xq = _new_i8(M, K, w.device)
     if sx is None:
-        sx = _torch.empty(M, dtype=f32, device=dev)
+        sx = _torch.empty(M, dtype=f32, device=w.device)
     _check(L.gemmq_linear_i8(
         w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", f32, N, dev),
         _type(x.dtype, "x"), x.data_ptr(), _matrix(x, "x", None, M, K, dev), xq.data_ptr(),
@@ -239,8 +245,8 @@ def linear_i8_grad(w, sw, dy, out=None, workspace=None, stream=None):
     activations (gemmq_linear_i8_grad): dy [M, N] -> [M, K] of dy's type.
     `workspace`: a tensor of at least linear_i8_grad_workspace bytes, or None."""
     L = _fns or lib_i8()
-    dev = w.device
-    at = _elsewhere(dev, stream)
+    dev = w.get_device()
+    at = _elsewhere(w, dev, stream)
     if at is not None:
         with at:
             return linear_i8_grad(w, sw, dy, out, workspace)
@@ -248,8 +254,8 @@ def linear_i8_grad(w, sw, dy, out=None, workspace=None, stream=None):
     M = dy.shape[0]
     ty = _type(dy.dtype, "dy")
     if out is None:
-        out = _torch.empty((M, K), dtype=dy.dtype, device=dev)
-    ws = _workspace(workspace, L.gemmq_linear_i8_grad_workspace(ty, M, N, K), dev)
+        out = _torch.empty((M, K), dtype=dy.dtype, device=w.device)
+    ws = _workspace(workspace, L.gemmq_linear_i8_grad_workspace(ty, M, N, K), w.device)
     _check(L.gemmq_linear_i8_grad(
         w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", _torch.float32, N, dev), ty,
         dy.data_ptr(), _matrix(dy, "dy", None, M, N, dev), out.data_ptr(),
@@ -263,8 +269,8 @@ def loss_i8(w, sw, xq, sx, target, loss=None, lse=None, workspace=None, stream=N
     [N, K], the logits never in memory (gemmq_loss_i8): returns (loss, lse), f32
     [M]; target int64 [M], negative where a position is ignored (loss 0)."""
     L = _fns or lib_i8()
-    dev = w.device
-    at = _elsewhere(dev, stream)
+    dev = w.get_device()
+    at = _elsewhere(w, dev, stream)
     if at is not None:
         with at:
             return loss_i8(w, sw, xq, sx, target, loss, lse, workspace)
@@ -272,10 +278,10 @@ def loss_i8(w, sw, xq, sx, target, loss=None, lse=None, workspace=None, stream=N
     M = xq.shape[0]
     f32 = _torch.float32
     if loss is None:
-        loss = _torch.empty(M, dtype=f32, device=dev)
+        loss = _torch.empty(M, dtype=f32, device=w.device)
     if lse is None:
-        lse = _torch.empty(M, dtype=f32, device=dev)
-    ws = _workspace(workspace, L.gemmq_loss_i8_workspace(M, N, K), dev)
+        lse = _torch.empty(M, dtype=f32, device=w.device)
+    ws = _workspace(workspace, L.gemmq_loss_i8_workspace(M, N, K), w.device)
     _check(L.gemmq_loss_i8(
         w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", f32, N, dev),
         xq.data_ptr(), _i8_matrix(xq, "xq", M, K, dev), _vector(sx, "sx", f32, M, dev),
@@ -291,17 +297,17 @@ def loss_i8_grad(w, sw, xq, sx, target, lse, dloss, out=None, out_dtype=None, wo
     states sx xq (gemmq_loss_i8_grad): [M, K] in `out_dtype` (bf16 by default);
     lse from loss_i8."""
     L = _fns or lib_i8()
-    dev = w.device
-    at = _elsewhere(dev, stream)
+    dev = w.get_device()
+    at = _elsewhere(w, dev, stream)
     if at is not None:
         with at:
             return loss_i8_grad(w, sw, xq, sx, target, lse, dloss, out, out_dtype, workspace)
     N, K = w.shape
     M = xq.shape[0]
     f32 = _torch.float32
-    out = _result(out, out_dtype, _torch.bfloat16, (M, K), dev)
+    out = _result(out, out_dtype, _torch.bfloat16, (M, K), w.device)
     ty = _type(out.dtype, "out")
-    ws = _workspace(workspace, L.gemmq_loss_i8_grad_workspace(ty, M, N, K), dev)
+    ws = _workspace(workspace, L.gemmq_loss_i8_grad_workspace(ty, M, N, K), w.device)
     _check(L.gemmq_loss_i8_grad(
         w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", f32, N, dev),
         xq.data_ptr(), _i8_matrix(xq, "xq", M, K, dev), _vector(sx, "sx", f32, M, dev),
