@@ -287,14 +287,14 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
   // from the registers, four values of a token at a time and 32 tokens an
   // instruction, the factor of M = 1024 by 50688 rows took 200 us instead of 160.
   // Their image: BN / 8 chunks of 16 bytes a row, chunk c of row m in slot c ^ (m
-  // mod BN / 8).
-  constexpr int kChunks = BN / 8;
+  // mod BN / 8), or c ^ (m mod 8) where that is no power of two.
+  constexpr int kChunks = BN / 8, kMix = (kChunks & (kChunks - 1)) == 0 ? kChunks - 1 : 7;
   static_assert(BM * BN * 2 <= GROUPS * DEPTH * S::kBytes, "the results fit the steps' buffers");
   bool staged = false;
   if constexpr (EPI == kLinear) staged = a.lin.type != GEMMQ_F32;
   if constexpr (EPI == kFactor) staged = a.fac.planes == 1;
   auto put = [&](int ml, int nl, uint32_t lo, uint32_t hi) {
-    *reinterpret_cast<uint2*>(lds + (ml * kChunks + ((nl >> 3) ^ (ml & (kChunks - 1)))) * 16 +
+    *reinterpret_cast<uint2*>(lds + (ml * kChunks + ((nl >> 3) ^ (ml & kMix))) * 16 +
                               8 * h) = make_uint2(lo, hi);
   };
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
           const int64_t n = n0 + 8 * c;
           if (m0 + ml >= op.M || n >= width) continue;
           const v4i v = *reinterpret_cast<const v4i*>(
-              lds + (ml * kChunks + (c ^ (ml & (kChunks - 1)))) * 16);
+              lds + (ml * kChunks + (c ^ (ml & kMix))) * 16);
           uint16_t* to = out + (m0 + ml) * pitch + n;
           if (n + 8 <= width) {
             *reinterpret_cast<v4i*>(to) = v;
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
           const int ml = i / BN, nl = i % BN;
           if (m0 + ml >= op.M || n0 + nl >= width) continue;
           out[(m0 + ml) * pitch + n0 + nl] = *reinterpret_cast<const uint16_t*>(
-              lds + (ml * kChunks + ((nl >> 3) ^ (ml & (kChunks - 1)))) * 16 + 2 * (nl & 7));
+              lds + (ml * kChunks + ((nl >> 3) ^ (ml & kMix))) * 16 + 2 * (nl & 7));
         }
       }
     }
@@ -535,30 +535,39 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
 
 constexpr int kCUs = 256;
 
-// The tiles, their groups of waves, and how many of their workgroups a compute
-// unit holds (by LDS).
+// A tile, its groups of waves, and the time of a K step (us) on a compute unit that
+// works on one, two or three such workgroups at a time, 0 where its LDS holds
+// fewer.  A step waits for its loads: the times are near 64 bytes a nanosecond
+// where much is in flight, and never below the 0.42 us of a round trip.
 struct Tile {
-  int bn, bm, groups, resident;
+  int bn, bm, groups;
+  float step[3];
 };
-constexpr Tile kTiles[] = {{256, 256, 1, 1}, {128, 256, 1, 1}, {128, 128, 1, 2}, {128, 64, 1, 3},
-                           {64, 64, 1, 3},   {128, 64, 2, 1},  {64, 64, 2, 2},   {64, 32, 4, 1},
-                           {64, 32, 1, 3},   {128, 32, 1, 2}};
+constexpr Tile kTiles[] = {
+    {256, 256, 1, {1.55f, 0, 0}},       {128, 256, 1, {1.02f, 0, 0}},
+    {192, 128, 1, {0.86f, 0, 0}},       {128, 128, 1, {0.70f, 1.05f, 0}},
+    {128, 128, 1, {0.66f, 0, 0}},       {128, 64, 1, {0.50f, 0.70f, 1.0f}},
+    {64, 64, 1, {0.43f, 0.50f, 0.75f}}, {128, 64, 2, {0.88f, 0, 0}},
+    {64, 64, 2, {0.74f, 0.88f, 0}},     {64, 32, 4, {0.85f, 0, 0}},
+    {64, 32, 1, {0.42f, 0.45f, 0.6f}},  {128, 32, 1, {}}};
 constexpr int kMaxThreads = 512;
-constexpr int kTileCount = 9;  // of those that pick_tile compares
-constexpr int kWideTile = 9;
+constexpr int kTileCount = 11;  // of those that pick_tile compares
+constexpr int kWideTile = 11;
 
 int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div(N, c.bn); }
 
-// The tile with the least estimated time.  What the K loop waits for is its loads:
-// per compute unit 44, 52 and 62 bytes a nanosecond with one, two and more groups
-// of waves on it; a step has a round trip of 0.42 us in it that small tiles do not
-// get below; a workgroup costs 2 us around its loop, and an output 0.08 ns.
-// Measured against it (us; tiles in the order of kTiles):
-//   M 2048 N 4096 K 12288  137 / 106 / 107 / 164 / 192 / - / - / - / -
-//   M 512 N 12288 K 4096   50 / 37 / 37 / 36 / 45 / - / - / - / -
-//   M 512 N 4096 K 4096    - / - / 24 / 22 / 20 / 16 / 17 / 31 / 30
-//   M 128 N 4096 K 4096    - / - / 21 / 17 / 14 / 14 / 11 / 9 / 15
-//   M 64 N 4096 K 4096     - / - / 20 / 16 / 14 / 14 / 11 / 8 / 14
+// The tile with the least estimated time: rounds of the chip, each of the K steps,
+// 2 us around them, and 0.08 ns for an output.  Measured (us, random int8 data;
+// tiles in the order of kTiles, the one taken in brackets):
+//   M 4096 N 4096 K 4096   [63] 74   80    72    85   87   106   108   115
+//   M 2048 N 4096 K 12288  127 [102] 147   104   136  155  183   158   177
+//   M 512 N 12288 K 4096   51   37  [32]   34    45   36   45    44    46
+//   M 1504 N 5008 K 2560   36  [27]  36    26    31   36   37    40    41
+//   M 1024 N 4096 K 4096   49   34   28    28   [25]  26   33    30    31
+//   M 512 N 4096 K 4096    45   30   26    24    22   22   18.5 [16.8] 16.6
+//   M 200 N 2048 K 2048    26   18   16    12    12   11   10    10   [8.4]
+// and, with the last two, 4096 x 4096: M 128 14 / 14 / 11 / [9] / 15 and M 64
+// 14 / 14 / 11 / [8] / 14 from {64, 64} on.
 // Up to 32 tokens of a vocabulary W's stream decides, and 128 channels a workgroup
 // are ahead of 64 (M = 8, 151936 x 2048 57 us against 59).
 int pick_tile(int M, int N, int K) {
@@ -569,14 +578,11 @@ int pick_tile(int M, int N, int K) {
   for (int i = 0; i < kTileCount; ++i) {
     const Tile& c = kTiles[i];
     const int64_t n = tiles(c, M, N);
-    int64_t r = ceil_div(n, kCUs);
-    if (r > c.resident) r = c.resident;
-    const int64_t on = r * c.groups;
+    int r = 1;
+    while (r < 3 && c.step[r] > 0.0f && n > kCUs * r) ++r;
     const double rounds = (double)ceil_div(n, kCUs * r);
-    double step = (double)on * (c.bn + c.bm) * kStep / (on == 1 ? 44.0 : on == 2 ? 52.0 : 62.0);
-    if (step < 420.0) step = 420.0;
-    const double t = rounds * ((double)ceil_div(steps, c.groups) * step + 2000.0 +
-                               0.08 * (double)r * c.bn * c.bm);
+    const double t = rounds * ((double)ceil_div(steps, c.groups) * c.step[r - 1] + 2.0 +
+                               0.08e-3 * r * c.bn * c.bm);
     if (i == 0 || t < least) {
       best = i;
       least = t;
@@ -607,13 +613,15 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
   switch (pick) {
     case 0: tile_kernel<256, 256, 2, 4, 2, 1, EPI><<<grid, 512, 0, st>>>(a); break;
     case 1: tile_kernel<128, 256, 2, 4, 3, 1, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 2: tile_kernel<128, 128, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 3: tile_kernel<128, 64, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 4: tile_kernel<64, 64, 2, 2, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 5: tile_kernel<128, 64, 2, 2, 3, 2, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 6: tile_kernel<64, 64, 2, 2, 2, 2, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 7: tile_kernel<64, 32, 2, 1, 3, 4, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 8: tile_kernel<64, 32, 2, 1, 4, 1, EPI><<<grid, 128, 0, st>>>(a); break;
+    case 2: tile_kernel<192, 128, 2, 4, 3, 1, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 3: tile_kernel<128, 128, 2, 4, 2, 1, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 4: tile_kernel<128, 128, 2, 4, 4, 1, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 5: tile_kernel<128, 64, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 6: tile_kernel<64, 64, 2, 2, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
+    case 7: tile_kernel<128, 64, 2, 2, 3, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 8: tile_kernel<64, 64, 2, 2, 2, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 9: tile_kernel<64, 32, 2, 1, 3, 4, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 10: tile_kernel<64, 32, 2, 1, 4, 1, EPI><<<grid, 128, 0, st>>>(a); break;
     default: tile_kernel<128, 32, 4, 1, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
   }
   return 0;

@@ -90,12 +90,17 @@ __device__ __forceinline__ void put_result(const GradOut& o, int64_t m, int k, i
   store4_as(o.dX, m * o.lddx + k, o.type, o.wide, K - k, v.x, v.y, v.z, v.w);
 }
 
+// Two waves a SIMD, or the one that four waves with more than half of the LDS are.
+template <int BK, int BM, int WAVES, int DEPTH, int PLANES>
+constexpr int kWavesPerSimd =
+    WAVES <= 4 && DEPTH * GradStage<BK, BM, PLANES>::kBytes > 81920 ? 1 : 2;
+
 // PLANES planes at a time (1, or all of them): W's tile is then read and converted
 // once for them.  SCALED: the factor is a bf16 matrix of the caller's, N a multiple
 // of 8, and W's rows are scaled by sw as they are converted.
 template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES, bool SCALED>
-__global__ __launch_bounds__(64 * WK * WM, 2) void grad_kernel(GradArgs a, uint32_t ktiles,
-                                                               uint32_t mtiles) {
+__global__ __launch_bounds__(64 * WK * WM, (kWavesPerSimd<BK, BM, WK * WM, DEPTH, PLANES>)) void
+grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   constexpr int NW = WK * WM;
   constexpr int TK = BK / WK / 32, TM = BM / WM / 32;
   using S = GradStage<BK, BM, PLANES>;

@@ -162,7 +162,8 @@ WIDE = [(1, 40000, 1030), (1, 300, 16384), (1, 130, 20000), (2, 16400, 300), (2,
         (48, 4096, 4100), (64, 70000, 100), (90, 5000, 900), (128, 4096, 640), (300, 4100, 1300),
         (513, 2052, 2200), (512, 12300, 300), (700, 2000, 600), (1030, 6200, 200),
         (2048, 4100, 500), (2050, 8200, 130), (4100, 4200, 200), (530, 13500, 40), (780, 7760, 36),
-        (641, 4430, 40), (99, 12340, 36), (33, 8420, 40), (66, 11700, 140), (36, 8230, 140)]
+        (641, 4430, 40), (99, 12340, 36), (33, 8420, 40), (66, 11700, 140), (36, 8230, 140),
+        (560, 11030, 140), (560, 11030, 1100), (282, 13580, 1100), (641, 4430, 1100)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES + WIDE)
@@ -408,7 +409,7 @@ LOSSES = [(1, 1, 1), (1, 1000, 64), (1, 32003, 515), (2, 127, 100), (5, 128, 128
           (128, 256, 512), (130, 1111, 640), (257, 2050, 255), (500, 513, 64), (3, 16390, 200),
           (12, 16384, 600), (20, 70001, 260), (48, 4096, 1000), (100, 20000, 130), (300, 9000, 300),
           (600, 12300, 140), (2050, 8200, 130), (530, 13500, 40), (780, 7760, 36), (641, 4430, 40),
-          (66, 11700, 140), (36, 8230, 140)]
+          (66, 11700, 140), (36, 8230, 140), (99, 12340, 36), (282, 13580, 300), (641, 4430, 700)]
 
 
 @pytest.mark.parametrize("M,N,K", LOSSES)
