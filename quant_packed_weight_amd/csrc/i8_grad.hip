@@ -95,9 +95,10 @@ template <int BK, int BM, int WAVES, int DEPTH, int PLANES>
 constexpr int kWavesPerSimd =
     WAVES <= 4 && DEPTH * GradStage<BK, BM, PLANES>::kBytes > 81920 ? 1 : 2;
 
-// PLANES planes at a time (1, or all of them): W's tile is then read and converted
-// once for them.  SCALED: the factor is a bf16 matrix of the caller's, N a multiple
-// of 8, and W's rows are scaled by sw as they are converted.
+// All PLANES planes in a step: W's tile is read and converted once for them (M =
+// 2048, 4096 x 4096 in f32 152 us, one plane after another 188).  SCALED: the factor
+// is a bf16 matrix of the caller's, N a multiple of 8, and W's rows are scaled by sw
+// as they are converted.
 template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES, bool SCALED>
 __global__ __launch_bounds__(64 * WK * WM, (kWavesPerSimd<BK, BM, WK * WM, DEPTH, PLANES>)) void
 grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
@@ -121,14 +122,15 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   id /= mtiles;
   const int k0 = (int)(id % ktiles) * BK, split = (int)(id / ktiles);
 
-  // this split's share of the steps of kRed rows; the planes go over it PLANES at a time
+  // this split's share of the steps of kRed rows
   const int steps = (a.N + kRed - 1) / kRed;
   const int per = steps / a.splits, more = steps % a.splits;
-  const int first = split * per + min(split, more), count = per + (split < more ? 1 : 0);
-  const int turns = a.planes / PLANES, its = count * turns;
+  const int first = split * per + min(split, more), its = per + (split < more ? 1 : 0);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const uint32_t swl0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)swl;
+  uint32_t swl0 = 0;
+  if constexpr (SCALED)
+    swl0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)swl;
   const int mvalid = (int)min((int64_t)BM, a.M - m0);
   const uint32_t arow = (uint32_t)(2 * a.pitch);
   int wrow[kLw];
@@ -148,11 +150,9 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   }
   // (NW is even: the slot is the same in all of a wave's loads)
   const int achunk = 16 * aslot(8 * (wave & 1) + (lane >> 3), lane & 7);
-  // iteration `it` reads step first + it / turns, its planes from PLANES (it % turns)
-  // on; astep and aplane are those that are loaded next
-  int astep = first, aplane = 0;
+  int next = first;  // the step that is loaded next
   auto load = [&](int j, uint32_t take, uint32_t to) {
-    const int64_t n = (int64_t)min(astep, steps - 1) * kRed;
+    const int64_t n = (int64_t)min(next, steps - 1) * kRed;
     if (j < kLw) {
       // rows of W past the last one repeat it: the factor is zero there
       const int nvalid = (int)min((int64_t)kRed, a.N - n);
@@ -167,17 +167,10 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
       const int p = (j - kLw) / kLa, l = (j - kLw) % kLa;
       // columns of the caller's matrix past the last eight repeat them (clear_tail)
       const int over = SCALED ? min(0, 2 * a.N - 16 - (2 * (int)n + achunk)) : 0;
-      const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)(aplane + p) * a.M + m0) * a.pitch,
+      const rsrc_t rs = gk::make_rsrc(a.P + ((int64_t)p * a.M + m0) * a.pitch,
                                       (uint32_t)mvalid * arow);
       gk::dma16_if(take, rs, aoff[l] + (uint32_t)over, (uint32_t)(2 * n),
                    to + S::kA + p * S::kPlane + 1024 * (wave + NW * l));
-    }
-  };
-  auto advance = [&] {
-    aplane += PLANES;
-    if (aplane == a.planes) {
-      aplane = 0;
-      ++astep;
     }
   };
 
@@ -261,10 +254,10 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   for (int s = 0; s < DEPTH; ++s) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) load(j, s < its, lds0 + s * S::kBytes);
-    advance();
+    ++next;
   }
   // the factor's columns from N on, in the last step of all
-  const bool tail = SCALED && a.N % kRed && first + count == steps;
+  const bool tail = SCALED && a.N % kRed && first + its == steps;
   auto clear_tail = [&](int stage) {
     for (int i = t; i < BM * 8; i += 64 * NW) {
       const int row = i >> 3, c = i & 7;
@@ -292,7 +285,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
     gk::lds_barrier();
     if (tail && it + 2 == its) clear_tail(nbuf);
     quarter(3, nbuf, it + DEPTH < its, lds0 + buf * S::kBytes);
-    advance();
+    ++next;
     buf = nbuf;
   }
 
@@ -417,38 +410,61 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* acc, int64_t k
   if (k < K) put_result(out, m, k, K, v);
 }
 
+// A tile, and by the factor's planes (1 to 3) the time of a step (us) on a compute
+// unit that works on one, two or three such workgroups at a time, 0 where its LDS
+// holds fewer or there is no such tile.
 struct Tile {
-  int bk, bm, grid;  // grid: workgroups that fill the chip
-  double us;         // of a step, measured
+  int bk, bm;
+  float step[3][3];
 };
-constexpr Tile kTiles[] = {{256, 256, 256, 1.9}, {128, 256, 256, 1.15}, {128, 128, 512, 0.9},
-                           {128, 64, 512, 0.7},  {128, 32, 512, 0.6}};
+constexpr Tile kTiles[] = {
+    {256, 256, {{1.5f}}},
+    {256, 128, {{1.0f, 1.7f}, {1.5f}, {2.15f}}},
+    {128, 128, {{0.69f, 1.05f}, {0.9f, 1.55f}, {1.25f}}},
+    {128, 64, {{0.56f, 0.77f, 1.1f}, {0.67f, 1.0f}, {0.8f, 1.3f}}},
+    {128, 32, {{0.5f, 0.6f}, {0.55f, 0.75f}, {0.62f, 0.85f}}}};
+constexpr int kCUs = 256, kMaxThreads = 512;
 
 int64_t tiles(const Tile& c, int M, int K) { return ceil_div(M, c.bm) * ceil_div(K, c.bk); }
 
 }  // namespace
 
-// Up to 128 tokens the lowest tile that holds them; beyond, the one of the two
-// with the least estimated time, the partial sums' passage through memory (4.5
-// TB/s) and the launch that adds them counted: M = 2048, N = 12288, K = 4096 takes
-// 222 us in 128 x 256 tiles as one range, and 190 in 256 x 256 as two, which 14
-// then add up; M = 1024, N = 50688, K = 2048 216 in four ranges and 181 in eight.
-// A range has at least one step.
+// The tile and the number of ranges with the least estimated time: rounds of the
+// chip, each of its range's steps and 3 us around them, and for partial sums their
+// passage through memory (4.5 TB/s) and a launch's 3 (M = 1 over 364 x 2724 took 12 us
+// as one range and 16 as six).  Measured (us, with the sums' launch; the best number
+// of ranges for each tile in the order of kTiles, the one taken in brackets):
+//   one plane   M 16 N 4096 K 4096      -      -      -     11.8 [11.1]
+//               M 128 N 12288 K 4096    40     33   [30]    32    33
+//               M 200 N 2048 K 2048     23     18     15   [14]
+//               M 512 N 12288 K 4096    66   [65]     67    85
+//               M 2048 N 4096 K 4096    88   [74]     77   107
+//               M 2048 N 12288 K 4096 [193]   202    218   309
+//   two         M 1024 N 4096 K 4096     -     69   [67]    73
+//   three       M 1500 N 2560 K 5008     -   [92]    114   118
+//               M 64 N 12288 K 4096      -     38     41   [30]   31
+// The two widest would be more than half empty up to 128 tokens, the lowest reads W
+// too often beyond.  A range has at least one step.
 GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
   const int64_t steps = ceil_div(N < 1 ? 1 : N, kRed);
-  const int from = M <= 32 ? 4 : M <= 64 ? 3 : M <= 128 ? 2 : 0, to = M <= 128 ? from : 1;
-  GradSplit best{from, 1};
-  double least = -1.0;
-  for (int i = from; i <= to; ++i) {
+  GradSplit best{0, 0};
+  double least = 0.0;
+  for (int i = M <= 128 ? 2 : 0; i <= (M <= 128 ? 4 : 3); ++i) {
+    const float* step = kTiles[i].step[planes - 1];
+    if (!(step[0] > 0.0f)) continue;
     const int64_t n = tiles(kTiles[i], M, K);
-    int64_t most = n < kTiles[i].grid ? kTiles[i].grid / n : 1;
-    if (most > steps) most = steps;
-    // the low tiles take all planes in a step
-    const double each = kTiles[i].us * (i >= 2 ? 0.65 + 0.35 * planes : (double)planes);
-    for (const int64_t s : {(int64_t)1, most}) {
-      double t = (double)ceil_div(n * s, kTiles[i].grid) * (double)ceil_div(steps, s) * each;
-      if (s > 1 || !whole) t += 6.0 + (double)s * M * K * 8e-6 / 4.5;
-      if (least < 0.0 || t < least) {
+    // one range, or as many as fill the chip with one, two or three workgroups
+    for (int f = 0; f <= 3; ++f) {
+      if (f > 0 && !(step[f - 1] > 0.0f)) break;
+      int64_t s = f == 0 ? 1 : kCUs * f / n;
+      if (s > steps) s = steps;
+      if (s < 1) continue;
+      int r = 1;
+      while (r < 3 && step[r] > 0.0f && n * s > kCUs * r) ++r;
+      double t = (double)ceil_div(n * s, kCUs * r) *
+                 ((double)ceil_div(steps, s) * step[r - 1] + 3.0);
+      if (s > 1 || !whole) t += 3.0 + (double)s * M * K * 8e-6 / 4.5;
+      if (best.splits == 0 || t < least) {
         best = GradSplit{i, (int)s};
         least = t;
       }
@@ -458,24 +474,28 @@ GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
 }
 
 bool grad_fits(const GradSplit& s, int M, int K) {
-  return grid_fits(tiles(kTiles[s.tile], M, K) * s.splits, 512);
+  return grid_fits(tiles(kTiles[s.tile], M, K) * s.splits, kMaxThreads);
 }
 
 int launch_grad(const GradArgs& a, hipStream_t st) {
   const Tile& c = kTiles[a.tile];
   const uint32_t mt = (uint32_t)ceil_div(a.M, c.bm), kt = (uint32_t)ceil_div(a.K, c.bk);
   const int64_t n = (int64_t)mt * kt * a.splits;
-  if (!grid_fits(n, 512)) return -1;
+  if (!grid_fits(n, kMaxThreads)) return -1;
   const dim3 grid((uint32_t)n);
   const auto run = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, st>>>(a, kt, mt); };
+  // with sw: up to 128 tokens, in the lower three tiles
   switch (a.tile) {
-    // M > 128: never with sw
     case 0: run(grad_kernel<256, 256, 4, 2, 3, 1, false>, 512); break;
-    case 1: run(grad_kernel<128, 256, 2, 4, 3, 1, false>, 512); break;
+    case 1:
+      a.planes == 1   ? run(grad_kernel<256, 128, 4, 2, 2, 1, false>, 512)
+      : a.planes == 2 ? run(grad_kernel<256, 128, 4, 2, 3, 2, false>, 512)
+                      : run(grad_kernel<256, 128, 4, 2, 2, 3, false>, 512);
+      break;
     case 2:
       a.sw            ? run(grad_kernel<128, 128, 2, 2, 3, 1, true>, 256)
       : a.planes == 1 ? run(grad_kernel<128, 128, 2, 2, 3, 1, false>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 3, 2, false>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 2, 2, false>, 256)
                       : run(grad_kernel<128, 128, 2, 2, 2, 3, false>, 256);
       break;
     case 3:

@@ -275,7 +275,8 @@ GRADS = [(1, 1, 1), (1, 64, 64), (1, 1000, 300), (2, 63, 130), (5, 65, 33), (8, 
          (64, 1111, 640), (77, 1037, 515), (128, 128, 128), (129, 2000, 255), (200, 50, 1000),
          (256, 1024, 512), (300, 333, 777), (513, 640, 264), (16, 20000, 200), (40, 9000, 600),
          (100, 30000, 130), (700, 3001, 2050), (2050, 130, 4100), (1500, 70, 5000), (4, 64, 100000),
-         (1400, 3001, 70)]
+         (1400, 3001, 70), (500, 4097, 1030), (1030, 1100, 4090), (1030, 2300, 4090),
+         (2050, 777, 4100), (270, 3716, 7555)]
 
 
 @pytest.mark.parametrize("M,N,K", GRADS)
