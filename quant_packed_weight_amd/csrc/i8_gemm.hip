@@ -535,39 +535,40 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
 
 constexpr int kCUs = 256;
 
-// A tile, its groups of waves, and the time of a K step (us) on a compute unit that
+// A tile, its groups of waves, the waves of a group, and the time of a K step (us) on a compute unit that
 // works on one, two or three such workgroups at a time, 0 where its LDS holds
 // fewer.  A step waits for its loads: the times are near 64 bytes a nanosecond
 // where much is in flight, and never below the 0.42 us of a round trip.
 struct Tile {
-  int bn, bm, groups;
+  int bn, bm, groups, waves;
   float step[3];
 };
 constexpr Tile kTiles[] = {
-    {256, 256, 1, {1.55f, 0, 0}},       {128, 256, 1, {1.02f, 0, 0}},
-    {192, 128, 1, {0.86f, 0, 0}},       {128, 128, 1, {0.70f, 1.05f, 0}},
-    {128, 128, 1, {0.66f, 0, 0}},       {128, 64, 1, {0.50f, 0.70f, 1.0f}},
-    {64, 64, 1, {0.43f, 0.50f, 0.75f}}, {128, 64, 2, {0.88f, 0, 0}},
-    {64, 64, 2, {0.74f, 0.88f, 0}},     {64, 32, 4, {0.85f, 0, 0}},
-    {64, 32, 1, {0.42f, 0.45f, 0.6f}},  {128, 32, 1, {}}};
+    {256, 256, 1, 8, {1.55f, 0, 0}},       {128, 256, 1, 8, {1.02f, 0, 0}},
+    {192, 128, 1, 8, {0.86f, 0, 0}},       {128, 128, 1, 8, {0.70f, 1.05f, 0}},
+    {128, 128, 1, 8, {0.66f, 0, 0}},       {128, 64, 1, 4, {0.50f, 0.70f, 1.0f}},
+    {64, 64, 1, 4, {0.43f, 0.50f, 0.75f}}, {64, 64, 2, 4, {0.74f, 0.88f, 0}},
+    {64, 32, 4, 2, {0.85f, 0, 0}},         {64, 32, 1, 2, {0.42f, 0.45f, 0.6f}},
+    {128, 32, 1, 4, {}}};
 constexpr int kMaxThreads = 512;
-constexpr int kTileCount = 11;  // of those that pick_tile compares
-constexpr int kWideTile = 11;
+constexpr int kTileCount = 10;  // of those that pick_tile compares
+constexpr int kWideTile = 10;
 
 int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div(N, c.bn); }
 
 // The tile with the least estimated time: rounds of the chip, each of the K steps,
-// 2 us around them, and 0.08 ns for an output.  Measured (us, random int8 data;
-// tiles in the order of kTiles, the one taken in brackets):
-//   M 4096 N 4096 K 4096   [63] 74   80    72    85   87   106   108   115
-//   M 2048 N 4096 K 12288  127 [102] 147   104   136  155  183   158   177
-//   M 512 N 12288 K 4096   51   37  [32]   34    45   36   45    44    46
-//   M 1504 N 5008 K 2560   36  [27]  36    26    31   36   37    40    41
-//   M 1024 N 4096 K 4096   49   34   28    28   [25]  26   33    30    31
-//   M 512 N 4096 K 4096    45   30   26    24    22   22   18.5 [16.8] 16.6
-//   M 200 N 2048 K 2048    26   18   16    12    12   11   10    10   [8.4]
-// and, with the last two, 4096 x 4096: M 128 14 / 14 / 11 / [9] / 15 and M 64
-// 14 / 14 / 11 / [8] / 14 from {64, 64} on.
+// 2 us around them, and 0.08 ns for an output, more where fewer than eight waves (two
+// a SIMD) write them: the groups' sums are one group's to finish.  Measured (us,
+// random int8 data; tiles in the order of kTiles, the one taken in brackets):
+//   M 4096 N 4096 K 4096   [63] 74   80    72    85    87   106   115
+//   M 2048 N 4096 K 12288  127 [102] 147   104   136   155  183   177
+//   M 512 N 12288 K 4096   51   37  [32]   34    45    36   45    46
+//   M 1504 N 5008 K 2560   36  [27]  36    26    31    36   37    41
+//   M 1024 N 4096 K 4096   49   34   28    28   [25]   26   33    31
+//   M 64 N 151936 K 2048   -    -    82    76    78   [69]  67    72    120   81
+//   M 512 N 4096 K 4096    45   30   26    24    22    22   18.5 [16.6]
+//   M 64 N 32000 K 4096    -    -    26    28    25    31   22.3 [22.2] 33    30
+//   M 128 N 4096 K 4096                                17   14    11   [9]    15
 // Up to 32 tokens of a vocabulary W's stream decides, and 128 channels a workgroup
 // are ahead of 64 (M = 8, 151936 x 2048 57 us against 59).
 int pick_tile(int M, int N, int K) {
@@ -581,8 +582,9 @@ int pick_tile(int M, int N, int K) {
     int r = 1;
     while (r < 3 && c.step[r] > 0.0f && n > kCUs * r) ++r;
     const double rounds = (double)ceil_div(n, kCUs * r);
+    const int writers = r * c.waves < 8 ? r * c.waves : 8;
     const double t = rounds * ((double)ceil_div(steps, c.groups) * c.step[r - 1] + 2.0 +
-                               0.08e-3 * r * c.bn * c.bm);
+                               0.64e-3 / writers * r * c.bn * c.bm);
     if (i == 0 || t < least) {
       best = i;
       least = t;
@@ -618,10 +620,9 @@ int launch_tiles(TileArgs& a, hipStream_t st) {
     case 4: tile_kernel<128, 128, 2, 4, 4, 1, EPI><<<grid, 512, 0, st>>>(a); break;
     case 5: tile_kernel<128, 64, 2, 2, 2, 1, EPI><<<grid, 256, 0, st>>>(a); break;
     case 6: tile_kernel<64, 64, 2, 2, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
-    case 7: tile_kernel<128, 64, 2, 2, 3, 2, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 8: tile_kernel<64, 64, 2, 2, 2, 2, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 9: tile_kernel<64, 32, 2, 1, 3, 4, EPI><<<grid, 512, 0, st>>>(a); break;
-    case 10: tile_kernel<64, 32, 2, 1, 4, 1, EPI><<<grid, 128, 0, st>>>(a); break;
+    case 7: tile_kernel<64, 64, 2, 2, 2, 2, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 8: tile_kernel<64, 32, 2, 1, 3, 4, EPI><<<grid, 512, 0, st>>>(a); break;
+    case 9: tile_kernel<64, 32, 2, 1, 4, 1, EPI><<<grid, 128, 0, st>>>(a); break;
     default: tile_kernel<128, 32, 4, 1, 3, 1, EPI><<<grid, 256, 0, st>>>(a); break;
   }
   return 0;

@@ -410,7 +410,8 @@ LOSSES = [(1, 1, 1), (1, 1000, 64), (1, 32003, 515), (2, 127, 100), (5, 128, 128
           (128, 256, 512), (130, 1111, 640), (257, 2050, 255), (500, 513, 64), (3, 16390, 200),
           (12, 16384, 600), (20, 70001, 260), (48, 4096, 1000), (100, 20000, 130), (300, 9000, 300),
           (600, 12300, 140), (2050, 8200, 130), (530, 13500, 40), (780, 7760, 36), (641, 4430, 40),
-          (66, 11700, 140), (36, 8230, 140), (99, 12340, 36), (282, 13580, 300), (641, 4430, 700)]
+          (66, 11700, 140), (36, 8230, 140), (99, 12340, 36), (282, 13580, 300), (641, 4430, 700),
+          (50, 70000, 60)]
 
 
 @pytest.mark.parametrize("M,N,K", LOSSES)
