@@ -102,6 +102,13 @@ __device__ __forceinline__ void clear_tail(uint8_t* x, int k0, int K, int t) {
   }
 }
 
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+// the upper half of the wave's lanes in a and the lower half in b, exchanged
+__device__ __forceinline__ v2u swap_halves(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return (v2u){r[0], r[1]};
+}
+
 // (max, sum) of one part of a row, the sum taken relative to the row's maximum
 __device__ __forceinline__ float join_term(float2 p, float top) {
   // a part without columns is (-inf, 0)
@@ -411,20 +418,55 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
           for (int g = 0; g < 4; ++g) {
             const int nl = nw + 32 * i + 8 * g;
             const float4 sw = *reinterpret_cast<const float4*>(swl + nl);
-            float f[4] = {v[i][4 * g] * sw.x, v[i][4 * g + 1] * sw.y, v[i][4 * g + 2] * sw.z,
-                          v[i][4 * g + 3] * sw.w};
+            float(&f)[16] = v[i];
+            f[4 * g] *= sw.x, f[4 * g + 1] *= sw.y, f[4 * g + 2] *= sw.z, f[4 * g + 3] *= sw.w;
             if (edge) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (n0 + nl + e >= op.N) f[e] = 0.0f;
+                if (n0 + nl + e >= op.N) f[4 * g + e] = 0.0f;
             }
             if (staged)
-              put(ml, nl, bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
-                  bf16_bits(f[2]) | bf16_bits(f[3]) << 16);
-            else if (n0 + nl < a.fac.pitch)  // a multiple of 4
-              store_planes(a.fac.P + m * a.fac.pitch + n0 + nl, (int64_t)op.M * a.fac.pitch,
-                           a.fac.planes, f);
+              put(ml, nl, bf16_bits(f[4 * g]) | bf16_bits(f[4 * g + 1]) << 16,
+                  bf16_bits(f[4 * g + 2]) | bf16_bits(f[4 * g + 3]) << 16);
           }
+        // More planes, from the registers: lanes l and l + 32 hold a token's channels
+        // 0-3 and 4-7 of eight; of two such groups the lower lane takes the first
+        // whole and the upper one the second, 16 bytes each and 32 next to each other
+        // (three planes of 1000 x 32000: 158 -> 120 us; through LDS as above, a plane
+        // at a time, 155).  With one 32-channel tile a wave the values as they lie are
+        // faster (37 x 32003: 11 us, exchanged 13).
+        if (!staged) {
+          const int64_t plane = (int64_t)op.M * a.fac.pitch;
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+              float(&f)[16] = v[i];
+              if constexpr (TN == 1) {
+#pragma unroll
+                for (int u = g; u < g + 2; ++u) {
+                  float w[4] = {f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]};
+                  const int64_t n = n0 + nw + 8 * u;
+                  if (n < a.fac.pitch)  // a multiple of 64
+                    store_planes(a.fac.P + m * a.fac.pitch + n, plane, a.fac.planes, w);
+                }
+              } else {
+                const int64_t n = n0 + wn * TN * 32 + 32 * i + 8 * (g + h);
+                uint16_t* to = a.fac.P + m * a.fac.pitch + n;
+                for (int p = 0; p < a.fac.planes; ++p) {
+                  uint32_t b[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    b[e] = bf16_part(f[4 * g + e], p + 1 == a.fac.planes);
+                  const v2u lo = swap_halves(b[0] | b[1] << 16, b[4] | b[5] << 16);
+                  const v2u hi = swap_halves(b[2] | b[3] << 16, b[6] | b[7] << 16);
+                  if (n < a.fac.pitch)
+                    *reinterpret_cast<uint4*>(to + p * plane) =
+                        make_uint4(lo[0], hi[0], lo[1], hi[1]);
+                }
+              }
+            }
+        }
       }
     }
   }
@@ -535,10 +577,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
 
 constexpr int kCUs = 256;
 
-// A tile, its groups of waves, the waves of a group, and the time of a K step (us) on a compute unit that
-// works on one, two or three such workgroups at a time, 0 where its LDS holds
-// fewer.  A step waits for its loads: the times are near 64 bytes a nanosecond
-// where much is in flight, and never below the 0.42 us of a round trip.
+// A tile, its groups of waves, the waves of a group, and the time of a K step (us) on
+// a compute unit that works on one, two or three such workgroups at a time, 0 where
+// its LDS holds fewer.  A step waits for its loads: the times are near 64 bytes a
+// nanosecond where much is in flight, and never below the 0.42 us of a round trip.
 struct Tile {
   int bn, bm, groups, waves;
   float step[3];
