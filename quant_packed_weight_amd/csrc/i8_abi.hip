@@ -51,8 +51,8 @@ size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 // of kMinPiece columns where the rows alone are more: it bounds the workspace.  A
 // further piece costs a passage of the partial sums through memory and another
 // last round of tiles, more than a factor that fits the 256 MB last-level cache
-// saves (M = 1024 over 151936 rows: 128 MB, three pieces, 1094 us; 256 MB 1016; 384
-// MB, one piece, 981).
+// saves (M = 1024 over 151936 rows: 128 MB, three pieces, 1020 us; 256 MB 953; 384
+// MB, one piece, 924).
 constexpr int64_t kFactorBytes = (int64_t)384 << 20;
 constexpr int64_t kMinPiece = 1024;
 
@@ -89,9 +89,9 @@ bool grad_shape_ok(int64_t M, int64_t K, const GradPlan& p) {
 // Up to 128 tokens a bf16 dY whose rows allow 16-byte loads is read by the product as
 // it lies, and W scaled by sw instead (a rounding of sw * w to bf16 in the place of
 // one of dy * sw): no factor in the workspace, and a launch less (4096 x 4096 at M =
-// 16 15 -> 12 us, M = 128 29 -> 26).  The larger tiles' conversion has no room for
-// the scaling (M = 512, 12288 x 4096 72 us with the factor, 77 so; M = 4096, 4096 x
-// 12288 371 and 399).
+// 16 15 -> 12 us, M = 128 29 -> 26).  With more tokens the large tiles are the faster
+// ones, whose conversion has no room for the scaling: with the factor / as it lies M =
+// 129 over 2048 x 2048 15.4 / 14.3 us, 4096 x 12288 39 / 50, M = 512 68 / 82.
 constexpr int64_t kScaledMaxM = 128;
 
 bool reads_dy(int type, const void* dY, int64_t lddy, int64_t M, int64_t N) {

@@ -1,6 +1,7 @@
 // i8_grad.hip -- the product that both gradients need, acc[m, k] = sum_n
 // A[m, n] W[n, k]: int8 weights, exact in bf16, against a factor A given as one
-// to three bf16 matrices whose sum it is; and the kernels before and after it.
+// to three bf16 matrices whose sum it is, or weights scaled and rounded to bf16
+// against the caller's own bf16 rows; and the kernels before and after it.
 //
 // W is read as it lies, rows of N along the reduction: the transposing LDS read
 // hands each lane the eight consecutive n of its own k, which are converted to
