@@ -154,8 +154,9 @@ size_t gemmq_loss_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K);
  * target[m] >= N NaN.
  *   lse    f32 [M], from gemmq_loss_i8 on the same arguments.
  *   dloss  f32 [M].   type, dX, lddx  [M, K], overwritten.
- * `type` also sets the precision of the softmax factor, as gemmq_linear_i8_grad's
- * dY: one, two or three bf16 numbers for GEMMQ_BF16, GEMMQ_F16, GEMMQ_F32.
+ * `type` also sets the precision of the softmax factor: one bf16 number for
+ * GEMMQ_BF16 (two up to M == 8, and the target's to 16 bits for any M), two for
+ * GEMMQ_F16, three for GEMMQ_F32.
  * Errors: as gemmq_loss_i8.
  */
 int gemmq_loss_i8_grad(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Xq,

@@ -70,6 +70,7 @@ struct FactorOut {
   uint16_t* P;
   int64_t pitch, n0;
   int planes;
+  float* rest;  // [M], or null: what one plane's rounding leaves of the target's value
 };
 
 int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
@@ -108,6 +109,9 @@ struct GradOut {
   void* dX;
   int64_t lddx;
   bool wide;  // four consecutive values of a row may be stored at once
+  const float* rest;  // not null: rest[m] * (row target[m] of W) is added to v[m]
+  const int8_t* W;    // (with rest) all rows, as the entry point has them
+  int64_t ldw;
 };
 struct GradArgs {
   const int8_t* W;     // the piece's first row

@@ -65,9 +65,9 @@ struct GradPlan {
   size_t bytes() const { return factor_bytes + acc_bytes; }
 };
 
-GradPlan grad_plan(int type, int64_t M, int64_t N, int64_t K) {
+GradPlan grad_plan(int planes, int64_t M, int64_t N, int64_t K) {
   GradPlan p;
-  p.planes = planes_of(type);
+  p.planes = planes;
   int64_t most = kFactorBytes / (2 * p.planes * M) / 256 * 256;
   if (most < kMinPiece) most = kMinPiece;
   const int64_t n64 = (int64_t)align_up(N < 1 ? 1 : N, 64);
@@ -136,6 +136,15 @@ int run_grad(const GradPlan& p, const int8_t* W, int64_t ldw, const GradOut& out
   return launched(
       launch_finish(acc, p.kp, N > 0 ? p.split.splits : 0, out, (int)M, (int)K, st));
 }
+
+// The loss's factor is often a few large numbers a row: exp(z - lse) - 1 at the target,
+// and exp(z - lse) of the likeliest others.  With one bf16 number each their few
+// roundings do not average out (M = 2 over 3137 x 768 2.8e-3 relative, the result's
+// own rounding 1.6e-3).  So what is left of the target's is kept, and added at the end
+// (2.3e-3), and up to eight rows, where chance has the least rows to even out and the
+// product waits for W more than for the matrix cores, have two numbers for each value.
+int loss_planes(int type, int64_t M) { return type == GEMMQ_BF16 && M <= 8 ? 2 : planes_of(type); }
+size_t rest_bytes(const GradPlan& p, int64_t M) { return p.planes == 1 ? align_up(4 * M, 256) : 0; }
 
 GradOut grad_out(int type, void* dX, int64_t lddx) {
   GradOut o{};
@@ -234,7 +243,7 @@ int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, co
 
 size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
   if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0) return 0;
-  const GradPlan p = grad_plan(type, M, N, K);
+  const GradPlan p = grad_plan(planes_of(type), M, N, K);
   if (!grad_shape_ok(M, K, p)) return 0;
   // whichever way dY's rows will allow
   if (type != GEMMQ_BF16 || N == 0 || M > kScaledMaxM) return p.bytes();
@@ -254,7 +263,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
   if (rc == GEMMQ_OK && N > 0) rc = check_i8(W, ldw, sw, K);
   if (rc == GEMMQ_OK && N > 0) rc = check_rows(type, dY, lddy, N);
   if (rc != GEMMQ_OK) return rc;
-  const GradPlan p = grad_plan(type, M, N, K);
+  const GradPlan p = grad_plan(planes_of(type), M, N, K);
   const size_t need = gemmq_linear_i8_grad_workspace(type, M, N, K);
   if (need == 0) return GEMMQ_E_SHAPE;
   rc = check_ws(ws, ws_bytes, need);
@@ -320,7 +329,9 @@ int gemmq_loss_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* X
 }
 
 size_t gemmq_loss_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
-  return N < 1 ? 0 : gemmq_linear_i8_grad_workspace(type, M, N, K);
+  if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0) return 0;
+  const GradPlan p = grad_plan(loss_planes(type, M), M, N, K);
+  return grad_shape_ok(M, K, p) ? p.bytes() + rest_bytes(p, M) : 0;
 }
 
 int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq,
@@ -338,9 +349,9 @@ int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8
   if (rc != GEMMQ_OK) return rc;
   if (!target || !lse || !dloss) return GEMMQ_E_INVALID_ARG;
   if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return GEMMQ_E_ALIGNMENT;
-  const GradPlan p = grad_plan(type, M, N, K);
+  const GradPlan p = grad_plan(loss_planes(type, M), M, N, K);
   if (!grad_shape_ok(M, K, p)) return GEMMQ_E_SHAPE;
-  rc = check_ws(ws, ws_bytes, p.bytes());
+  rc = check_ws(ws, ws_bytes, p.bytes() + rest_bytes(p, M));
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -348,11 +359,19 @@ int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8
   out.g = dloss;
   out.target = target;
   out.nvocab = N;
+  float* rest = nullptr;
+  if (rest_bytes(p, M)) {
+    rest = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.bytes());
+    out.rest = rest;
+    out.W = W;
+    out.ldw = ldw;
+  }
   return run_grad(p, W, ldw, out, M, N, K, ws, st,
                   [&](int64_t n0, int64_t n, uint16_t* P, int64_t pitch) {
                     const Operands op{W + n0 * ldw, sw + n0, Xq,     sx,    ldw,
                                       ldq,          (int)M,  (int)n, (int)K};
-                    return launch_factor(op, FactorOut{target, lse, P, pitch, n0, p.planes}, st);
+                    const FactorOut f{target, lse, P, pitch, n0, p.planes, rest};
+                    return launch_factor(op, f, st);
                   });
 }
 

@@ -23,6 +23,10 @@ enum Epilogue { kLinear, kLoss, kFactor };
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (bf16_t)v);
 }
+// what that rounding leaves of v, exactly
+__device__ __forceinline__ float bf16_rest(float v) {
+  return v - __builtin_bit_cast(float, bf16_bits(v) << 16);
+}
 __device__ __forceinline__ uint32_t f16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (_Float16)v);
 }

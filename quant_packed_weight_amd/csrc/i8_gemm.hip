@@ -406,11 +406,18 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
             v[i][r] = __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -l2));
         const int64_t tg = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
         if (tg >= 0 && tg < TN * 32) {
+          float less = 0.0f;
+          bool mine = false;
 #pragma unroll
           for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              if (tg == 32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) v[i][r] -= 1.0f;
+              if (tg == 32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) {
+                v[i][r] -= 1.0f;
+                less = v[i][r];
+                mine = true;
+              }
+          if (mine && a.fac.rest) a.fac.rest[m] = bf16_rest(less * swl[wn * TN * 32 + tg]);
         }
 #pragma unroll
         for (int i = 0; i < TN; ++i)
@@ -567,11 +574,14 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
   if (lane == 0) sums[wave] = sum;
   __syncthreads();
   if (t == 0) {
-    const float l2 = top + __builtin_log2f((sums[0] + sums[1]) + (sums[2] + sums[3]));
+    const float rest = __builtin_log2f((sums[0] + sums[1]) + (sums[2] + sums[3]));
     const int d = (dots[0] + dots[1]) + (dots[2] + dots[3]);
-    const float z = hit ? (float)d * op.sw[tg] * (op.sx[m] * kLog2e) : __builtin_nanf("");
-    lse[m] = l2 * kLn2;
-    loss[m] = tg < 0 ? 0.0f : (l2 - z) * kLn2;
+    lse[m] = (top + rest) * kLn2;
+    // the target's logit taken from the maximum before anything of the two's size is
+    // rounded: the sums are relative to exactly this maximum
+    const float below =
+        hit ? fmaf(-((float)d * op.sw[tg]), op.sx[m] * kLog2e, top) : __builtin_nanf("");
+    loss[m] = tg < 0 ? 0.0f : (below + rest) * kLn2;
   }
 }
 

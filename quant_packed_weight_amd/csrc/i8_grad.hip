@@ -78,12 +78,18 @@ __device__ __forceinline__ int aslot(int m, int chunk) { return chunk ^ ((m >> 1
 
 // four values of row m of the result, from column k on
 __device__ __forceinline__ void put_result(const GradOut& o, int64_t m, int k, int K, float4 v) {
+  const int64_t tg = o.target ? o.target[m] : 0;
+  if (o.rest && tg >= 0 && tg < o.nvocab) {
+    const float r = o.rest[m];
+    const int w = *reinterpret_cast<const int*>(o.W + tg * o.ldw + k);  // inside: pitch % 16 == 0
+    v = make_float4(fmaf(r, (float)(int8_t)w, v.x), fmaf(r, (float)(int8_t)(w >> 8), v.y),
+                    fmaf(r, (float)(int8_t)(w >> 16), v.z), fmaf(r, (float)(w >> 24), v.w));
+  }
   if (o.g) {
     const float f = o.g[m];
     v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
   }
   if (o.target) {
-    const int64_t tg = o.target[m];
     const float nan = __builtin_nanf("");
     if (tg < 0) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (tg >= o.nvocab) v = make_float4(nan, nan, nan, nan);

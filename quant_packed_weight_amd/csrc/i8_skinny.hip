@@ -205,6 +205,7 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
       float p = __builtin_amdgcn_exp2f(fmaf((float)s[e] * sw[e], s2, -l2));
       if (tg == e) p -= 1.0f;
       f[e] = e < count ? p * sw[e] : 0.0f;
+      if (tg == e && e < count && a.fac.rest) a.fac.rest[m] = bf16_rest(f[e]);
     }
     store_planes(a.fac.P + m * a.fac.pitch + n, (int64_t)op.M * a.fac.pitch, a.fac.planes, f);
   } else {

@@ -525,6 +525,27 @@ def test_loss_grad(M, N, K, dtype):
     assert torch.equal(gq.loss_i8_grad(w, sw, xq, sx, t, lse, gw, out_dtype=dtype), dx)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 2000, 256), (2, 3137, 768), (16, 16000, 100),
+                                   (17, 4000, 515), (70, 30000, 200), (300, 9000, 300)])
+def test_loss_grad_where_the_target_is_most_of_it(M, N, K):
+    # nearly equal logits: a row's factor is -1 at its target and about 1 / N elsewhere.
+    # The target's part is not rounded to bf16: beside the result's own rounding there
+    # is that of the others, whose sum over N random rows is about sqrt(N) / N of the
+    # target's, six times that where its scale is 0.2 and theirs 1.2: 0.14 of the result
+    # at most, whose rounding adds 0.14^2 / 2 = 1% to the result's own
+    w, sw, xq, sx, t = head(M, N, K, 31 * M + N)
+    sx = sx * 1e-3
+    z = (xq.double() * sx.double()[:, None]) @ (w.double() * sw.double()[:, None]).t()
+    lse = torch.logsumexp(z, 1)
+    p = torch.exp(z - lse[:, None])
+    p[torch.arange(M, device="cuda"), t] -= 1.0
+    ref = p @ (w.double() * sw.double()[:, None])
+    one = torch.ones(M, device="cuda")
+    dx = gq.loss_i8_grad(w, sw, xq, sx, t, lse.float(), one)
+    own = float((ref.bfloat16().double() - ref).norm())
+    assert float((dx.double() - ref).norm()) <= 1.05 * own
+
+
 def test_loss_grad_special_rows():
     for M in (6, 40, 150):
         w, sw, xq, sx, t = head(M, 1000, 96, M)
