@@ -56,6 +56,11 @@ size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 constexpr int64_t kFactorBytes = (int64_t)384 << 20;
 constexpr int64_t kMinPiece = 1024;
 
+// Up to eight rows of bf16 have two numbers for each value of the factor: one's
+// rounding errors have the fewest rows to even out in, and the product waits for W
+// more than for the matrix cores.
+int grad_planes(int type, int64_t M) { return type == GEMMQ_BF16 && M <= 8 ? 2 : planes_of(type); }
+
 struct GradPlan {
   int planes;
   GradSplit split;
@@ -141,9 +146,7 @@ int run_grad(const GradPlan& p, const int8_t* W, int64_t ldw, const GradOut& out
 // and exp(z - lse) of the likeliest others.  With one bf16 number each their few
 // roundings do not average out (M = 2 over 3137 x 768 2.8e-3 relative, the result's
 // own rounding 1.6e-3).  So what is left of the target's is kept, and added at the end
-// (2.3e-3), and up to eight rows, where chance has the least rows to even out and the
-// product waits for W more than for the matrix cores, have two numbers for each value.
-int loss_planes(int type, int64_t M) { return type == GEMMQ_BF16 && M <= 8 ? 2 : planes_of(type); }
+// (2.3e-3), and see grad_planes.
 size_t rest_bytes(const GradPlan& p, int64_t M) { return p.planes == 1 ? align_up(4 * M, 256) : 0; }
 
 GradOut grad_out(int type, void* dX, int64_t lddx) {
@@ -243,7 +246,7 @@ int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, co
 
 size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
   if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0) return 0;
-  const GradPlan p = grad_plan(planes_of(type), M, N, K);
+  const GradPlan p = grad_plan(grad_planes(type, M), M, N, K);
   if (!grad_shape_ok(M, K, p)) return 0;
   // whichever way dY's rows will allow
   if (type != GEMMQ_BF16 || N == 0 || M > kScaledMaxM) return p.bytes();
@@ -263,7 +266,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
   if (rc == GEMMQ_OK && N > 0) rc = check_i8(W, ldw, sw, K);
   if (rc == GEMMQ_OK && N > 0) rc = check_rows(type, dY, lddy, N);
   if (rc != GEMMQ_OK) return rc;
-  const GradPlan p = grad_plan(planes_of(type), M, N, K);
+  const GradPlan p = grad_plan(grad_planes(type, M), M, N, K);
   const size_t need = gemmq_linear_i8_grad_workspace(type, M, N, K);
   if (need == 0) return GEMMQ_E_SHAPE;
   rc = check_ws(ws, ws_bytes, need);
@@ -330,7 +333,7 @@ int gemmq_loss_i8(const int8_t* W, int64_t ldw, const float* sw, const int8_t* X
 
 size_t gemmq_loss_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K) {
   if (!known(type) || check_shape(M, N, K) != GEMMQ_OK || M == 0 || N == 0) return 0;
-  const GradPlan p = grad_plan(loss_planes(type, M), M, N, K);
+  const GradPlan p = grad_plan(grad_planes(type, M), M, N, K);
   return grad_shape_ok(M, K, p) ? p.bytes() + rest_bytes(p, M) : 0;
 }
 
@@ -349,7 +352,7 @@ int gemmq_loss_i8_grad(const int8_t* W, int64_t ldw, const float* sw, const int8
   if (rc != GEMMQ_OK) return rc;
   if (!target || !lse || !dloss) return GEMMQ_E_INVALID_ARG;
   if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return GEMMQ_E_ALIGNMENT;
-  const GradPlan p = grad_plan(loss_planes(type, M), M, N, K);
+  const GradPlan p = grad_plan(grad_planes(type, M), M, N, K);
   if (!grad_shape_ok(M, K, p)) return GEMMQ_E_SHAPE;
   rc = check_ws(ws, ws_bytes, p.bytes() + rest_bytes(p, M));
   if (rc == GEMMQ_OK) rc = check_device();

@@ -398,12 +398,14 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
         if (h == 0) red[wn * BM + ml] = make_float2(top == -__builtin_inff() ? top : z, sum);
       } else {
         if (!inside) continue;
-        const float l2 = a.fac.lse[m] * kLog2e;
+        // the difference first, in units of e and rounded once, then the change to base
+        // 2: lse log2 e rounded would put all of a row off by |lse| 2^-24
+        const float lse = a.fac.lse[m], sx1 = sx * sign;
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            v[i][r] = __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -l2));
+            v[i][r] = __builtin_amdgcn_exp2f(fmaf(v[i][r], sx1, -lse) * kLog2e);
         const int64_t tg = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
         if (tg >= 0 && tg < TN * 32) {
           float less = 0.0f;

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* dY, int64_t ldd
     // columns from N on are zero, not the product of what is read there with zero
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[r][e] = n + e < N ? v[r][e] * f[e] : 0.0f;
-    if (TYPE == GEMMQ_BF16) {
+    if (planes == 1) {
       *reinterpret_cast<uint4*>(to) =
           make_uint4(bf16_bits(v[r][0]) | bf16_bits(v[r][1]) << 16,
                      bf16_bits(v[r][2]) | bf16_bits(v[r][3]) << 16,

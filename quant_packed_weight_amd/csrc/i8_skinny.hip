@@ -197,12 +197,12 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
               fmaf((float)s[2] * sx, sw[2], b[2]), fmaf((float)s[3] * sx, sw[3], b[3]));
   } else if constexpr (EPI == kFactor) {
     if (!inside || n >= a.fac.pitch) return;  // the pitch is a multiple of 4
-    const float s2 = sx * kLog2e, l2 = a.fac.lse[m] * kLog2e;
+    const float lse = a.fac.lse[m];
     const int64_t tg = a.fac.target[m] - a.fac.n0 - n;
     float f[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float p = __builtin_amdgcn_exp2f(fmaf((float)s[e] * sw[e], s2, -l2));
+      float p = __builtin_amdgcn_exp2f(fmaf((float)s[e] * sw[e], sx, -lse) * kLog2e);
       if (tg == e) p -= 1.0f;
       f[e] = e < count ? p * sw[e] : 0.0f;
       if (tg == e && e < count && a.fac.rest) a.fac.rest[m] = bf16_rest(f[e]);
