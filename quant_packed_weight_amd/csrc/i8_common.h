@@ -100,6 +100,14 @@ __device__ __forceinline__ void wait_vm_if(bool most) {
   }
 }
 
+// exp(z - lse) - 1 at the target, z = sx sw dot.  Near certainty the difference is
+// small against z, whose rounding (half a step of sw dot) would be most of it: the
+// product's remainder is carried along, and nothing is subtracted from 1.
+__device__ __forceinline__ float target_factor(int dot, float sw, float sx, float lse) {
+  const float d = (float)dot, v = d * sw, left = fmaf(d, sw, -v);
+  return expm1f(fmaf(left, sx, fmaf(v, sx, -lse)));
+}
+
 // f[0..3] as `planes` matrices of bf16 parts, `plane` elements apart
 __device__ __forceinline__ void store_planes(uint16_t* p, int64_t plane, int planes, float (&f)[4]) {
   if (planes == 1) {

@@ -343,6 +343,26 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
       float s2 = sx * kLog2e;
       const float sign = s2 < 0.0f ? -1.0f : 1.0f;
       s2 *= sign;
+      // the factor's target among the lane's channels, and its sum, here where the sums
+      // are still at hand.  The asm keeps the comparisons one after another: all at
+      // once their masks do not fit the scalar registers.
+      int tg = -1, dot = 0;
+      if constexpr (EPI == kFactor) {
+        if (inside) {
+          const int64_t at = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
+          if (at >= 0 && at < TN * 32) tg = (int)at;
+        }
+        tg = (tg >> 2 & 1) == h ? tg - 4 * h : -1;
+        if (tg >= 0) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              dot = tg == 32 * i + 8 * (r >> 2) + (r & 3) ? acc[i][j][r] : dot;
+              if ((r & 3) == 3) asm volatile("" : "+v"(tg), "+v"(dot));
+            }
+        }
+      }
       float v[TN][16];
 #pragma unroll
       for (int i = 0; i < TN; ++i)
@@ -406,20 +426,16 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             v[i][r] = __builtin_amdgcn_exp2f(fmaf(v[i][r], sx1, -lse) * kLog2e);
-        const int64_t tg = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
-        if (tg >= 0 && tg < TN * 32) {
-          float less = 0.0f;
-          bool mine = false;
+        if (tg >= 0) {
+          const float sw = swl[nw + tg], less = target_factor(dot, sw, sx, lse);
 #pragma unroll
           for (int i = 0; i < TN; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (tg == 32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) {
-                v[i][r] -= 1.0f;
-                less = v[i][r];
-                mine = true;
-              }
-          if (mine && a.fac.rest) a.fac.rest[m] = bf16_rest(less * swl[wn * TN * 32 + tg]);
+            for (int r = 0; r < 16; ++r) {
+              v[i][r] = tg == 32 * i + 8 * (r >> 2) + (r & 3) ? less : v[i][r];
+              if ((r & 3) == 3) asm volatile("" : "+v"(tg));
+            }
+          if (a.fac.rest) a.fac.rest[m] = bf16_rest(less * sw);
         }
 #pragma unroll
         for (int i = 0; i < TN; ++i)

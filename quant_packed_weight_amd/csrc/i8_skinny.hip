@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float p = __builtin_amdgcn_exp2f(fmaf((float)s[e] * sw[e], sx, -lse) * kLog2e);
-      if (tg == e) p -= 1.0f;
+      if (tg == e) p = target_factor(s[e], sw[e], sx, lse);
       f[e] = e < count ? p * sw[e] : 0.0f;
       if (tg == e && e < count && a.fac.rest) a.fac.rest[m] = bf16_rest(f[e]);
     }

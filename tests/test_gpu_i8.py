@@ -546,6 +546,35 @@ def test_loss_grad_where_the_target_is_most_of_it(M, N, K):
     assert float((dx.double() - ref).norm()) <= 1.05 * own
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 2112, 698), (16, 3000, 512), (40, 5000, 300)])
+def test_loss_grad_near_certainty(M, N, K):
+    # The target's factor is -(1 - p) with 1 - p well below the rounding of its logit;
+    # the sum of the others' as large.  z - lse is off by the rounding of its difference
+    # (u of it), so the factor by a few u and by the expansion; the others' by u |z| each.
+    # What the two of them leave is small against the result where W's rows differ.
+    g = gen(M + N)
+    w, sw = i8(N, K, g), scales(N, g, K ** -0.5 / 64)
+    t = torch.arange(M, device="cuda") * 7
+    xq, sx = gq.quantize_i8(w[t].float())
+    z = (xq.double() * sx.double()[:, None]) @ (w.double() * sw.double()[:, None]).t()
+    gap = z.gather(1, t[:, None])[:, 0] - z.scatter(1, t[:, None], -math.inf).amax(1)
+    sx = (sx.double() * (8.0 / gap)).float()  # the target's logit 8 above the next
+    z = (xq.double() * sx.double()[:, None]) @ (w.double() * sw.double()[:, None]).t()
+    lse = torch.logsumexp(z, 1).float()
+    rows = torch.arange(M, device="cuda")
+    p = torch.exp(z - lse.double()[:, None])
+    p[rows, t] = torch.expm1(z[rows, t] - lse.double())
+    wd = w.double() * sw.double()[:, None]
+    ref = p @ wd
+    dx = gq.loss_i8_grad(w, sw, xq, sx, t, lse, torch.ones(M, device="cuda"),
+                         out_dtype=torch.float32)
+    tol = (p.abs() * (4 * U + 2 * U * (z.abs() + 1) * (p > 0) + (3 * N + 70) * U)) @ wd.abs()
+    tol = tol + 4 * U * (z[rows, t] - lse.double()).abs()[:, None] * wd[t].abs()
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+    # the target's own logit adds nothing of its size
+    assert float((dx.double() - ref).norm()) <= 64 * U * float(ref.norm())
+
+
 def test_loss_grad_special_rows():
     for M in (6, 40, 150):
         w, sw, xq, sx, t = head(M, 1000, 96, M)
