@@ -326,7 +326,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
 // the pitch.  A workgroup takes 2048 columns of ROWS rows, a thread eight of each:
 // four rows where there are many (2048 x 12288 bf16: 21 us, one row 54), one
 // where few would leave the chip idle (77 x 1037 f32: 5 us, four rows 9).
-template <int TYPE, int ROWS>
+template <int TYPE, int ROWS, bool ONE>
 __global__ __launch_bounds__(256) void planes_kernel(const void* dY, int64_t lddy, bool wide,
                                                      const float* sw, uint16_t* P, int64_t pitch,
                                                      int planes, int M, int N) {
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* dY, int64_t ldd
     // columns from N on are zero, not the product of what is read there with zero
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[r][e] = n + e < N ? v[r][e] * f[e] : 0.0f;
-    if (planes == 1) {
+    if constexpr (ONE) {
       *reinterpret_cast<uint4*>(to) =
           make_uint4(bf16_bits(v[r][0]) | bf16_bits(v[r][1]) << 16,
                      bf16_bits(v[r][2]) | bf16_bits(v[r][3]) << 16,
@@ -522,17 +522,21 @@ int launch_grad(const GradArgs& a, hipStream_t st) {
 
 int launch_planes(int type, const void* dY, int64_t lddy, const float* sw, uint16_t* P,
                   int64_t pitch, int planes, int M, int N, hipStream_t st) {
-  const bool many = M * pitch >= (int64_t)1 << 22, wide = wide_rows(dY, lddy, type);
+  // (bf16 in two planes: up to eight rows)
+  const bool many = M * pitch >= (int64_t)1 << 22 && (type != GEMMQ_BF16 || planes == 1);
+  const bool wide = wide_rows(dY, lddy, type);
   const dim3 grid = rows_grid(ceil_div(pitch, 2048), many ? ceil_div(M, 4) : M);
   const auto run = [&](auto kernel) {
     kernel<<<grid, 256, 0, st>>>(dY, lddy, wide, sw, P, pitch, planes, M, N);
   };
   if (type == GEMMQ_F32)
-    many ? run(planes_kernel<GEMMQ_F32, 4>) : run(planes_kernel<GEMMQ_F32, 1>);
-  else if (type == GEMMQ_BF16)
-    many ? run(planes_kernel<GEMMQ_BF16, 4>) : run(planes_kernel<GEMMQ_BF16, 1>);
-  else
-    many ? run(planes_kernel<GEMMQ_F16, 4>) : run(planes_kernel<GEMMQ_F16, 1>);
+    many ? run(planes_kernel<GEMMQ_F32, 4, false>) : run(planes_kernel<GEMMQ_F32, 1, false>);
+  else if (type == GEMMQ_F16)
+    many ? run(planes_kernel<GEMMQ_F16, 4, false>) : run(planes_kernel<GEMMQ_F16, 1, false>);
+  else if (planes == 1)
+    many ? run(planes_kernel<GEMMQ_BF16, 4, true>) : run(planes_kernel<GEMMQ_BF16, 1, true>);
+  else  // few rows
+    run(planes_kernel<GEMMQ_BF16, 1, false>);
   return 0;
 }
 
