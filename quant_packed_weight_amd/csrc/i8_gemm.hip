@@ -349,8 +349,9 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
       int tg = -1, dot = 0;
       if constexpr (EPI == kFactor) {
         if (inside) {
-          const int64_t at = a.fac.target[m] - a.fac.n0 - n0 - wn * TN * 32;
-          if (at >= 0 && at < TN * 32) tg = (int)at;
+          // (one past the operands' rows is a later piece's, or no token's)
+          const int64_t in = a.fac.target[m] - a.fac.n0, at = in - n0 - wn * TN * 32;
+          if (at >= 0 && at < TN * 32 && in < op.N) tg = (int)at;
         }
         tg = (tg >> 2 & 1) == h ? tg - 4 * h : -1;
         if (tg >= 0) {
