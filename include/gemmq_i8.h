@@ -113,9 +113,10 @@ size_t gemmq_linear_i8_grad_workspace(int type, int64_t M, int64_t N, int64_t K)
  * matrix cores with the weights exact in bf16 and dY * sw, an f32 product,
  * written as a sum of bf16 numbers: one for GEMMQ_BF16 (8 bits, the precision
  * of dY itself; two up to M == 8), two for GEMMQ_F16 (16 bits), three for
- * GEMMQ_F32 (24 bits, all of an f32); the sums are f32.  For up to 128 rows of GEMMQ_BF16 with N a
- * multiple of 8 and rows on 16 bytes, dY enters as it is and sw * W is rounded
- * to bf16 instead: the same number of roundings, another of the two factors.
+ * GEMMQ_F32 (24 bits, all of an f32); the sums are f32.  For 9 to 128 rows of
+ * GEMMQ_BF16 with N a multiple of 8 and rows on 16 bytes, dY enters as it is and
+ * sw * W is rounded to bf16 instead: the same number of roundings, another of the
+ * two factors.
  *   type   of dY and dX.   dY, lddy  [M, N].   dX, lddx  [M, K], overwritten.
  * N == 0 writes zeros.
  * Errors: as gemmq_quantize_i8, and GEMMQ_E_INVALID_ARG for a workspace that is

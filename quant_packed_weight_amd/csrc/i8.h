@@ -123,7 +123,8 @@ struct GradArgs {
   int M, N, K, planes;
   int tile, splits;    // of grad_split
   bool add;            // add to what acc holds (a later piece)
-  const float* sw;     // not null (M <= 128): W's rows are scaled by it
+  const float* sw;     // not null (M <= 128): scales W's rows, or with two planes (M <= 8)
+                       // the caller's matrix, as two bf16 numbers
   GradOut out;
 };
 struct GradSplit {

@@ -56,9 +56,10 @@ size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 constexpr int64_t kFactorBytes = (int64_t)384 << 20;
 constexpr int64_t kMinPiece = 1024;
 
-// Up to eight rows of bf16 have two numbers for each value of the factor: one's
-// rounding errors have the fewest rows to even out in, and the product waits for W
-// more than for the matrix cores.
+// Up to eight rows of bf16 have two numbers for each value of the factor, in the
+// workspace or, where dY is read as it lies, in the product's LDS: one's rounding errors
+// have the fewest rows to even out in, and the product waits for W more than for the
+// matrix cores.
 int grad_planes(int type, int64_t M) { return type == GEMMQ_BF16 && M <= 8 ? 2 : planes_of(type); }
 
 struct GradPlan {
@@ -93,7 +94,7 @@ bool grad_shape_ok(int64_t M, int64_t K, const GradPlan& p) {
 
 // Up to 128 tokens a bf16 dY whose rows allow 16-byte loads is read by the product as
 // it lies, and W scaled by sw instead (a rounding of sw * w to bf16 in the place of
-// one of dy * sw): no factor in the workspace, and a launch less (4096 x 4096 at M =
+// one of dy * sw; up to eight tokens dY is scaled, with no rounding to one): no factor in the workspace, and a launch less (4096 x 4096 at M =
 // 16 15 -> 12 us, M = 128 29 -> 26).  With more tokens the large tiles are the faster
 // ones, whose conversion has no room for the scaling: with the factor / as it lies M =
 // 129 over 2048 x 2048 15.4 / 14.3 us, 4096 x 12288 39 / 50, M = 512 68 / 82.
@@ -106,10 +107,10 @@ bool reads_dy(int type, const void* dY, int64_t lddy, int64_t M, int64_t N) {
 
 GradPlan direct_plan(int64_t M, int64_t N, int64_t K) {
   GradPlan p;
-  p.planes = 1;
+  p.planes = grad_planes(GEMMQ_BF16, M);
   p.piece = N;
   p.kp = (int64_t)align_up(K, 4);
-  p.split = grad_split((int)M, (int)N, (int)K, 1, true);
+  p.split = grad_split((int)M, (int)N, (int)K, p.planes, true);
   p.direct = p.split.splits == 1;
   p.factor_bytes = 0;
   p.acc_bytes = p.direct ? 0 : align_up(4 * p.split.splits * M * p.kp, 256);
@@ -281,7 +282,7 @@ int gemmq_linear_i8_grad(const int8_t* W, int64_t ldw, const float* sw, int type
                      static_cast<const uint16_t*>(dY), lddy,
                      acc,       d.kp,
                      (int)M,    (int)N,
-                     (int)K,    1,
+                     (int)K,    d.planes,
                      d.split.tile, d.split.splits,
                      false,     sw,
                      out};

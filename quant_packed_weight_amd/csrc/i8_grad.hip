@@ -1,7 +1,8 @@
 // i8_grad.hip -- the product that both gradients need, acc[m, k] = sum_n
 // A[m, n] W[n, k]: int8 weights, exact in bf16, against a factor A given as one
-// to three bf16 matrices whose sum it is, or weights scaled and rounded to bf16
-// against the caller's own bf16 rows; and the kernels before and after it.
+// to three bf16 matrices whose sum it is, or as the caller's own bf16 rows, which sw
+// scales here: the weights, rounded to bf16, or for few rows A itself, in two numbers;
+// and the kernels before and after it.
 //
 // W is read as it lies, rows of N along the reduction: the transposing LDS read
 // hands each lane the eight consecutive n of its own k, which are converted to
@@ -59,6 +60,14 @@ __device__ __forceinline__ uint32_t widen_part(v2i w, const float (&s)[8], int e
   }
 }
 
+// How the factor A comes: kPlanes, PLANES matrices in the workspace.  The others are the
+// caller's own matrix of bf16, N a multiple of 8: kScaledW, W's rows are scaled by sw as
+// they are converted, and rounded once; kScaledA, A is, up to kSplitRows rows of it, as
+// PLANES numbers that take the place of a step's rows once these are in LDS (M = 8, 4096 x
+// 4096 11.5 us, N = 12288 20.1; W scaled 10.9 and 18.0, two matrices in memory 14.1 and 21.0).
+constexpr int kSplitRows = 8;
+enum Form { kPlanes, kScaledW, kScaledA };
+
 template <int BK, int BM, int PLANES>
 struct GradStage {
   static constexpr int kW = 0, kA = kRed * BK, kPlane = BM * 2 * kRed;
@@ -103,18 +112,20 @@ constexpr int kWavesPerSimd =
     WAVES <= 4 && DEPTH * GradStage<BK, BM, PLANES>::kBytes > 81920 ? 1 : 2;
 
 // All PLANES planes in a step: W's tile is read and converted once for them (M =
-// 2048, 4096 x 4096 in f32 152 us, one plane after another 188).  SCALED: the factor
-// is a bf16 matrix of the caller's, N a multiple of 8, and W's rows are scaled by sw
-// as they are converted.
-template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES, bool SCALED>
+// 2048, 4096 x 4096 in f32 152 us, one plane after another 188).
+template <int BK, int BM, int WK, int WM, int DEPTH, int PLANES, Form FORM>
 __global__ __launch_bounds__(64 * WK * WM, (kWavesPerSimd<BK, BM, WK * WM, DEPTH, PLANES>)) void
 grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
+  constexpr bool SCALED = FORM != kPlanes;
+  constexpr int kIn = SCALED ? 1 : PLANES;  // matrices that are loaded
   constexpr int NW = WK * WM;
   constexpr int TK = BK / WK / 32, TM = BM / WM / 32;
+  static_assert(FORM != kScaledW || PLANES == 1, "the caller's matrix is one");
+  static_assert(FORM != kScaledA || 64 * NW == kSplitRows * kRed / 2, "two values a thread");
   using S = GradStage<BK, BM, PLANES>;
   constexpr int kRowsPer = 1024 / BK;  // rows of W per load
   constexpr int kLw = kRed / kRowsPer / NW, kLa = BM / 8 / NW;
-  constexpr int kLoads = kLw + PLANES * kLa + (SCALED ? 1 : 0);
+  constexpr int kLoads = kLw + kIn * kLa + (SCALED ? 1 : 0);
   static_assert(kLw * kRowsPer * NW == kRed && kLa * 8 * NW == BM && NW % 2 == 0,
                 "every wave issues the same loads");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[DEPTH * S::kBytes];
@@ -195,12 +206,12 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   v2i wraw[2][TK];
   v8bf af[2][PLANES * TM];
   constexpr int kU = PLANES * TM;  // products of a fragment of W
-  constexpr int kReads = TK + kU + (SCALED ? 2 : 0), kProducts = TK * kU;
+  constexpr int kReads = TK + kU + (FORM == kScaledW ? 2 : 0), kProducts = TK * kU;
   constexpr int kPerProduct = (2 * kReads + kProducts - 1) / kProducts;
   const int h = lane >> 5;
   float sc[2][8];
   auto read = [&](int stage, int q, int r) {
-    if (SCALED && r >= TK + kU) {
+    if (FORM == kScaledW && r >= TK + kU) {
       const int x = r - TK - kU;
       const float4 v = *reinterpret_cast<const float4*>(
           swl + (stage * NW + wave) * kRed + 16 * q + 8 * h + 4 * x);
@@ -228,7 +239,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
   auto convert = [&](int set, int q, int i, int u) {
 #pragma unroll
     for (int e = 4 * u / kU; e < 4 * (u + 1) / kU; ++e)
-      wf[set][e] = (int)widen_part<SCALED>(wraw[q & 1][i], sc[q & 1], e);
+      wf[set][e] = (int)widen_part<FORM == kScaledW>(wraw[q & 1][i], sc[q & 1], e);
   };
   auto quarter = [&](int q, int from, uint32_t take, uint32_t to) {
 #pragma unroll
@@ -264,7 +275,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
     ++next;
   }
   // the factor's columns from N on, in the last step of all
-  const bool tail = SCALED && a.N % kRed && first + its == steps;
+  const bool tail = FORM == kScaledW && a.N % kRed && first + its == steps;
   auto clear_tail = [&](int stage) {
     for (int i = t; i < BM * 8; i += 64 * NW) {
       const int row = i >> 3, c = i & 7;
@@ -274,10 +285,28 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
     }
     gk::lds_barrier();
   };
+  // kScaledA: the factor's rows of step `step`, in place of the caller's; zero from N on
+  auto split_rows = [&](int stage, int step) {
+    const int row = t / (kRed / 2), n = 2 * (t % (kRed / 2));
+    uint8_t* p = lds + stage * S::kBytes + S::kA + row * 2 * kRed + 16 * aslot(row, n >> 3) +
+                 2 * (n & 7);
+    const uint32_t raw = *reinterpret_cast<const uint32_t*>(p);
+    const float2 s = *reinterpret_cast<const float2*>(swl + (stage * NW + wave) * kRed + n);
+    const bool in = (int64_t)step * kRed + n < a.N;  // (N is even)
+    float v0 = in ? __builtin_bit_cast(float, raw << 16) * s.x : 0.0f;
+    float v1 = in ? __builtin_bit_cast(float, raw & 0xffff0000u) * s.y : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) {
+      const uint32_t b = bf16_part(v0, i + 1 == PLANES);
+      *reinterpret_cast<uint32_t*>(p + i * S::kPlane) = b | bf16_part(v1, i + 1 == PLANES) << 16;
+    }
+    gk::lds_barrier();
+  };
   if (its > 0) {
     wait_vm_if<(DEPTH - 1) * kLoads>(its >= DEPTH);
     gk::lds_barrier();
     if (tail && its == 1) clear_tail(0);
+    if constexpr (FORM == kScaledA) split_rows(0, first);
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, 0, r);
 #pragma unroll
@@ -291,6 +320,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
     wait_vm_if<(DEPTH - 2) * kLoads>(it + DEPTH - 1 < its);
     gk::lds_barrier();
     if (tail && it + 2 == its) clear_tail(nbuf);
+    if (FORM == kScaledA && it + 1 < its) split_rows(nbuf, first + it + 1);
     quarter(3, nbuf, it + DEPTH < its, lds0 + buf * S::kBytes);
     ++next;
     buf = nbuf;
@@ -451,12 +481,12 @@ int64_t tiles(const Tile& c, int M, int K) { return ceil_div(M, c.bm) * ceil_div
 //   three       M 1500 N 2560 K 5008     -   [92]    114   118
 //               M 64 N 12288 K 4096      -     38     41   [30]   31
 // The two widest would be more than half empty up to 128 tokens, the lowest reads W
-// too often beyond.  A range has at least one step.
+// too often beyond; up to 8 it is the fastest of the three.  A range has at least one step.
 GradSplit grad_split(int M, int N, int K, int planes, bool whole) {
   const int64_t steps = ceil_div(N < 1 ? 1 : N, kRed);
   GradSplit best{0, 0};
   double least = 0.0;
-  for (int i = M <= 128 ? 2 : 0; i <= (M <= 128 ? 4 : 3); ++i) {
+  for (int i = M <= 8 ? 4 : M <= 128 ? 2 : 0; i <= (M <= 128 ? 4 : 3); ++i) {
     const float* step = kTiles[i].step[planes - 1];
     if (!(step[0] > 0.0f)) continue;
     const int64_t n = tiles(kTiles[i], M, K);
@@ -491,31 +521,32 @@ int launch_grad(const GradArgs& a, hipStream_t st) {
   if (!grid_fits(n, kMaxThreads)) return -1;
   const dim3 grid((uint32_t)n);
   const auto run = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, st>>>(a, kt, mt); };
-  // with sw: up to 128 tokens, in the lower three tiles
+  // with sw: up to 128 tokens, in the lower three tiles; two planes up to 8, in the lowest
   switch (a.tile) {
-    case 0: run(grad_kernel<256, 256, 4, 2, 3, 1, false>, 512); break;
+    case 0: run(grad_kernel<256, 256, 4, 2, 3, 1, kPlanes>, 512); break;
     case 1:
-      a.planes == 1   ? run(grad_kernel<256, 128, 4, 2, 2, 1, false>, 512)
-      : a.planes == 2 ? run(grad_kernel<256, 128, 4, 2, 3, 2, false>, 512)
-                      : run(grad_kernel<256, 128, 4, 2, 2, 3, false>, 512);
+      a.planes == 1   ? run(grad_kernel<256, 128, 4, 2, 2, 1, kPlanes>, 512)
+      : a.planes == 2 ? run(grad_kernel<256, 128, 4, 2, 3, 2, kPlanes>, 512)
+                      : run(grad_kernel<256, 128, 4, 2, 2, 3, kPlanes>, 512);
       break;
     case 2:
-      a.sw            ? run(grad_kernel<128, 128, 2, 2, 3, 1, true>, 256)
-      : a.planes == 1 ? run(grad_kernel<128, 128, 2, 2, 3, 1, false>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 2, 2, false>, 256)
-                      : run(grad_kernel<128, 128, 2, 2, 2, 3, false>, 256);
+      a.sw            ? run(grad_kernel<128, 128, 2, 2, 3, 1, kScaledW>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 128, 2, 2, 3, 1, kPlanes>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 128, 2, 2, 2, 2, kPlanes>, 256)
+                      : run(grad_kernel<128, 128, 2, 2, 2, 3, kPlanes>, 256);
       break;
     case 3:
-      a.sw            ? run(grad_kernel<128, 64, 2, 2, 3, 1, true>, 256)
-      : a.planes == 1 ? run(grad_kernel<128, 64, 2, 2, 3, 1, false>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 64, 2, 2, 3, 2, false>, 256)
-                      : run(grad_kernel<128, 64, 2, 2, 2, 3, false>, 256);
+      a.sw            ? run(grad_kernel<128, 64, 2, 2, 3, 1, kScaledW>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 64, 2, 2, 3, 1, kPlanes>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 64, 2, 2, 3, 2, kPlanes>, 256)
+                      : run(grad_kernel<128, 64, 2, 2, 2, 3, kPlanes>, 256);
       break;
     default:
-      a.sw            ? run(grad_kernel<128, 32, 4, 1, 3, 1, true>, 256)
-      : a.planes == 1 ? run(grad_kernel<128, 32, 4, 1, 3, 1, false>, 256)
-      : a.planes == 2 ? run(grad_kernel<128, 32, 4, 1, 3, 2, false>, 256)
-                      : run(grad_kernel<128, 32, 4, 1, 3, 3, false>, 256);
+      a.sw            ? a.planes == 1 ? run(grad_kernel<128, 32, 4, 1, 3, 1, kScaledW>, 256)
+                                      : run(grad_kernel<128, 32, 4, 1, 3, 2, kScaledA>, 256)
+      : a.planes == 1 ? run(grad_kernel<128, 32, 4, 1, 3, 1, kPlanes>, 256)
+      : a.planes == 2 ? run(grad_kernel<128, 32, 4, 1, 3, 2, kPlanes>, 256)
+                      : run(grad_kernel<128, 32, 4, 1, 3, 3, kPlanes>, 256);
   }
   return 0;
 }

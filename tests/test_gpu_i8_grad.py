@@ -152,3 +152,38 @@ def test_loss_grad_in_several_pieces(dtype, M, N, K, even):
         own = (ref.bfloat16().double() - ref).norm()
         assert float((dx - ref).norm() / own) <= 1.05
     assert torch.equal(gq.loss_i8_grad(w, sw, xq, sx, t, lse.float(), gw, out_dtype=dtype)[keep].double(), dx)
+
+
+# ------------------------------------------------------------------ bf16 rows as they lie
+@pytest.mark.parametrize("M", [1, 2, 5, 8])
+@pytest.mark.parametrize("N,K", [(8, 40), (64, 128), (520, 1000), (1000, 515), (4104, 300), (72, 20000),
+                                 (12296, 515), (20000, 130)])
+@pytest.mark.parametrize("aligned", [True, False], ids=["aligned", "odd"])
+def test_linear_grad_of_few_rows_rounds_once(M, N, K, aligned):
+    # dy sw is two bf16 numbers up to eight rows, however dy lies: 2^-16 of each value is
+    # left at most, beside which the result's own rounding, 2^-9.3 in the norm, is all
+    g = gen(5 * M + N + K)
+    w, sw = i8(N, K, g, full=True), scales(N, g, 0.01)
+    dy = torch.zeros((M, N + (8 if aligned else 1)), dtype=BF16, device="cuda")[:, :N]
+    dy.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    out = Guarded(M, K, BF16, extra=N % 4)
+    dx = gq.linear_i8_grad(w, sw, dy, out=out.t)
+    torch.cuda.synchronize()
+    out.check()
+    ref = (dy.double() * sw.double()) @ w.double()
+    mag = (dy.double() * sw.double()).abs() @ w.double().abs()
+    tol = ((1 + 2 * N + 64) * U + 2.0 ** -16) * mag
+    assert bool(((dx.double() - ref).abs() <= tol + HALF[BF16] * (ref.abs() + tol)).all())
+    # a value may lie near the middle of two bf16 numbers: 2^-16 sqrt(N) random parts of
+    # the result's size sqrt(N) move the error's norm by 2^-13 of the result's at most
+    own = float((ref.bfloat16().double() - ref).norm())
+    assert float((dx.double() - ref).norm()) <= own + 2.0 ** -13 * float(ref.norm())
+    dy[0, N - 1] = math.inf
+    if M > 1:
+        dy[1, 0] = math.nan
+    dz = gq.linear_i8_grad(w, sw, dy)
+    # an infinity stays one where the weight is not zero
+    want = torch.where(w[N - 1] == 0, math.nan, w[N - 1].double() * math.inf)
+    assert torch.equal(dz[0].double().nan_to_num(7.0), want.nan_to_num(7.0))
+    assert M == 1 or bool(torch.isnan(dz[1]).all())
+    assert torch.equal(dz[2:], dx[2:])
