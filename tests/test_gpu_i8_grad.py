@@ -187,3 +187,37 @@ def test_linear_grad_of_few_rows_rounds_once(M, N, K, aligned):
     assert torch.equal(dz[0].double().nan_to_num(7.0), want.nan_to_num(7.0))
     assert M == 1 or bool(torch.isnan(dz[1]).all())
     assert torch.equal(dz[2:], dx[2:])
+
+
+# The taller tiles of the product that scales W (by 64 and 128 tokens): several ranges and
+# one, a last step of eight columns (N % 64 == 8) and whole ones, K off the tile's 128
+@pytest.mark.parametrize("M,N,K", [(128, 12288, 4096), (96, 4096, 4096), (100, 8200, 2050),
+                                   (128, 20000, 1030), (65, 4104, 11000), (100, 72, 20000),
+                                   (128, 8, 20000), (64, 4104, 11000), (33, 8200, 2050),
+                                   (128, 12296, 515), (64, 72, 20000), (100, 1032, 9000)])
+def test_linear_grad_of_aligned_rows_in_taller_tiles(M, N, K):
+    g = gen(M + N + K)
+    w, sw = i8(N, K, g, full=True), scales(N, g, 0.01)
+    wide = torch.full((M, N + 8 * (M % 3)), math.nan, dtype=BF16, device="cuda")
+    dy = wide[:, :N]
+    dy.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    need = gq.linear_i8_grad_workspace(BF16, M, N, K)
+    ws = torch.full((need + 64,), 173, dtype=torch.uint8, device="cuda")
+    out = Guarded(M, K, BF16, extra=N % 3)
+    dx = gq.linear_i8_grad(w, sw, dy, out=out.t, workspace=ws[:need])
+    torch.cuda.synchronize()
+    out.check()
+    assert bool((ws[need:] == 173).all())
+    a = dy.double() * sw.double()
+    ref = a @ w.double()
+    mag = a.abs() @ w.double().abs()
+    # as in test_linear_grad_of_aligned_rows
+    tol = ((2 + N + 64) * U + 2.0 ** -8) * mag
+    tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+    # one rounding of sw w, whose parts of N values average out, and one of the result
+    assert float((dx.double() - ref).norm() / ref.norm()) <= norm_error(BF16, M, N)
+    dy[1, N - 1], dy[2, 0] = math.nan, math.inf
+    dz = gq.linear_i8_grad(w, sw, dy)
+    assert bool(torch.isnan(dz[1]).all()) and not bool(torch.isfinite(dz[2]).any())
+    assert torch.equal(dz[3:], dx[3:]) and torch.equal(dz[0], dx[0])
