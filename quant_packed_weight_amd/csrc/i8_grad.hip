@@ -283,6 +283,9 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
         *reinterpret_cast<v4i*>(lds + stage * S::kBytes + S::kA + row * 2 * kRed +
                                 16 * aslot(row, c)) = (v4i){0, 0, 0, 0};
     }
+    // and the scales that stand there, the last one's copies, which may be infinite
+    for (int i = t; i < NW * kRed; i += 64 * NW)
+      if (i % kRed >= a.N % kRed) swl[stage * NW * kRed + i] = 0.0f;
     gk::lds_barrier();
   };
   // kScaledA: the factor's rows of step `step`, in place of the caller's; zero from N on

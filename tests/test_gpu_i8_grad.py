@@ -221,3 +221,19 @@ def test_linear_grad_of_aligned_rows_in_taller_tiles(M, N, K):
     dz = gq.linear_i8_grad(w, sw, dy)
     assert bool(torch.isnan(dz[1]).all()) and not bool(torch.isfinite(dz[2]).any())
     assert torch.equal(dz[3:], dx[3:]) and torch.equal(dz[0], dx[0])
+
+
+@pytest.mark.parametrize("M", [3, 20, 60, 128, 200])
+@pytest.mark.parametrize("N,K", [(72, 130), (72, 20000), (200, 515), (4104, 300)])
+@pytest.mark.parametrize("extra", [0, 1])
+def test_linear_grad_with_an_infinite_last_scale(M, N, K, extra):
+    # the last channel's scale belongs to no column past it, where the factor is zero
+    g = gen(M + N)
+    w, sw = i8(N, K, g, full=True), scales(N, g, 0.01)
+    sw[N - 1] = math.inf
+    dy = torch.zeros((M, N + extra), dtype=BF16, device="cuda")[:, :N]
+    dy.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    dx = gq.linear_i8_grad(w, sw, dy).double()
+    # infinite with the sign of dy w in the last channel; NaN where either is zero
+    ref = (dy[:, N - 1:].double() * math.inf) * w[N - 1].double()
+    assert torch.equal(dx.nan_to_num(7.0), ref.nan_to_num(7.0))
