@@ -100,11 +100,21 @@ __device__ __forceinline__ void wait_vm_if(bool most) {
   }
 }
 
+// v = sw dot as the epilogues have it, in f32 from dot in f32, and what its two roundings
+// leave: sw dot = v + left, to f32 precision of left.  (|dot| <= 2^31 - 2^14, so dot in f32
+// is an int32 too, and dot less it, at most 64, an f32.)
+__device__ __forceinline__ float scaled(int dot, float sw, float& left) {
+  const float d = (float)dot, v = d * sw;
+  left = fmaf((float)(dot - (int)d), sw, fmaf(d, sw, -v));
+  return v;
+}
+
 // exp(z - lse) - 1 at the target, z = sx sw dot.  Near certainty the difference is
 // small against z, whose rounding (half a step of sw dot) would be most of it: the
 // product's remainder is carried along, and nothing is subtracted from 1.
 __device__ __forceinline__ float target_factor(int dot, float sw, float sx, float lse) {
-  const float d = (float)dot, v = d * sw, left = fmaf(d, sw, -v);
+  float left;
+  const float v = scaled(dot, sw, left);
   return expm1f(fmaf(left, sx, fmaf(v, sx, -lse)));
 }
 
