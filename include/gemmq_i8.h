@@ -134,7 +134,7 @@ size_t gemmq_loss_i8_workspace(int64_t M, int64_t N, int64_t K);
  * z[m, n] = sx[m] * sw[n] * sum_k Xq[m, k] * W[n, k] never written to memory:
  *   lse[m]  = log sum_n exp(z[m, n])
  *   loss[m] = lse[m] - z[m, target[m]]
- * target[m] < 0 (an ignored position): loss[m] = 0, lse[m] as always.
+ * target[m] < 0 (an ignored position): loss[m] = 0, lse[m] as always, to a rounding.
  * target[m] >= N: loss[m] = NaN.  N >= 1 (GEMMQ_E_SHAPE otherwise).
  *   target  int64 [M], 8-byte aligned.   loss, lse  f32 [M], overwritten.
  * Errors: as gemmq_linear_i8_grad.

@@ -53,8 +53,8 @@ struct LinearOut {
   bool lines;  // of 16 bits, and eight may
 };
 
-// Softmax statistics per column tile: (max, sum of exp2(z - max)) of the base-2
-// logits of row m in tile t at part[m * ntiles + t].
+// Softmax statistics per column tile: of row m in tile t, with v = sw I and the sign of
+// sx, (max v, sum of exp(|sx| (v - max v))) at part[m * ntiles + t].
 struct LossOut {
   const int64_t* target;
   float2* part;

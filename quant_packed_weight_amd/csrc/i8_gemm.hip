@@ -109,10 +109,11 @@ __device__ __forceinline__ v2u swap_halves(uint32_t a, uint32_t b) {
   return (v2u){r[0], r[1]};
 }
 
-// (max, sum) of one part of a row, the sum taken relative to the row's maximum
-__device__ __forceinline__ float join_term(float2 p, float top) {
+// (max, sum) of one part of a row, the sum taken relative to the row's maximum; s2 as
+// where the parts were made
+__device__ __forceinline__ float join_term(float2 p, float top, float s2) {
   // a part without columns is (-inf, 0)
-  return p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - top);
+  return p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f((p.x - top) * s2);
 }
 
 // GROUPS groups of WN x WM waves compute the tile, group g the steps g, g + GROUPS,
@@ -390,14 +391,16 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
               if (n0 + nw + 32 * i + 8 * (r >> 2) + (r & 3) >= op.N) v[i][r] = -__builtin_inff();
         }
         // A NaN is dropped by the maximum and kept by the sum.  A wave whose
-        // columns all lie past N takes 0 as its maximum, and has the sum 0.
+        // columns all lie past N takes 0 as its maximum, and has the sum 0.  The sum is
+        // of exp2((v - top) s2), the largest term exactly 1 (with v s2 - top s2 in one
+        // step, top s2 rounded, the sum is off by |z| 2^-24).
         float top = v[0][0];
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r) top = fmaxf(top, v[i][r]);
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float z = top == -__builtin_inff() ? 0.0f : top * s2;
+        const float v0 = top == -__builtin_inff() ? 0.0f : top;
         float sum = 0.0f;
         if (edge) {
 #pragma unroll
@@ -405,18 +408,18 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
 #pragma unroll
             for (int r = 0; r < 16; ++r)
               if (n0 + nw + 32 * i + 8 * (r >> 2) + (r & 3) < op.N)
-                sum += __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -z));
+                sum += __builtin_amdgcn_exp2f((v[i][r] - v0) * s2);
         } else {
           float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              part[r & 3] += __builtin_amdgcn_exp2f(fmaf(v[i][r], s2, -z));
+              part[r & 3] += __builtin_amdgcn_exp2f((v[i][r] - v0) * s2);
           sum = (part[0] + part[1]) + (part[2] + part[3]);
         }
         sum += __shfl_xor(sum, 32, 64);
-        if (h == 0) red[wn * BM + ml] = make_float2(top == -__builtin_inff() ? top : z, sum);
+        if (h == 0) red[wn * BM + ml] = make_float2(top, sum);
       } else {
         if (!inside) continue;
         // the difference first, in units of e and rounded once, then the change to base
@@ -543,8 +546,9 @@ __global__ __launch_bounds__(64 * WN * WM * GROUPS, 2) void tile_kernel(TileArgs
 #pragma unroll
       for (int w = 1; w < WN; ++w) top = fmaxf(top, red[w * BM + ml].x);
       float sum = 0.0f;
+      const float s2 = fabsf(op.sx[m0 + ml]) * kLog2e;
 #pragma unroll
-      for (int w = 0; w < WN; ++w) sum += join_term(red[w * BM + ml], top);
+      for (int w = 0; w < WN; ++w) sum += join_term(red[w * BM + ml], top, s2);
       a.loss.part[(m0 + ml) * a.loss.ntiles + n0 / BN] = make_float2(top, sum);
     }
   }
@@ -587,20 +591,32 @@ __global__ __launch_bounds__(256) void loss_join_kernel(Operands op, LossOut o, 
   __syncthreads();
   top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
   float sum = 0.0f;
-  for (int i = t; i < o.ntiles; i += 256) sum += join_term(p[i], top);
+  const float sx = op.sx[m], size = fabsf(sx), s2 = size * kLog2e;
+  for (int i = t; i < o.ntiles; i += 256) sum += join_term(p[i], top, s2);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
   if (lane == 0) sums[wave] = sum;
   __syncthreads();
   if (t == 0) {
-    const float rest = __builtin_log2f((sums[0] + sums[1]) + (sums[2] + sums[3]));
-    const int d = (dots[0] + dots[1]) + (dots[2] + dots[3]);
-    lse[m] = (top + rest) * kLn2;
-    // the target's logit taken from the maximum before anything of the two's size is
-    // rounded: the sums are relative to exactly this maximum
-    const float below =
-        hit ? fmaf(-((float)d * op.sw[tg]), op.sx[m] * kLog2e, top) : __builtin_nanf("");
-    loss[m] = tg < 0 ? 0.0f : (below + rest) * kLn2;
+    // lse = z(top) + log(sum): the large one of the two is a product, carried with its
+    // remainder and rounded once with the rest.  (From base 2, top log2 e and back, lse
+    // was two to three times as far off as its rounding, and 1 - p of a certain row with
+    // it.)  The target's logit is taken from the maximum before anything of the two's
+    // size is rounded.  What the target's v leaves of its logit (and the other columns' of
+    // theirs: not known here) counts in lse by its probability and in the loss by the rest.
+    const float rest = __builtin_log2f((sums[0] + sums[1]) + (sums[2] + sums[3])) * kLn2;
+    const float high = top * size, low = fmaf(top, size, -high);
+    float below = __builtin_nanf(""), off = 0.0f;
+    if (hit) {
+      float left;
+      const float v = scaled((dots[0] + dots[1]) + (dots[2] + dots[3]), op.sw[tg], left);
+      below = fmaf(sx < 0.0f ? top + v : top - v, size, rest);
+      const float p = __expf(-below);
+      off = left * sx * p;
+      below -= left * sx * (1.0f - p);
+    }
+    lse[m] = high + (low + rest + off);
+    loss[m] = tg < 0 ? 0.0f : below;
   }
 }
 

@@ -211,18 +211,18 @@ __global__ __launch_bounds__(64 * KS) void skinny_kernel(SkinnyArgs a) {
   } else {
     // (max, sum) of a token over the 16 channels, as in i8_gemm.hip; the first of
     // them exists, so there is a maximum
-    const float s2 = sx * kLog2e;
+    const float s2 = fabsf(sx) * kLog2e;
     float v[4], top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] = (float)s[e] * sw[e];
-      if (e < count) top = fmaxf(top, v[e] * s2);
+      v[e] = (float)s[e] * (sx < 0.0f ? -sw[e] : sw[e]);
+      if (e < count) top = fmaxf(top, v[e]);
     }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < count) sum += __builtin_amdgcn_exp2f(fmaf(v[e], s2, -top));
+      if (e < count) sum += __builtin_amdgcn_exp2f((v[e] - top) * s2);
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
     if (inside && lane < 16)

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import quant_packed_weight_amd as gq
-from test_gpu_i8 import U, gen, i8, scales
+from test_gpu_i8 import U, gen, i8, loss_reference, scales
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,58 @@ def test_loss_grad_of_a_certain_target_with_a_large_sum(M, N, K):
     dx = gq.loss_i8_grad(w, sw, xq, sx, t, lse, torch.ones(M, device="cuda"), out_dtype=torch.float32)
     # the others' gradients, below 10^-20 of a weight each, are no part of f
     assert bool(((dx.double() - ref).abs() <= 16 * U * ref.abs() + 2.0 ** -40 * wd.abs() + 1e-15).all())
+
+
+CERTAIN = [(1, 500, 1000), (8, 500, 8000), (5, 16000, 2048), (40, 500, 1000), (150, 3000, 8000), (20, 70000, 515),
+           (300, 9000, 2048), (33, 200, 131071)]
+
+
+@pytest.mark.parametrize("negative", [False, True], ids=["", "negative"])
+@pytest.mark.parametrize("M,N,K", CERTAIN)
+def test_lse_of_a_certain_target_is_rounded_once(M, N, K, negative):
+    # logits of 96 to 120, whose half step is 2^-18; the others' e^-80 of them
+    w, sw, xq, sx, t = certain(M, N, K, 120.0, 0.9, M + K, negative)
+    assert bool((sx < 0).all()) == negative
+    z = (xq.double() * w[t].double()).sum(1) * sx.double() * sw[t].double()
+    loss, lse = gq.loss_i8(w, sw, xq, sx, t)
+    # the product's remainder is exact, the sum and the loss of one term are 1 and 0
+    assert float((lse.double() - z).abs().max()) <= 2.0 ** -18 * (1 + 2.0 ** -10)
+    assert float(loss.abs().max()) <= 1e-12
+    # without the target's sum in hand the largest sw dot is known to two roundings more
+    for other in (torch.full_like(t, -100), (t + 2) % N):
+        loss, lse = gq.loss_i8(w, sw, xq, sx, other)
+        assert float((lse.double() - z).abs().max()) <= 2.0 ** -18 * (1 + 2.0 ** -10) + 2 * U * 120
+        zo = (xq.double() * w[other.clamp(min=0)].double()).sum(1) * sx.double() * sw[other.clamp(min=0)].double()
+        ref = torch.where(other < 0, torch.zeros_like(z), z - zo)
+        # both logits' v and their difference, and the product
+        assert bool(((loss.double() - ref).abs() <= 2 * U * (z.abs() + zo.abs()) + 2 * U * ref.abs()).all())
+
+
+@pytest.mark.parametrize("negative", [False, True], ids=["", "negative"])
+@pytest.mark.parametrize("M,N,K", CERTAIN)
+def test_gradient_of_a_nearly_certain_row_from_the_loss_s_own_lse(M, N, K, negative):
+    # logits of 80 to 100 and one other token within about 8: 1 - p of 10^-4, which the
+    # half step of lse, 2^-18, moves by some per cent and nothing else by more than that
+    w, sw, xq, sx, t = certain(M, N, K, 100.0, 0.09, 3 * M + K, negative)
+    z, _, loss_r = loss_reference(w, sw, xq, sx, t)
+    loss, lse = gq.loss_i8(w, sw, xq, sx, t)
+    dx = gq.loss_i8_grad(w, sw, xq, sx, t, lse, torch.ones(M, device="cuda"), out_dtype=torch.float32)
+    rows = torch.arange(M, device="cuda")
+    p = torch.softmax(z, 1)
+    a = p.clone()
+    a[rows, t] = torch.expm1(-loss_r)
+    wd = w.double() * sw.double()[:, None]
+    ref = a @ wd
+    # lse by its half step and, where the others' probability is p', by p' (their v's
+    # two roundings); the others' factors by that and their own roundings, the
+    # additions by a few u of all
+    e = 2.0 ** -18 * (1 + 2.0 ** -10) + (1 - p[rows, t]) * 4 * U * 100
+    other = p.clone()
+    other[rows, t] = 0
+    tol = (e + 4 * U)[:, None] * wd[t].abs() + (other * (e + 6 * U * 100)[:, None]) @ wd.abs()
+    # (where w is 0 in both, only factors of 2^-115 are left, whose last parts lie below f32's
+    # smallest normal number, 2^-126, and may be lost: N of them, times w < 2^7)
+    tol = tol + 32 * U * (a.abs() @ wd.abs()) + N * 2.0 ** -119
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+    # 1 + p': a sum near one, rounded by a few u
+    assert bool(((loss.double() - loss_r).abs() <= 8 * U + (1 - p[rows, t]) * 8 * U * 100).all())
