@@ -89,8 +89,9 @@ def _matrix(t, name, dtype, rows, cols, index):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s must have consecutive values in its rows" % name)
-    # a single row has no next one: any pitch describes it
-    return ld if rows > 1 else -(-cols // 4) * 4
+    # a single row has no next one: any pitch describes it, one of eight values allows
+    # 16-byte accesses in every type
+    return ld if rows > 1 else -(-cols // 8) * 8
 
 
 def _i8_matrix(t, name, rows, cols, index):

@@ -175,3 +175,18 @@ def test_unknown_element_types_are_refused(L):
         gq.quantize_i8(torch.zeros((4, 32), dtype=torch.float64))
     with pytest.raises(TypeError):
         gq.linear_i8_grad_workspace(torch.int8, 4, 4, 4)
+
+
+def test_a_single_row_allows_wide_accesses_at_any_width():
+    # the pitch that the binding names for one row is a multiple of 16 bytes in every type
+    import torch
+
+    from quant_packed_weight_amd import _i8
+
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        for cols in (1, 7, 8, 12, 515, 1028):
+            x = torch.zeros((1, cols + 3), dtype=dtype)[:, :cols]
+            ld = _i8._matrix(x, "x", dtype, 1, cols, -1)
+            assert ld >= cols and ld * x.element_size() % 16 == 0
+            x = torch.zeros((2, cols + 3), dtype=dtype)[:, :cols]
+            assert _i8._matrix(x, "x", dtype, 2, cols, -1) == cols + 3
