@@ -6,6 +6,12 @@ matrices have rows that start 16 bytes apart or a multiple of it; `quantize_i8`
 allocates such a matrix for any width.  Every call runs on the device of its
 tensors, on `stream` or that device's current stream, and allocates what it is
 not given on that stream.
+
+No call records an autograd graph: the gradients are calls of their own
+(`linear_i8_grad`, `loss_i8_grad`), from a torch.autograd.Function's backward or by
+hand.  A call on tensors that require a gradient, with grad mode on, is refused
+rather than cut the graph unseen; `quantize_i8` takes parameters (leaves) all the
+same, whose int8 copy is a constant.
 """
 from __future__ import annotations
 
@@ -121,6 +127,13 @@ def _vector(t, name, dtype, n, index):
     return t.data_ptr()
 
 
+def _untracked():
+    """Raises where autograd would record a graph of the call."""
+    if _torch.is_grad_enabled():
+        raise ValueError("the int8 calls record no gradient: call them under torch.no_grad() or "
+                         "on detached tensors, and linear_i8_grad or loss_i8_grad for it")
+
+
 def _elsewhere(t, index, stream):
     """None where a call on tensors of t's device runs on the current stream of the
     current device; else a context in which it does: the tensors' device and
@@ -174,6 +187,8 @@ def quantize_i8(x, out=None, scale=None, stream=None):
     or weights [N, K] per output channel."""
     L = _fns or lib_i8()
     ty = _type(x.dtype, "x")
+    if not x.is_leaf:
+        _untracked()
     at = _elsewhere(x, x.get_device(), stream)
     if at is not None:
         with at:
@@ -195,6 +210,8 @@ def gemm_i8(w, sw, xq, sx, bias=None, out=None, out_dtype=None, stream=None):
     """y = (sx xq) (sw w)^T + bias for int8 w [N, K], xq [M, K] and their scales
     (gemmq_gemm_i8): f32, bf16 or f16 [M, N] (`out_dtype`, f32 by default)."""
     L = _fns or lib_i8()
+    if sw.requires_grad or sx.requires_grad or (bias is not None and bias.requires_grad):
+        _untracked()
     dev = w.get_device()
     at = _elsewhere(w, dev, stream)
     if at is not None:
@@ -218,6 +235,8 @@ def linear_i8(w, sw, x, bias=None, out=None, out_dtype=None, xq=None, sx=None, s
     token, then gemm_i8 (gemmq_linear_i8).  Returns [M, N] in `out_dtype` (x's by
     default); xq and sx, when given, receive the quantized activations."""
     L = _fns or lib_i8()
+    if sw.requires_grad or x.requires_grad or (bias is not None and bias.requires_grad):
+        _untracked()
     dev = w.get_device()
     at = _elsewhere(w, dev, stream)
     if at is not None:
@@ -246,6 +265,8 @@ def linear_i8_grad(w, sw, dy, out=None, workspace=None, stream=None):
     activations (gemmq_linear_i8_grad): dy [M, N] -> [M, K] of dy's type.
     `workspace`: a tensor of at least linear_i8_grad_workspace bytes, or None."""
     L = _fns or lib_i8()
+    if sw.requires_grad or dy.requires_grad:
+        _untracked()
     dev = w.get_device()
     at = _elsewhere(w, dev, stream)
     if at is not None:
@@ -270,6 +291,8 @@ def loss_i8(w, sw, xq, sx, target, loss=None, lse=None, workspace=None, stream=N
     [N, K], the logits never in memory (gemmq_loss_i8): returns (loss, lse), f32
     [M]; target int64 [M], negative where a position is ignored (loss 0)."""
     L = _fns or lib_i8()
+    if sw.requires_grad or sx.requires_grad:
+        _untracked()
     dev = w.get_device()
     at = _elsewhere(w, dev, stream)
     if at is not None:
@@ -298,6 +321,8 @@ def loss_i8_grad(w, sw, xq, sx, target, lse, dloss, out=None, out_dtype=None, wo
     states sx xq (gemmq_loss_i8_grad): [M, K] in `out_dtype` (bf16 by default);
     lse from loss_i8."""
     L = _fns or lib_i8()
+    if sw.requires_grad or sx.requires_grad or lse.requires_grad or dloss.requires_grad:
+        _untracked()
     dev = w.get_device()
     at = _elsewhere(w, dev, stream)
     if at is not None:

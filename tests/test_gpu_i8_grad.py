@@ -237,3 +237,52 @@ def test_linear_grad_with_an_infinite_last_scale(M, N, K, extra):
     # infinite with the sign of dy w in the last channel; NaN where either is zero
     ref = (dy[:, N - 1:].double() * math.inf) * w[N - 1].double()
     assert torch.equal(dx.nan_to_num(7.0), ref.nan_to_num(7.0))
+
+
+# ------------------------------------------------------------------ under autograd
+def test_in_a_function_of_autograd():
+    # the calls run where autograd records nothing: in a Function's forward and backward;
+    # a tensor that would lose its gradient unseen is refused
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, sw):
+            ctx.save_for_backward(w, sw)
+            return gq.linear_i8(w, sw, x)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return gq.linear_i8_grad(*ctx.saved_tensors, dy.contiguous()), None, None
+
+    class Loss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, h, w, sw, t):
+            hq, sh = gq.quantize_i8(h)
+            loss, lse = gq.loss_i8(w, sw, hq, sh, t)
+            ctx.save_for_backward(w, sw, hq, sh, t, lse)
+            ctx.dtype = h.dtype
+            return loss
+
+        @staticmethod
+        def backward(ctx, dloss):
+            return (gq.loss_i8_grad(*ctx.saved_tensors, dloss.contiguous(), out_dtype=ctx.dtype),
+                    None, None, None)
+
+    g = gen(3)
+    M, D, N, V = 20, 200, 320, 3001
+    p1 = torch.nn.Parameter(torch.randn((N, D), generator=g, device="cuda") * D ** -0.5)
+    w1, s1 = gq.quantize_i8(p1)  # a parameter's int8 copy is a constant
+    w2, s2 = gq.quantize_i8(torch.randn((V, N), generator=g, device="cuda") * N ** -0.5)
+    x = torch.randn((M, D), generator=g, device="cuda").bfloat16().requires_grad_()
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    loss = Loss.apply(Layer.apply(x, w1, s1), w2, s2, t)
+    (loss / M).sum().backward()
+    with torch.no_grad():
+        h = gq.linear_i8(w1, s1, x)
+        hq, sh = gq.quantize_i8(h)
+        l2, lse = gq.loss_i8(w2, s2, hq, sh, t)
+        dh = gq.loss_i8_grad(w2, s2, hq, sh, t, lse, torch.full((M,), 1.0 / M, device="cuda"))
+        assert torch.equal(loss, l2) and torch.equal(x.grad, gq.linear_i8_grad(w1, s1, dh))
+    for call in (lambda: gq.linear_i8(w1, s1, x), lambda: gq.quantize_i8(2 * x),
+                 lambda: gq.linear_i8(w1, s1, x.detach(), bias=p1[:, 0].contiguous())):
+        with pytest.raises(ValueError, match="record no gradient"):
+            call()

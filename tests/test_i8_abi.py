@@ -190,3 +190,30 @@ def test_a_single_row_allows_wide_accesses_at_any_width():
             assert ld >= cols and ld * x.element_size() % 16 == 0
             x = torch.zeros((2, cols + 3), dtype=dtype)[:, :cols]
             assert _i8._matrix(x, "x", dtype, 2, cols, -1) == cols + 3
+
+
+def test_tensors_that_require_a_gradient_are_refused(L):
+    # no result has a graph, so none is cut unseen; without grad mode the calls go on (here
+    # to the refusal of host tensors)
+    import torch
+
+    w, sw = torch.zeros((32, 32), dtype=torch.int8), torch.zeros(32)
+    xq, one, t = torch.zeros((4, 32), dtype=torch.int8), torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    x, leaf = torch.zeros((4, 32)), torch.zeros((4, 32), requires_grad=True)
+    s1, b1, one1 = sw.clone().requires_grad_(), sw.clone().requires_grad_(), one.clone().requires_grad_()
+    calls = [lambda: gq.linear_i8(w, sw, leaf), lambda: gq.linear_i8(w, sw, x, bias=b1),
+             lambda: gq.linear_i8(w, s1, x), lambda: gq.linear_i8(w, sw, 2 * leaf),
+             lambda: gq.gemm_i8(w, sw, xq, one1), lambda: gq.gemm_i8(w, s1, xq, one),
+             lambda: gq.gemm_i8(w, sw, xq, one, bias=b1), lambda: gq.linear_i8_grad(w, sw, leaf),
+             lambda: gq.loss_i8(w, sw, xq, one1, t), lambda: gq.loss_i8(w, s1, xq, one, t),
+             lambda: gq.loss_i8_grad(w, sw, xq, one, t, one, one1),
+             lambda: gq.loss_i8_grad(w, sw, xq, one, t, one1, one),
+             lambda: gq.quantize_i8(2 * leaf)]
+    for call in calls:
+        with pytest.raises(ValueError, match="record no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(TypeError, match="device tensors"):
+            call()
+    # a parameter's int8 copy is a constant
+    with pytest.raises(TypeError, match="device tensors"):
+        gq.quantize_i8(leaf)
