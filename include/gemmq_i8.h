@@ -25,8 +25,10 @@
  *    pitch allow them.
  *  - Element types: GEMMQ_F32, GEMMQ_BF16, GEMMQ_F16.
  *  - 1 <= K <= GEMMQ_I8_MAX_K: the int32 sums cannot overflow, also with -128 in
- *    both matrices.  M and N up to GEMMQ_I8_MAX_ROWS.  M == 0 is a valid empty
- *    call: nothing is touched.
+ *    both matrices.  M and N up to GEMMQ_I8_MAX_ROWS.  One launch holds all output
+ *    tiles: M * N of a product or a loss and M * K of a gradient fit up to
+ *    GEMMQ_I8_MAX_OUTPUTS, whatever the shape; beyond it a call may be refused with
+ *    GEMMQ_E_SHAPE.  M == 0 is a valid empty call: nothing is touched.
  *  - `ws` is scratch memory of at least the bytes that the entry's ..._workspace
  *    function gives for the same arguments, 16-byte aligned; its contents before
  *    the call do not matter and are not defined after it.  Calls that can run at
@@ -58,6 +60,7 @@ extern "C" {
 #define GEMMQ_I8_MAX_K 131071        /* 2^14 * 131071 < 2^31 */
 #define GEMMQ_I8_MAX_ROWS 16777216   /* 2^24 rows of any matrix */
 #define GEMMQ_I8_MAX_PITCH 1048576   /* bytes between rows of an int8 matrix */
+#define GEMMQ_I8_MAX_OUTPUTS 68719476736 /* 2^36: outputs that always fit a launch */
 
 /* GEMMQ_I8_ABI_VERSION of the library that was loaded.  Never fails. */
 int gemmq_i8_abi_version(void);

@@ -25,6 +25,7 @@ I8_ABI_VERSION = 1
 I8_MAX_K = 131071
 I8_MAX_ROWS = 1 << 24
 I8_MAX_PITCH = 1 << 20
+I8_MAX_OUTPUTS = 1 << 36
 
 _P, _I, _I64, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 # every entry point include/gemmq_i8.h declares: name -> (restype, argtypes)

@@ -117,7 +117,8 @@ const char* gemmq_status_str(int status) {
       return "GEMMQ_E_SHAPE: K must be a positive multiple of 256 up to 2^24, rows up to 2^31; "
              "the GEMV path takes M <= 8, the small-M path M <= 64 (q6_K: 16), the GEMM path M <= "
              "4194240; the int8 calls take K <= 131071, rows up to 2^24, pitches of int8 matrices "
-             "from K to 2^20 in multiples of 16, and at least one vocabulary row";
+             "from K to 2^20 in multiples of 16, at least one vocabulary row, and no more output "
+             "tiles than a launch holds (2^36 outputs always fit)";
     case GEMMQ_E_ALIGNMENT: return "GEMMQ_E_ALIGNMENT: a pointer breaks the documented alignment";
     case GEMMQ_E_DEVICE: return "GEMMQ_E_DEVICE: the current HIP device is not a gfx950";
     case GEMMQ_E_LAUNCH: return "GEMMQ_E_LAUNCH: the HIP runtime rejected a kernel launch";

@@ -217,3 +217,27 @@ def test_tensors_that_require_a_gradient_are_refused(L):
     # a parameter's int8 copy is a constant
     with pytest.raises(TypeError, match="device tensors"):
         gq.quantize_i8(leaf)
+
+
+def test_outputs_that_always_fit(L):
+    # the header's limits: every shape of up to 2^36 outputs is taken, and a status text names them
+    import math
+    import random
+
+    src = open(HEADER).read()
+    most = int(re.search(r"#define GEMMQ_I8_MAX_OUTPUTS (\d+)", src).group(1))
+    assert most == gq.I8_MAX_OUTPUTS == 1 << 36
+    r = random.Random(3)
+
+    def size(low, high):
+        return int(round(math.exp(r.uniform(math.log(low), math.log(high)))))
+
+    for n in range(6000):
+        M = size(1, gq.I8_MAX_ROWS)
+        N = min(gq.I8_MAX_ROWS, most // M) if n % 2 else size(1, min(gq.I8_MAX_ROWS, most // M))
+        K = min(gq.I8_MAX_K, most // M) if n % 3 else size(1, min(gq.I8_MAX_K, most // M))
+        assert L.gemmq_loss_i8_workspace(M, N, size(1, gq.I8_MAX_K)) > 0, (M, N)
+        for ty in (0, 1, 2):
+            assert L.gemmq_linear_i8_grad_workspace(ty, M, N, K) > 0, (ty, M, N, K)
+            assert L.gemmq_loss_i8_grad_workspace(ty, M, N, K) > 0, (ty, M, N, K)
+    assert "2^36 outputs" in gq.status_str(SHAPE)
