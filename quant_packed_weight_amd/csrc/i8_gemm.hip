@@ -656,10 +656,12 @@ int64_t tiles(const Tile& c, int M, int N) { return ceil_div(M, c.bm) * ceil_div
 //   M 512 N 4096 K 4096    45   30   26    24    22    22   18.5 [16.6]
 //   M 64 N 32000 K 4096    -    -    26    28    25    31   22.3 [22.2] 33    30
 //   M 128 N 4096 K 4096                                17   14    11   [9]    15
-// Up to 32 tokens of a vocabulary W's stream decides, and 128 channels a workgroup
-// are ahead of 64 (M = 8, 151936 x 2048 57 us against 59).
+// Up to 32 tokens of a vocabulary W's stream decides, and 128 channels a workgroup are
+// ahead of 64 once there are more than three such workgroups a CU, 98304 channels (the
+// loss at M = 8 over K = 2048, 128 / 64 channels: N = 66000 31.3 / 28.5 us, 80000 33.0 /
+// 32.0, 98304 36.2 / 36.9, 115000 41.1 / 44.2, 151936 56.6 / 58.5, 200000 79.9 / 88.1).
 int pick_tile(int M, int N, int K) {
-  if (M <= 32 && N > 65536) return kWideTile;
+  if (M <= 32 && N > 98304) return kWideTile;
   const int64_t steps = ceil_div(K, kStep);
   int best = 0;
   double least = 0.0;

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import quant_packed_weight_amd as gq
-from test_gpu_i8 import U, gen, i8, loss_reference, scales
+from test_gpu_i8 import FLOOR, HALF, U, gen, i8, loss_reference, scales
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,29 @@ def test_gradient_of_a_nearly_certain_row_from_the_loss_s_own_lse(M, N, K, negat
     assert bool(((dx.double() - ref).abs() <= tol).all())
     # 1 + p': a sum near one, rounded by a few u
     assert bool(((loss.double() - loss_r).abs() <= 8 * U + (1 - p[rows, t]) * 8 * U * 100).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 98305, 64), (5, 100001, 260), (17, 98304, 130), (20, 100001, 140),
+                                   (32, 99999, 515), (33, 100001, 140)])
+def test_few_rows_over_a_large_vocabulary(M, N, K):
+    # on both sides of the number of channels from which workgroups take 128 of them
+    g = gen(M + N)
+    w, sw, xq, sx = i8(N, K, g, full=True), scales(N, g, K ** -0.5 / 64), i8(M, K, g), scales(M, g, 0.05)
+    t = torch.randint(0, N, (M,), generator=g, device="cuda")
+    t[M - 1] = N - 1
+    z, lse_r, loss_r = loss_reference(w, sw, xq, sx, t)
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        y = gq.gemm_i8(w, sw, xq, sx, out_dtype=dt)
+        # the sum to f32 and two scalings, the result's type
+        assert bool(((y.double() - z).abs() <= (4 * U + HALF[dt]) * z.abs() + FLOOR[dt]).all())
+    loss, lse = gq.loss_i8(w, sw, xq, sx, t)
+    # a logit's two roundings (v, and its difference with the maximum), the exponentials' 2 u
+    # and the additions, a term in 300 at most
+    tol = 3 * U * z.abs().amax(1) + (302 + 3) * U + U * lse_r.abs()
+    assert bool(((lse.double() - lse_r).abs() <= tol).all())
+    assert bool(((loss.double() - loss_r).abs() <= tol + 3 * U * z.abs().amax(1)).all())
+    p = torch.softmax(z, 1)
+    p[torch.arange(M, device="cuda"), t] = torch.expm1(-loss_r)
+    ref = p @ (w.double() * sw.double()[:, None])
+    dx = gq.loss_i8_grad(w, sw, xq, sx, t, lse, torch.ones(M, device="cuda"), out_dtype=torch.float32)
+    assert float((dx.double() - ref).norm() / ref.norm()) <= 2.0 ** -18
