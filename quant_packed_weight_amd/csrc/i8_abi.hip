@@ -51,8 +51,9 @@ size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 // of kMinPiece columns where the rows alone are more: it bounds the workspace.  A
 // further piece costs a passage of the partial sums through memory and another
 // last round of tiles, more than a factor that fits the 256 MB last-level cache
-// saves (M = 1024 over 151936 rows: 128 MB, three pieces, 1020 us; 256 MB 953; 384
-// MB, one piece, 924).
+// saves (bf16 over 151936 x 2048, with 128 / 256 / 384 / 768 MB: M = 1024 1028 / 956 /
+// 913 / 913 us, one piece from 384; M = 2048 1881 / 1858 / 1800 / 1735; f32 at M = 700
+// 1578 / 1618 / 1568 / 1539).  768 MB would buy 4% there with twice the memory.
 constexpr int64_t kFactorBytes = (int64_t)384 << 20;
 constexpr int64_t kMinPiece = 1024;
 
