@@ -357,7 +357,7 @@ grad_kernel(GradArgs a, uint32_t ktiles, uint32_t mtiles) {
 
 // A[m, n] = dY[m, n] * sw[n] as `planes` bf16 matrices, zero from column N to
 // the pitch.  A workgroup takes 2048 columns of ROWS rows, a thread eight of each:
-// four rows where there are many (2048 x 12288 bf16: 21 us, one row 54), one
+// four rows where there are many (2048 x 12288 bf16: 18.4 us, one row 54), one
 // where few would leave the chip idle (77 x 1037 f32: 5 us, four rows 9).
 template <int TYPE, int ROWS, bool ONE>
 __global__ __launch_bounds__(256) void planes_kernel(const void* dY, int64_t lddy, bool wide,
