@@ -94,11 +94,12 @@ bool grad_shape_ok(int64_t M, int64_t K, const GradPlan& p) {
 }
 
 // Up to 128 tokens a bf16 dY whose rows allow 16-byte loads is read by the product as
-// it lies, and W scaled by sw instead (a rounding of sw * w to bf16 in the place of
-// one of dy * sw; up to eight tokens dY is scaled, with no rounding to one): no factor in the workspace, and a launch less (4096 x 4096 at M =
-// 16 15 -> 12 us, M = 128 29 -> 26).  With more tokens the large tiles are the faster
-// ones, whose conversion has no room for the scaling: with the factor / as it lies M =
-// 129 over 2048 x 2048 15.4 / 14.3 us, 4096 x 12288 39 / 50, M = 512 68 / 82.
+// it lies, and W scaled by sw instead (a rounding of sw * w to bf16 in the place of one
+// of dy * sw; up to eight tokens dY is scaled, in two numbers): no factor in the
+// workspace, and a launch less (4096 x 4096 at M = 16 15 -> 12 us, M = 128 29 -> 26).
+// With more tokens the large tiles are the faster ones, whose conversion has no room for
+// the scaling: with the factor / as it lies M = 129 over 2048 x 2048 15.4 / 14.3 us, 4096
+// x 12288 39 / 50, M = 512 68 / 82.
 constexpr int64_t kScaledMaxM = 128;
 
 bool reads_dy(int type, const void* dY, int64_t lddy, int64_t M, int64_t N) {
