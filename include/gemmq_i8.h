@@ -3,8 +3,9 @@
  * weights with one scale per output channel and int8 activations with one scale
  * per token, its gradient with respect to the activations, and the softmax
  * cross-entropy over a vocabulary that reads such weights (a language-model
- * head) without keeping the logits, with its gradient.  gemmq.h holds the
- * K-quant half, the status codes and gemmq_status_str.
+ * head) without keeping the logits, with its gradient; and what a decoder has
+ * between such products.  gemmq.h holds the K-quant half, the status codes and
+ * gemmq_status_str.
  *
  * The values:  w[n, k] = sw[n] * W[n, k],   x[m, k] = sx[m] * Xq[m, k].
  *
@@ -34,7 +35,8 @@
  *    the call do not matter and are not defined after it.  Calls that can run at
  *    the same time (other streams, graphs replayed together) need workspaces of
  *    their own, as they need outputs of their own.
- *  - No output may overlap an input, another output or the workspace.
+ *  - No output may overlap an input, another output or the workspace, but where an
+ *    entry says that it may be an input itself.
  *  - Results do not depend on timing: no floating-point atomics, every sum has a
  *    fixed order for given arguments.  A row m of a result depends on row m of the
  *    activations only, so a row with a NaN does not touch the others.
@@ -167,6 +169,53 @@ int gemmq_loss_i8_grad(const int8_t *W, int64_t ldw, const float *sw, const int8
                        int64_t ldq, const float *sx, const int64_t *target, const float *lse,
                        const float *dloss, int type, void *dX, int64_t lddx, int64_t M, int64_t N,
                        int64_t K, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands between the int8 products of a decoder.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Residual addition, root-mean-square norm and quantization, of each row:
+ *   h = x + r                      rounded to the rows' type (r == NULL: h = x)
+ *   p[k] = h[k] * w[k]             in f32
+ *   Q, s0 = gemmq_quantize_i8 of p
+ *   s = s0 * rstd,  rstd = 1 / sqrt(mean_k h[k]^2 + eps)
+ * so that s[m] * Q[m, k] is the quantized norm(h) * w: rstd is one positive factor
+ * of a row, which cancels in p / max|p|, and the integers do not depend on it.  The sum
+ * of squares is in 64 bits; s is rounded once.
+ * A row whose p is not all finite has s = NaN and Q = 0, as in gemmq_quantize_i8.
+ *   type      of X, R and H.   R  [M, K] or NULL.
+ *   H, ldh    [M, K] or NULL: receives h, and may be X or R itself (the same
+ *             pointer and pitch; otherwise it overlaps neither).
+ *   w         f32 [K].   eps  >= 0 and finite.
+ *   Q, ldq, s as in gemmq_quantize_i8.
+ * Errors: as gemmq_quantize_i8, and GEMMQ_E_INVALID_ARG for eps.
+ */
+int gemmq_rms_i8(int type, const void *X, int64_t ldx, const void *R, int64_t ldr, void *H,
+                 int64_t ldh, const float *w, float eps, int8_t *Q, int64_t ldq, float *s,
+                 int64_t M, int64_t K, void *stream);
+
+/* Workspace bytes of gemmq_rms_i8_grad with a dw (0 for arguments it refuses; without
+   a dw no workspace is needed). */
+size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K);
+
+/*
+ * The gradient of norm(h) * w (the quantizer's rounding taken as the identity), with
+ * n = h * rstd and d = dy * w:
+ *   dX[m, k] = rstd (d[k] - n[k] mean_j d[j] n[j])  (+ dH[m, k])
+ *   dw[k]    = sum_m dY[m, k] n[m, k]
+ * dX is the gradient with respect to x and to r, where dH is what arrives at h by the
+ * residual path.
+ *   type  of H, dY, dH and dX, all [M, K].   dH  may be NULL.
+ *   dX    may be dY or dH itself (the same pointer and pitch).
+ *   dw    f32 [K], overwritten (zeros where M == 0), or NULL: not computed.
+ *   ws    may be NULL where dw is.
+ * Errors: as gemmq_rms_i8, and GEMMQ_E_INVALID_ARG for a workspace that is too small.
+ */
+int gemmq_rms_i8_grad(int type, const void *H, int64_t ldh, const float *w, float eps,
+                      const void *dY, int64_t lddy, const void *dH, int64_t lddh, void *dX,
+                      int64_t lddx, float *dw, int64_t M, int64_t K, void *ws, size_t ws_bytes,
+                      void *stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,7 @@ from ._i8 import (  # noqa: F401
     loss_i8_workspace,
     quantize_i8,
 )
+from ._i8_block import rms_i8, rms_i8_grad, rms_i8_grad_workspace  # noqa: F401
 from ._lib import (  # noqa: F401
     ABI_VERSION,
     BLOCK_BYTES,

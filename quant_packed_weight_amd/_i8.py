@@ -28,6 +28,7 @@ I8_MAX_PITCH = 1 << 20
 I8_MAX_OUTPUTS = 1 << 36
 
 _P, _I, _I64, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 # every entry point include/gemmq_i8.h declares: name -> (restype, argtypes)
 EXPORTS_I8 = {
     "gemmq_i8_abi_version": (_I, []),
@@ -43,6 +44,10 @@ EXPORTS_I8 = {
     "gemmq_loss_i8_grad_workspace": (_S, [_I, _I64, _I64, _I64]),
     "gemmq_loss_i8_grad": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _P, _P, _I, _P, _I64, _I64, _I64,
                                 _I64, _P, _S, _P]),
+    "gemmq_rms_i8": (_I, [_I, _P, _I64, _P, _I64, _P, _I64, _P, _F, _P, _I64, _P, _I64, _I64, _P]),
+    "gemmq_rms_i8_grad_workspace": (_S, [_I, _I64, _I64]),
+    "gemmq_rms_i8_grad": (_I, [_I, _P, _I64, _P, _F, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64,
+                               _P, _S, _P]),
 }
 
 _fns = None
@@ -132,7 +137,7 @@ def _untracked():
     """Raises where autograd would record a graph of the call."""
     if _torch.is_grad_enabled():
         raise ValueError("the int8 calls record no gradient: call them under torch.no_grad() or "
-                         "on detached tensors, and linear_i8_grad or loss_i8_grad for it")
+                         "on detached tensors, and the _grad calls for it")
 
 
 def _elsewhere(t, index, stream):

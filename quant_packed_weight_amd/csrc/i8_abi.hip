@@ -1,9 +1,7 @@
 // i8_abi.hip -- the int8 half of the C ABI (gemmq_i8.h): validation, workspace
 // layout and the order of launches.  As in abi.hip, a bad call returns a named
 // status and launches nothing, and the library owns no memory.
-#include "abi_util.h"
-#include "gemmq_i8.h"
-#include "i8.h"
+#include "i8_check.h"
 
 using gemmq::aligned;
 using gemmq::check_device;
@@ -12,40 +10,6 @@ using gemmq::launched;
 using namespace gemmq::i8;
 
 namespace {
-
-constexpr int64_t kMaxPitchElems = (int64_t)1 << 40;  // keeps element offsets below 2^63
-
-bool known(int type) { return type == GEMMQ_F32 || type == GEMMQ_BF16 || type == GEMMQ_F16; }
-
-int check_shape(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0) return GEMMQ_E_INVALID_ARG;
-  if (K < 1 || K > GEMMQ_I8_MAX_K || M > GEMMQ_I8_MAX_ROWS || N > GEMMQ_I8_MAX_ROWS)
-    return GEMMQ_E_SHAPE;
-  return GEMMQ_OK;
-}
-
-// an int8 matrix with its scales
-int check_i8(const void* p, int64_t ld, const void* s, int64_t K) {
-  if (!p || !s) return GEMMQ_E_INVALID_ARG;
-  if (ld < K || ld > GEMMQ_I8_MAX_PITCH) return GEMMQ_E_SHAPE;
-  if (ld % 16 != 0 || !aligned(p, 16) || !aligned(s, 4)) return GEMMQ_E_ALIGNMENT;
-  return GEMMQ_OK;
-}
-
-// a matrix of element type `type`
-int check_rows(int type, const void* p, int64_t ld, int64_t width) {
-  if (!known(type) || !p) return GEMMQ_E_INVALID_ARG;
-  if (ld < width || ld > kMaxPitchElems) return GEMMQ_E_SHAPE;
-  if (!aligned(p, (uintptr_t)type_bytes(type))) return GEMMQ_E_ALIGNMENT;
-  return GEMMQ_OK;
-}
-
-int check_ws(const void* ws, size_t have, size_t need) {
-  if (!ws || have < need) return GEMMQ_E_INVALID_ARG;
-  return aligned(ws, 16) ? GEMMQ_OK : GEMMQ_E_ALIGNMENT;
-}
-
-size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 
 // The gradients walk N in pieces whose bf16 factor stays within this many bytes, or
 // of kMinPiece columns where the rows alone are more: it bounds the workspace.  A

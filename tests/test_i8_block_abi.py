@@ -1,0 +1,124 @@
+"""The entry points of what stands between the int8 products, without a GPU: every
+refusal.  The calls below fail validation (or are empty), so none reaches HIP."""
+import os
+
+import pytest
+
+import quant_packed_weight_amd as gq
+
+A = 0x10000  # never dereferenced
+B = 0x20000
+INVALID, SHAPE, ALIGN = -1, -3, -4
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(gq.LIB_PATH):
+        pytest.fail("libgemmq.so not built: run python -m quant_packed_weight_amd.build")
+    return gq.lib_i8()
+
+
+NAN, INF = float("nan"), float("inf")
+RMS = dict(type=1, X=A, ldx=100, R=A, ldr=100, H=B, ldh=100, w=A, eps=1e-6, Q=A, ldq=112, s=A, M=4,
+           K=100)
+RGRAD = dict(type=1, H=A, ldh=100, w=A, eps=1e-6, dY=A, lddy=100, dH=A, lddh=100, dX=B, lddx=100,
+             dw=A, M=4, K=100, ws=A, bytes=1 << 40)
+ENTRIES = {"rms_i8": RMS, "rms_i8_grad": RGRAD}
+# matrices of the element type: name, pitch, width, and whether it may be NULL
+MATRICES = {"rms_i8": [("X", "ldx", "K", False), ("R", "ldr", "K", True), ("H", "ldh", "K", True)],
+            "rms_i8_grad": [("H", "ldh", "K", False), ("dY", "lddy", "K", False),
+                            ("dH", "lddh", "K", True), ("dX", "lddx", "K", False)]}
+I8_MATRICES = {"rms_i8": [("Q", "ldq")]}
+# f32 vectors: name, and whether it may be NULL
+VECTORS = {"rms_i8": [("w", False), ("s", False)], "rms_i8_grad": [("w", False), ("dw", True)]}
+OWN = {"rms_i8": [(dict(H=A, ldh=104, R=B), INVALID),            # X, but not as X lies
+                  (dict(H=B, ldh=104, R=B), INVALID)],
+       "rms_i8_grad": [(dict(dX=A, lddx=104, dH=B), INVALID), (dict(dX=B, lddx=104, dH=B), INVALID)]}
+
+
+def _changes(entry, a):
+    yield dict(M=-1), INVALID
+    yield dict(M=gq.I8_MAX_ROWS + 1), SHAPE
+    for c in ("K", "N"):
+        if c in a:
+            yield {c: gq.I8_MAX_K + 1 if c == "K" else gq.I8_MAX_ROWS + 1}, SHAPE
+    if "K" in a:
+        yield dict(K=0), SHAPE
+    if "N" in a:
+        yield dict(N=-1), INVALID
+    for t in ("type", "xtype", "ytype"):
+        if t in a:
+            yield {t: 3}, INVALID
+            yield {t: -1}, INVALID
+    if "eps" in a:
+        for v in (-1.0, NAN, INF):
+            yield dict(eps=v), INVALID
+    for p, ld, width, null in MATRICES[entry]:
+        if not null:
+            yield {p: None}, INVALID
+        yield {p: A + 1}, ALIGN
+        yield {ld: a[width] - 1}, SHAPE
+        yield {ld: (1 << 40) + 1}, SHAPE
+    for p, ld in I8_MATRICES.get(entry, []):
+        yield {p: None}, INVALID
+        yield {p: A + 8}, ALIGN
+        yield {ld: 104}, ALIGN
+        yield {ld: 96}, SHAPE
+        yield {ld: gq.I8_MAX_PITCH + 16}, SHAPE
+    for v, null in VECTORS[entry]:
+        if not null:
+            yield {v: None}, INVALID
+        yield {v: A + 2}, ALIGN
+    if "ws" in a:
+        yield dict(ws=None), INVALID
+        yield dict(ws=A + 8), ALIGN
+        yield dict(bytes=16), INVALID
+    yield from OWN.get(entry, [])
+
+
+CASES = [(e, c, s) for e, a in ENTRIES.items() for c, s in _changes(e, a)]
+
+
+@pytest.mark.parametrize("entry,change,status", CASES,
+                         ids=["%s-%s" % (e, "-".join("%s=%s" % i for i in c.items()))
+                              for e, c, _ in CASES])
+def test_refusals(L, entry, change, status):
+    args = dict(ENTRIES[entry], **change)
+    assert getattr(L, "gemmq_" + entry)(*args.values(), None) == status
+
+
+def test_empty_calls(L):
+    assert L.gemmq_rms_i8(*dict(RMS, M=0).values(), None) == 0
+    # no rows and no sum over them; with one, zeros are written
+    assert L.gemmq_rms_i8_grad(*dict(RGRAD, M=0, dw=None).values(), None) == 0
+
+
+def test_workspace_sizes(L):
+    import torch
+
+    for ty, dtype in enumerate((torch.float32, torch.bfloat16, torch.float16)):
+        need = L.gemmq_rms_i8_grad_workspace(ty, 4, 100)
+        assert need >= 4 * 100 * 4
+        assert L.gemmq_rms_i8_grad(*dict(RGRAD, type=ty, bytes=need - 1).values(), None) == INVALID
+        assert gq.rms_i8_grad_workspace(dtype, 4, 100) == need
+        # a few rows of partial sums, not one for each row
+        assert L.gemmq_rms_i8_grad_workspace(ty, 1 << 20, 4096) < 64 << 20
+    for bad in ((3, 4, 100), (0, -1, 100), (0, 4, 0), (0, 0, 100)):
+        assert L.gemmq_rms_i8_grad_workspace(*bad) == 0
+
+
+def test_binding_refusals(L):
+    import torch
+
+    x, w, leaf = torch.zeros((4, 32)), torch.zeros(32), torch.zeros((4, 32), requires_grad=True)
+    w1 = w.clone().requires_grad_()
+    calls = [lambda: gq.rms_i8(leaf, w), lambda: gq.rms_i8(x, w1), lambda: gq.rms_i8(x, w, residual=leaf),
+             lambda: gq.rms_i8_grad(leaf, w, x), lambda: gq.rms_i8_grad(x, w1, x),
+             lambda: gq.rms_i8_grad(x, w, leaf), lambda: gq.rms_i8_grad(x, w, x, dh=leaf)]
+    for call in calls:
+        with pytest.raises(ValueError, match="record no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(TypeError, match="device tensors"):
+            call()
+    with pytest.raises(TypeError):
+        gq.rms_i8_grad_workspace(torch.int8, 4, 4)
