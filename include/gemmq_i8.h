@@ -217,6 +217,81 @@ int gemmq_rms_i8_grad(int type, const void *H, int64_t ldh, const float *w, floa
                       int64_t lddx, float *dw, int64_t M, int64_t K, void *ws, size_t ws_bytes,
                       void *stream);
 
+/* The activations, act(z). */
+#define GEMMQ_ACT_NONE 0
+#define GEMMQ_ACT_SILU 1      /* z / (1 + exp(-z)) */
+#define GEMMQ_ACT_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define GEMMQ_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define GEMMQ_ACT_RELU 4      /* max(z, 0) */
+
+/*
+ * gemmq_gemm_i8 with an activation and a residual in its epilogue:
+ *   z[m, n] = sx[m] * sw[n] * sum_k Xq[m, k] * W[n, k]  (+ bias[n])
+ *   Y[m, n] = act(z[m, n])  (+ R[m, n])
+ * in f32, rounded once to Y's type.
+ *   R, ldr  [M, N] of Y's type, or NULL; Y may be R itself (the same pointer and pitch).
+ *   Z, ldz  [M, N] of Y's type, or NULL: receives z, rounded, for gemmq_act_grad.
+ * Errors: as gemmq_gemm_i8, and GEMMQ_E_INVALID_ARG for an unknown act.
+ */
+int gemmq_gemm_i8_act(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Xq, int64_t ldq,
+                      const float *sx, const float *bias, int act, const void *R, int64_t ldr,
+                      int ytype, void *Y, int64_t ldy, void *Z, int64_t ldz, int64_t M, int64_t N,
+                      int64_t K, void *stream);
+
+/* Quantize X into Xq and sx, then gemmq_gemm_i8_act: the same bits as the two calls. */
+int gemmq_linear_i8_act(const int8_t *W, int64_t ldw, const float *sw, int xtype, const void *X,
+                        int64_t ldx, int8_t *Xq, int64_t ldq, float *sx, const float *bias,
+                        int act, const void *R, int64_t ldr, int ytype, void *Y, int64_t ldy,
+                        void *Z, int64_t ldz, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * A gated pair of matrices on the same activations, both [N, K]:
+ *   z[m, n] = sx[m] * sw[n] * sum_k Xq[m, k] * W[n, k]  (+ bias[n])
+ *   u[m, n] = sx[m] * swu[n] * sum_k Xq[m, k] * Wu[n, k]  (+ biasu[n])
+ *   Y[m, n] = act(z[m, n]) * u[m, n]
+ * in f32, rounded once to Y's type.
+ *   Z, ldz and U, ldu  [M, N] of Y's type, or NULL: receive z and u, rounded.
+ * M * 2 N counts against GEMMQ_I8_MAX_OUTPUTS.
+ * Errors: as gemmq_gemm_i8_act.
+ */
+int gemmq_gemm_i8_gate(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Wu,
+                       int64_t ldwu, const float *swu, const int8_t *Xq, int64_t ldq,
+                       const float *sx, const float *bias, const float *biasu, int act, int ytype,
+                       void *Y, int64_t ldy, void *Z, int64_t ldz, void *U, int64_t ldu, int64_t M,
+                       int64_t N, int64_t K, void *stream);
+
+/* Quantize X into Xq and sx, then gemmq_gemm_i8_gate: the same bits as the two calls. */
+int gemmq_linear_i8_gate(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Wu,
+                         int64_t ldwu, const float *swu, int xtype, const void *X, int64_t ldx,
+                         int8_t *Xq, int64_t ldq, float *sx, const float *bias, const float *biasu,
+                         int act, int ytype, void *Y, int64_t ldy, void *Z, int64_t ldz, void *U,
+                         int64_t ldu, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* Workspace bytes of gemmq_act_grad with a db or dbu (0 for arguments it refuses;
+   without them no workspace is needed). */
+size_t gemmq_act_grad_workspace(int type, int64_t M, int64_t N);
+
+/*
+ * The gradients behind the two products above, which gemmq_linear_i8_grad takes on to
+ * the activations:
+ *   without U:  dZ = dY act'(Z)
+ *   with U:     dZ = dY U act'(Z),  dU = dY act(Z)
+ *   db[n] = sum_m dZ[m, n],  dbu[n] = sum_m dU[m, n]   of the values before their rounding
+ * (relu' (0) = 0; the residual's gradient is dY itself).
+ *   type  of Z, U, dY, dZ and dU, all [M, N].   U and dU  both or neither (NULL).
+ *   dZ    may be Z or dY itself, dU may be U or dY itself, not both dY (the same
+ *         pointer and pitch).
+ *   db, dbu  f32 [N], overwritten (zeros where M == 0), or NULL: not computed; dbu
+ *         only with U.
+ *   ws    may be NULL where db and dbu are.
+ * Errors: as gemmq_quantize_i8, and GEMMQ_E_INVALID_ARG for an unknown act, one of U
+ *         and dU alone, a dbu without U, or a workspace that is too small.
+ */
+int gemmq_act_grad(int act, int type, const void *Z, int64_t ldz, const void *U, int64_t ldu,
+                   const void *dY, int64_t lddy, void *dZ, int64_t lddz, void *dU, int64_t lddu,
+                   float *db, float *dbu, int64_t M, int64_t N, void *ws, size_t ws_bytes,
+                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif

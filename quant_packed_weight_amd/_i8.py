@@ -48,6 +48,17 @@ EXPORTS_I8 = {
     "gemmq_rms_i8_grad_workspace": (_S, [_I, _I64, _I64]),
     "gemmq_rms_i8_grad": (_I, [_I, _P, _I64, _P, _F, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64,
                                _P, _S, _P]),
+    "gemmq_gemm_i8_act": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I, _P, _I64, _I, _P, _I64, _P, _I64,
+                               _I64, _I64, _I64, _P]),
+    "gemmq_linear_i8_act": (_I, [_P, _I64, _P, _I, _P, _I64, _P, _I64, _P, _P, _I, _P, _I64, _I, _P,
+                                 _I64, _P, _I64, _I64, _I64, _I64, _P]),
+    "gemmq_gemm_i8_gate": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I, _I, _P, _I64,
+                                _P, _I64, _P, _I64, _I64, _I64, _I64, _P]),
+    "gemmq_linear_i8_gate": (_I, [_P, _I64, _P, _P, _I64, _P, _I, _P, _I64, _P, _I64, _P, _P, _P,
+                                  _I, _I, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]),
+    "gemmq_act_grad_workspace": (_S, [_I, _I64, _I64]),
+    "gemmq_act_grad": (_I, [_I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64,
+                            _I64, _P, _S, _P]),
 }
 
 _fns = None

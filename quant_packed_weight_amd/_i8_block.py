@@ -92,3 +92,145 @@ def rms_i8_grad_workspace(dtype, M, K):
     """Bytes of rms_i8_grad's workspace for rows of `dtype` [M, K] with a dw."""
     L = lib_i8()
     return L.gemmq_rms_i8_grad_workspace(_type(dtype, "dtype"), M, K)
+
+
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)  # GEMMQ_ACT_*
+
+
+def _act_product(name, w, sw, pair, x, xq, sx, bias, act, residual, pre, up, out, out_dtype):
+    """The product of gemm_i8_act (x None) or linear_i8_act, or with pair = (wu, swu, bias_up)
+    of their gated forms, on the current stream."""
+    L = _i8._fns
+    dev = w.get_device()
+    N, K = w.shape
+    M = (xq if x is None else x).shape[0]
+    torch = _i8._torch
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or (f32 if x is None else x.dtype), device=w.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+    dt = out.dtype
+    args = [w.data_ptr(), _i8_matrix(w, "w", N, K, dev), _vector(sw, "sw", f32, N, dev)]
+    if pair is not None:
+        wu, swu, bias_up = pair
+        args += [wu.data_ptr(), _i8_matrix(wu, "wu", N, K, dev), _vector(swu, "swu", f32, N, dev)]
+    if x is not None:
+        if xq is None:
+            xq = _new_i8(M, K, w.device)
+        if sx is None:
+            sx = torch.empty(M, dtype=f32, device=w.device)
+        args += [_type(x.dtype, "x"), x.data_ptr(), _matrix(x, "x", None, M, K, dev)]
+    args += [xq.data_ptr(), _i8_matrix(xq, "xq", M, K, dev), _vector(sx, "sx", f32, M, dev),
+             None if bias is None else _vector(bias, "bias", f32, N, dev)]
+    if pair is not None:
+        args += [None if bias_up is None else _vector(bias_up, "bias_up", f32, N, dev), act]
+    else:
+        args += [act, *_optional(residual, "residual", dt, M, N, dev)]
+    args += [_type(dt, "out"), out.data_ptr(), _matrix(out, "out", None, M, N, dev),
+             *_optional(pre, "pre", dt, M, N, dev)]
+    if pair is not None:
+        args += _optional(up, "up", dt, M, N, dev)
+    _check(getattr(L, name)(*args, M, N, K, _here(dev)), name)
+    return out
+
+
+def gemm_i8_act(w, sw, xq, sx, act, bias=None, residual=None, pre=None, out=None, out_dtype=None,
+                stream=None):
+    """act(z) + residual with z = (sx xq) (sw w)^T + bias (gemmq_gemm_i8_act), act one of
+    ACT_*: f32, bf16 or f16 [M, N] (`out_dtype`, f32 by default).  residual and pre are of
+    the result's type; residual may be `out` itself, and pre, when given, receives z."""
+    _i8._fns or lib_i8()
+    _tracked(sw, sx, bias, residual)
+    at = _elsewhere(w, w.get_device(), stream)
+    if at is not None:
+        with at:
+            return gemm_i8_act(w, sw, xq, sx, act, bias, residual, pre, out, out_dtype)
+    return _act_product("gemmq_gemm_i8_act", w, sw, None, None, xq, sx, bias, act, residual, pre,
+                        None, out, out_dtype)
+
+
+def linear_i8_act(w, sw, x, act, bias=None, residual=None, pre=None, out=None, out_dtype=None,
+                  xq=None, sx=None, stream=None):
+    """gemm_i8_act on activations x (f32, bf16 or f16 [M, K]), quantized per token
+    (gemmq_linear_i8_act): [M, N] in `out_dtype` (x's by default)."""
+    _i8._fns or lib_i8()
+    _tracked(sw, x, bias, residual)
+    at = _elsewhere(w, w.get_device(), stream)
+    if at is not None:
+        with at:
+            return linear_i8_act(w, sw, x, act, bias, residual, pre, out, out_dtype, xq, sx)
+    return _act_product("gemmq_linear_i8_act", w, sw, None, x, xq, sx, bias, act, residual, pre,
+                        None, out, out_dtype)
+
+
+def gemm_i8_gate(w, sw, wu, swu, xq, sx, act=ACT_SILU, bias=None, bias_up=None, pre=None, up=None,
+                 out=None, out_dtype=None, stream=None):
+    """act(z) u for the products z and u of two int8 matrices [N, K] with the same
+    activations (gemmq_gemm_i8_gate); pre and up, when given, receive z and u."""
+    _i8._fns or lib_i8()
+    _tracked(sw, swu, sx, bias, bias_up)
+    at = _elsewhere(w, w.get_device(), stream)
+    if at is not None:
+        with at:
+            return gemm_i8_gate(w, sw, wu, swu, xq, sx, act, bias, bias_up, pre, up, out, out_dtype)
+    return _act_product("gemmq_gemm_i8_gate", w, sw, (wu, swu, bias_up), None, xq, sx, bias, act,
+                        None, pre, up, out, out_dtype)
+
+
+def linear_i8_gate(w, sw, wu, swu, x, act=ACT_SILU, bias=None, bias_up=None, pre=None, up=None,
+                   out=None, out_dtype=None, xq=None, sx=None, stream=None):
+    """gemm_i8_gate on activations x (f32, bf16 or f16 [M, K]), quantized per token
+    (gemmq_linear_i8_gate): the gate and up projections of a feed-forward block."""
+    _i8._fns or lib_i8()
+    _tracked(sw, swu, x, bias, bias_up)
+    at = _elsewhere(w, w.get_device(), stream)
+    if at is not None:
+        with at:
+            return linear_i8_gate(w, sw, wu, swu, x, act, bias, bias_up, pre, up, out, out_dtype,
+                                  xq, sx)
+    return _act_product("gemmq_linear_i8_gate", w, sw, (wu, swu, bias_up), x, xq, sx, bias, act,
+                        None, pre, up, out, out_dtype)
+
+
+def act_grad(act, z, dy, up=None, out=None, dup=None, dbias=None, dbias_up=None, workspace=None,
+             stream=None):
+    """The gradients behind linear_i8_act and, with `up`, linear_i8_gate (gemmq_act_grad):
+    dz = dy act'(z), or dz = dy up act'(z) and dup = dy act(z), for linear_i8_grad to take
+    on.  z, dy and up [M, N] of one type.  Returns (dz, dup), dup None without `up`; dbias
+    and dbias_up, when given, f32 [N], receive the sums of dz and dup over the rows.
+    `workspace`: at least act_grad_workspace bytes, or None."""
+    L = _i8._fns or lib_i8()
+    _tracked(z, dy, up)
+    dev = z.get_device()
+    at = _elsewhere(z, dev, stream)
+    if at is not None:
+        with at:
+            return act_grad(act, z, dy, up, out, dup, dbias, dbias_up, workspace)
+    M, N = z.shape
+    torch = _i8._torch
+    dt, f32 = z.dtype, torch.float32
+    ty = _type(dt, "z")
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=z.device)
+    if dup is None and up is not None:
+        dup = torch.empty((M, N), dtype=dt, device=z.device)
+    ws = None
+    if dbias is not None or dbias_up is not None:
+        ws = _workspace(workspace, L.gemmq_act_grad_workspace(ty, M, N), z.device)
+    u, ldu = _optional(up, "up", dt, M, N, dev)
+    du, lddu = _optional(dup, "dup", dt, M, N, dev)
+    _check(L.gemmq_act_grad(
+        act, ty, z.data_ptr(), _matrix(z, "z", dt, M, N, dev), u, ldu, dy.data_ptr(),
+        _matrix(dy, "dy", dt, M, N, dev), out.data_ptr(), _matrix(out, "out", dt, M, N, dev), du,
+        lddu, None if dbias is None else _vector(dbias, "dbias", f32, N, dev),
+        None if dbias_up is None else _vector(dbias_up, "dbias_up", f32, N, dev), M, N,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _here(dev)),
+        "gemmq_act_grad")
+    return out, dup
+
+
+def act_grad_workspace(dtype, M, N):
+    """Bytes of act_grad's workspace for [M, N] of `dtype`, with a bias's gradient."""
+    L = lib_i8()
+    return L.gemmq_act_grad_workspace(_type(dtype, "dtype"), M, N)

@@ -39,5 +39,40 @@ int launch_rms_grad(const RmsGradArgs& a, hipStream_t st);
 // out[k] = the sum of `count` rows of part, in a fixed order (count 0: zeros)
 int launch_join(const float* part, int64_t pitch, int count, float* out, int K, hipStream_t st);
 
+// The product with an activation, and the gated pair of products (i8_act.hip):
+// y = act(z) (+ r), or act(z) u.  A matrix of results or residuals has 16-bit rows that
+// can be accessed eight values at a time (`lines`, 16 bytes) and, in any type, four
+// (`wide`).
+struct Rows {
+  void* p;  // null: left out
+  int64_t ld;
+  bool wide, lines;
+};
+struct ActOut {
+  const float *bias, *biasu;  // may be null
+  const int8_t* Wu;           // the second matrix of a pair, with its scales
+  const float* swu;
+  int64_t ldwu;
+  Rows R, Y, Z, U;
+  int act, type;
+};
+// rows of W that a launch goes through: N, 2 N of a pair (`pair`: of ActOut::Wu)
+int launch_act(const Operands& op, const ActOut& out, bool pair, hipStream_t st);
+bool act_fits(int M, int N, int K, bool pair);
+bool act_fuses(int M, int N, int K, bool pair);
+int launch_act_fused(int xtype, const void* X, int64_t ldx, const Operands& op, const ActOut& out,
+                     bool pair, hipStream_t st);
+
+// i8_act_grad.hip: dZ = dY act'(Z), or with U dZ = dY U act'(Z) and dU = dY act(Z);
+// part (or null) receives [2 of a pair][act_grad_groups][np] sums over rows.
+struct ActGradArgs {
+  Rows Z, U, dY, dZ, dU;  // U, dU null: no pair
+  float* part;
+  int64_t np;  // N rounded up to a multiple of 4
+  int act, type, M, N, groups;
+};
+int act_grad_groups(int type, int64_t M, int64_t N);  // with sums over rows
+int launch_act_grad(ActGradArgs a, hipStream_t st);
+
 }  // namespace i8
 }  // namespace gemmq

@@ -22,6 +22,87 @@ int check_optional(int type, const void* p, int64_t ld, int64_t width) {
   return p ? check_rows(type, p, ld, width) : GEMMQ_OK;
 }
 
+bool known_act(int act) { return act >= GEMMQ_ACT_NONE && act <= GEMMQ_ACT_RELU; }
+
+Rows rows(int type, const void* p, int64_t ld) {
+  return {const_cast<void*>(p), ld, ld % 4 == 0 && aligned(p, (uintptr_t)(4 * type_bytes(type))),
+          wide_rows(p, ld, type)};
+}
+
+// A second int8 matrix, its scales and its bias, and what receives its products
+struct Pair {
+  const int8_t* W;
+  int64_t ldw;
+  const float *sw, *bias;
+  void* U;
+  int64_t ldu;
+};
+
+// Everything of a product with an activation (pair null) or of a gated pair but the
+// quantizer's input; `empty` where there is nothing to compute.
+int check_act(const int8_t* W, int64_t ldw, const float* sw, const Pair* pair, const int8_t* Xq,
+              int64_t ldq, const float* sx, const float* bias, int act, const void* R, int64_t ldr,
+              int ytype, void* Y, int64_t ldy, void* Z, int64_t ldz, int64_t M, int64_t N,
+              int64_t K, Operands& op, ActOut& out, bool& empty) {
+  int rc = check_shape(M, N, K);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(ytype) || !known_act(act)) return GEMMQ_E_INVALID_ARG;
+  empty = M == 0 || N == 0;
+  if (empty) return GEMMQ_OK;
+  rc = check_i8(W, ldw, sw, K);
+  if (rc == GEMMQ_OK && pair) rc = check_i8(pair->W, pair->ldw, pair->sw, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc == GEMMQ_OK) rc = check_rows(ytype, Y, ldy, N);
+  if (rc == GEMMQ_OK) rc = check_optional(ytype, R, ldr, N);
+  if (rc == GEMMQ_OK) rc = check_optional(ytype, Z, ldz, N);
+  if (rc == GEMMQ_OK && pair) rc = check_optional(ytype, pair->U, pair->ldu, N);
+  if (rc != GEMMQ_OK) return rc;
+  if (!aligned(bias, 4) || (pair && !aligned(pair->bias, 4))) return GEMMQ_E_ALIGNMENT;
+  if (!same_rows(Y, ldy, R, ldr, M)) return GEMMQ_E_INVALID_ARG;
+  if (!act_fits((int)M, (int)N, (int)K, pair != nullptr)) return GEMMQ_E_SHAPE;
+  op = Operands{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
+  out = ActOut{};
+  out.bias = bias;
+  out.R = rows(ytype, R, ldr);
+  out.Y = rows(ytype, Y, ldy);
+  out.Z = rows(ytype, Z, ldz);
+  out.act = act;
+  out.type = ytype;
+  if (pair) {
+    out.biasu = pair->bias;
+    out.Wu = pair->W;
+    out.ldwu = pair->ldw;
+    out.swu = pair->sw;
+    out.U = rows(ytype, pair->U, pair->ldu);
+  }
+  return GEMMQ_OK;
+}
+
+int run_gemm(const Operands& op, const ActOut& out, bool pair, hipStream_t st) {
+  const int rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  clear_pending();
+  return launched(launch_act(op, out, pair, st));
+}
+
+// the same with the quantizer before it or in the same launch
+int run_linear(int xtype, const void* X, int64_t ldx, int8_t* Xq, int64_t ldq, float* sx, int64_t M,
+               int64_t K, bool empty, const Operands& op, const ActOut& out, bool pair,
+               hipStream_t st) {
+  if (!known(xtype)) return GEMMQ_E_INVALID_ARG;
+  if (M == 0) return GEMMQ_OK;
+  int rc = check_rows(xtype, X, ldx, K);
+  if (rc == GEMMQ_OK) rc = check_i8(Xq, ldq, sx, K);
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  clear_pending();
+  if (!empty && act_fuses(op.M, op.N, op.K, pair))
+    return launched(launch_act_fused(xtype, X, ldx, op, out, pair, st));
+  rc = launched(launch_quantize(xtype, X, ldx, Xq, ldq, sx, (int)M, (int)K, st));
+  if (rc != GEMMQ_OK || empty) return rc;
+  return launched(launch_act(op, out, pair, st));
+}
+
 bool eps_ok(float eps) { return eps >= 0.0f && eps < __builtin_inff(); }
 
 }  // namespace
@@ -96,6 +177,113 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
   rc = launched(launch_rms_grad(a, st));
   if (rc != GEMMQ_OK || !dw) return rc;
   return launched(launch_join(part, kp, rms_grad_groups(M), dw, (int)K, st));
+}
+
+int gemmq_gemm_i8_act(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
+                      const float* sx, const float* bias, int act, const void* R, int64_t ldr,
+                      int ytype, void* Y, int64_t ldy, void* Z, int64_t ldz, int64_t M, int64_t N,
+                      int64_t K, void* stream) {
+  Operands op;
+  ActOut out;
+  bool empty;
+  const int rc = check_act(W, ldw, sw, nullptr, Xq, ldq, sx, bias, act, R, ldr, ytype, Y, ldy, Z,
+                           ldz, M, N, K, op, out, empty);
+  if (rc != GEMMQ_OK || empty) return rc;
+  return run_gemm(op, out, false, static_cast<hipStream_t>(stream));
+}
+
+int gemmq_linear_i8_act(const int8_t* W, int64_t ldw, const float* sw, int xtype, const void* X,
+                        int64_t ldx, int8_t* Xq, int64_t ldq, float* sx, const float* bias,
+                        int act, const void* R, int64_t ldr, int ytype, void* Y, int64_t ldy,
+                        void* Z, int64_t ldz, int64_t M, int64_t N, int64_t K, void* stream) {
+  Operands op;
+  ActOut out;
+  bool empty;
+  const int rc = check_act(W, ldw, sw, nullptr, Xq, ldq, sx, bias, act, R, ldr, ytype, Y, ldy, Z,
+                           ldz, M, N, K, op, out, empty);
+  if (rc != GEMMQ_OK) return rc;
+  return run_linear(xtype, X, ldx, Xq, ldq, sx, M, K, empty, op, out, false,
+                    static_cast<hipStream_t>(stream));
+}
+
+int gemmq_gemm_i8_gate(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Wu,
+                       int64_t ldwu, const float* swu, const int8_t* Xq, int64_t ldq,
+                       const float* sx, const float* bias, const float* biasu, int act, int ytype,
+                       void* Y, int64_t ldy, void* Z, int64_t ldz, void* U, int64_t ldu, int64_t M,
+                       int64_t N, int64_t K, void* stream) {
+  Operands op;
+  ActOut out;
+  bool empty;
+  const Pair pair{Wu, ldwu, swu, biasu, U, ldu};
+  const int rc = check_act(W, ldw, sw, &pair, Xq, ldq, sx, bias, act, nullptr, 0, ytype, Y, ldy, Z,
+                           ldz, M, N, K, op, out, empty);
+  if (rc != GEMMQ_OK || empty) return rc;
+  return run_gemm(op, out, true, static_cast<hipStream_t>(stream));
+}
+
+int gemmq_linear_i8_gate(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Wu,
+                         int64_t ldwu, const float* swu, int xtype, const void* X, int64_t ldx,
+                         int8_t* Xq, int64_t ldq, float* sx, const float* bias, const float* biasu,
+                         int act, int ytype, void* Y, int64_t ldy, void* Z, int64_t ldz, void* U,
+                         int64_t ldu, int64_t M, int64_t N, int64_t K, void* stream) {
+  Operands op;
+  ActOut out;
+  bool empty;
+  const Pair pair{Wu, ldwu, swu, biasu, U, ldu};
+  const int rc = check_act(W, ldw, sw, &pair, Xq, ldq, sx, bias, act, nullptr, 0, ytype, Y, ldy, Z,
+                           ldz, M, N, K, op, out, empty);
+  if (rc != GEMMQ_OK) return rc;
+  return run_linear(xtype, X, ldx, Xq, ldq, sx, M, K, empty, op, out, true,
+                    static_cast<hipStream_t>(stream));
+}
+
+size_t gemmq_act_grad_workspace(int type, int64_t M, int64_t N) {
+  if (!known(type) || check_shape(M, N, 1) != GEMMQ_OK || M == 0 || N == 0) return 0;
+  return align_up(8 * act_grad_groups(type, M, N) * (int64_t)align_up(N, 4), 256);
+}
+
+int gemmq_act_grad(int act, int type, const void* Z, int64_t ldz, const void* U, int64_t ldu,
+                   const void* dY, int64_t lddy, void* dZ, int64_t lddz, void* dU, int64_t lddu,
+                   float* db, float* dbu, int64_t M, int64_t N, void* ws, size_t ws_bytes,
+                   void* stream) {
+  int rc = check_shape(M, N, 1);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(type) || !known_act(act)) return GEMMQ_E_INVALID_ARG;
+  // (a matrix without rows may have no address)
+  if (M > 0 && (!U != !dU || (dbu && !U))) return GEMMQ_E_INVALID_ARG;
+  if (!aligned(db, 4) || !aligned(dbu, 4)) return GEMMQ_E_ALIGNMENT;
+  const bool sums = db || dbu;
+  if (N == 0 || (M == 0 && !sums)) return GEMMQ_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (M > 0) {
+    rc = check_rows(type, Z, ldz, N);
+    if (rc == GEMMQ_OK) rc = check_rows(type, dY, lddy, N);
+    if (rc == GEMMQ_OK) rc = check_rows(type, dZ, lddz, N);
+    if (rc == GEMMQ_OK) rc = check_optional(type, U, ldu, N);
+    if (rc == GEMMQ_OK) rc = check_optional(type, dU, lddu, N);
+    if (rc != GEMMQ_OK) return rc;
+    if (!same_rows(dZ, lddz, Z, ldz, M) || !same_rows(dZ, lddz, dY, lddy, M) ||
+        !same_rows(dU, lddu, U, ldu, M) || !same_rows(dU, lddu, dY, lddy, M) || dZ == dU)
+      return GEMMQ_E_INVALID_ARG;
+    if (sums) rc = check_ws(ws, ws_bytes, gemmq_act_grad_workspace(type, M, N));
+  }
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  clear_pending();
+  float* part = sums && M > 0 ? static_cast<float*>(ws) : nullptr;
+  const int64_t np = (int64_t)align_up(N, 4);
+  const int groups = part ? act_grad_groups(type, M, N) : 0;
+  if (M > 0) {
+    const ActGradArgs a{rows(type, Z, ldz),   rows(type, U, ldu), rows(type, dY, lddy),
+                        rows(type, dZ, lddz), rows(type, dU, lddu), part, np, act, type,
+                        (int)M, (int)N, 0};
+    rc = launched(launch_act_grad(a, st));
+    if (rc != GEMMQ_OK) return rc;
+  }
+  if (db) rc = launched(launch_join(part, np, groups, db, (int)N, st));
+  if (rc == GEMMQ_OK && dbu)
+    rc = launched(launch_join(part ? part + groups * np : nullptr, np, groups, dbu, (int)N, st));
+  return rc;
 }
 
 }  // extern "C"

@@ -17,7 +17,7 @@ typedef __bf16 bf16_t;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // what a product's kernel does with its sums
-enum Epilogue { kLinear, kLoss, kFactor };
+enum Epilogue { kLinear, kLoss, kFactor, kAct, kGate };
 
 // f32 -> the type's 16 bits, round to nearest even
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
@@ -66,6 +66,37 @@ __device__ __forceinline__ void store4_as(void* p, int64_t i, int type, bool wid
   if (count > 1) store_as(p, i + 1, type, v1);
   if (count > 2) store_as(p, i + 2, type, v2);
   if (count > 3) store_as(p, i + 3, type, v3);
+}
+
+// the values of two 16-bit halves of a word, bf16 or f16
+__device__ __forceinline__ float2 halves(uint32_t w, int type) {
+  if (type == GEMMQ_BF16)
+    return make_float2(__builtin_bit_cast(float, w << 16),
+                       __builtin_bit_cast(float, w & 0xffff0000u));
+  return make_float2((float)__builtin_bit_cast(_Float16, (uint16_t)w),
+                     (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)));
+}
+// two values as such a word, rounded
+__device__ __forceinline__ uint32_t two_bits(float a, float b, int type) {
+  return type == GEMMQ_BF16 ? bf16_bits(a) | bf16_bits(b) << 16 : f16_bits(a) | f16_bits(b) << 16;
+}
+
+// four consecutive values of a row from element i, as store4_as; zero past `count`
+__device__ __forceinline__ void load4_as(const void* p, int64_t i, int type, bool wide, int count,
+                                         float (&v)[4]) {
+  if (wide && count >= 4) {
+    if (type == GEMMQ_F32) {
+      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      const float2 lo = halves(x.x, type), hi = halves(x.y, type);
+      v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = e < count ? load_as_f32(p, i + e, type) : 0.0f;
 }
 
 // The next bf16 of v's expansion, its top 16 bits, and what is left of v: both
@@ -210,6 +241,53 @@ template <int TYPE, int V>
 __device__ __forceinline__ void load_values(const void* p, int64_t i, int64_t left, bool wide,
                                             float (&v)[V]) {
   unpack<TYPE, V>(load_raw<TYPE>(p, i, left, wide), v);
+}
+
+// how many values of a row 16 bytes hold
+template <int TYPE>
+constexpr int kValues = TYPE == GEMMQ_F32 ? 4 : 8;
+
+// f32 values as 16 bytes of a row, rounded to its type
+template <int TYPE, int V>
+__device__ __forceinline__ uint4 pack(const float (&v)[V]) {
+  static_assert(V == kValues<TYPE>, "16 bytes");
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (TYPE == GEMMQ_F32)
+      u[i] = __builtin_bit_cast(uint32_t, v[i]);
+    else if constexpr (TYPE == GEMMQ_BF16)
+      u[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+    else
+      u[i] = f16_bits(v[2 * i]) | f16_bits(v[2 * i + 1]) << 16;
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// 16 bytes to a row from element i on, those of its first `left` values
+template <int TYPE>
+__device__ __forceinline__ void store_raw(void* p, int64_t i, int left, bool wide, uint4 w) {
+  constexpr int V = kValues<TYPE>;
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if constexpr (TYPE == GEMMQ_F32) {
+    uint32_t* to = static_cast<uint32_t*>(p) + i;
+    if (wide && left >= V) {
+      *reinterpret_cast<uint4*>(to) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < left) to[e] = u[e];
+    }
+  } else {
+    uint16_t* to = static_cast<uint16_t*>(p) + i;
+    if (wide && left >= V) {
+      *reinterpret_cast<uint4*>(to) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < left) to[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+    }
+  }
 }
 
 // V quantized values as bytes, zero in a row whose scale is 0 or NaN

@@ -12,10 +12,6 @@ namespace gemmq {
 namespace i8 {
 namespace {
 
-// 16 bytes of a row from element k on, as the loads of i8_common.h take them
-template <int TYPE>
-constexpr int kValues = TYPE == GEMMQ_F32 ? 4 : 8;
-
 // V values of an f32 vector from element k on, zero from element `end` on
 template <int V>
 __device__ __forceinline__ void load_vector(const float* w, int k, int end, bool wide,
@@ -26,49 +22,6 @@ __device__ __forceinline__ void load_vector(const float* w, int k, int end, bool
     load_values<GEMMQ_F32, 4>(w, k + i, end - (k + i), wide, four);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[i + e] = four[e];
-  }
-}
-
-// f32 values as 16 bytes of a row, rounded to its type
-template <int TYPE, int V>
-__device__ __forceinline__ uint4 pack(const float (&v)[V]) {
-  static_assert(V == kValues<TYPE>, "16 bytes");
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (TYPE == GEMMQ_F32)
-      u[i] = __builtin_bit_cast(uint32_t, v[i]);
-    else if constexpr (TYPE == GEMMQ_BF16)
-      u[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
-    else
-      u[i] = f16_bits(v[2 * i]) | f16_bits(v[2 * i + 1]) << 16;
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-// 16 bytes to a row from element i on, those of its first `left` values
-template <int TYPE>
-__device__ __forceinline__ void store_raw(void* p, int64_t i, int left, bool wide, uint4 w) {
-  constexpr int V = kValues<TYPE>;
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  if constexpr (TYPE == GEMMQ_F32) {
-    uint32_t* to = static_cast<uint32_t*>(p) + i;
-    if (wide && left >= V) {
-      *reinterpret_cast<uint4*>(to) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < left) to[e] = u[e];
-    }
-  } else {
-    uint16_t* to = static_cast<uint16_t*>(p) + i;
-    if (wide && left >= V) {
-      *reinterpret_cast<uint4*>(to) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < left) to[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
-    }
   }
 }
 
