@@ -292,6 +292,41 @@ int gemmq_act_grad(int act, int type, const void *Z, int64_t ldz, const void *U,
                    float *db, float *dbu, int64_t M, int64_t N, void *ws, size_t ws_bytes,
                    void *stream);
 
+/* Workspace bytes of gemmq_sample (0 for arguments it refuses). */
+size_t gemmq_sample_workspace(int64_t M, int64_t N);
+
+/*
+ * One token a row from its logits, with the row's own settings and random number.
+ * The tokens of a row stand in the order of their logits, the largest first, equal
+ * ones (+0 and -0 are equal) by their index, with the weights
+ *   e = exp((z - max z) / temperature)
+ * and the first of them are kept: no more than
+ *   top_k  of them (<= 0: no limit);
+ *   top_p  < 1: the fewest whose weights' sum is at least top_p times that of all
+ *          that top_k leaves (<= 0: one; >= 1 or NaN: no limit);
+ *   min_p  > 0: those with e >= min_p (above 1 as 1; NaN: no limit);
+ * one at least.  Of these the token is the first where the running sum of the weights
+ * is more than u times their whole sum.
+ * temperature <= 0: the largest logit, whatever the rest says.
+ *   Z, ldz       [M, N], N >= 1 (GEMMQ_E_SHAPE otherwise).  -inf takes a token out.
+ *   temperature, top_p, min_p  f32 [M], top_k  int32 [M]; each may be NULL: 1, and no
+ *                limits.
+ *   u            f32 [M], in [0, 1) (below 0 or NaN as 0, from 1 on as the largest f32
+ *                below 1).
+ *   token        int64 [M].   logprob  f32 [M] or NULL: the logarithm of the token's
+ *                share of the kept tokens' weights.
+ * A row without a token to draw (a NaN, a +inf, nothing but -inf, or a temperature
+ * that is NaN or +inf) has token -1 and logprob NaN.
+ * Weights are fixed-point numbers with 62 - ceil(log2 N) bits (50 at most) behind the
+ * point, the largest one 1, and their sums are exact: a result does not depend on the order
+ * of anything.  A weight below half a unit is zero, and drawn by no u.
+ * Errors: as gemmq_loss_i8.
+ */
+int gemmq_sample(int type, const void *Z, int64_t ldz, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                 int64_t *token, float *logprob, int64_t M, int64_t N, void *ws, size_t ws_bytes,
+                 void *stream);
+
 #ifdef __cplusplus
 }
 #endif

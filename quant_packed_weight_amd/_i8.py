@@ -59,6 +59,8 @@ EXPORTS_I8 = {
     "gemmq_act_grad_workspace": (_S, [_I, _I64, _I64]),
     "gemmq_act_grad": (_I, [_I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64,
                             _I64, _P, _S, _P]),
+    "gemmq_sample_workspace": (_S, [_I64, _I64]),
+    "gemmq_sample": (_I, [_I, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _S, _P]),
 }
 
 _fns = None

@@ -234,3 +234,41 @@ def act_grad_workspace(dtype, M, N):
     """Bytes of act_grad's workspace for [M, N] of `dtype`, with a bias's gradient."""
     L = lib_i8()
     return L.gemmq_act_grad_workspace(_type(dtype, "dtype"), M, N)
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprob=None,
+           workspace=None, stream=None):
+    """One token a row of logits (f32, bf16 or f16 [M, N]; gemmq_sample) from the random
+    numbers u, f32 [M] in [0, 1).  Each row's settings, or None: temperature (<= 0 greedy),
+    top_p and min_p f32 [M], top_k int32 [M].  Returns (token int64 [M], logprob f32 [M]):
+    the logarithm of the token's share of what the settings leave; -1 and NaN for a row
+    without a token to draw.  `workspace`: at least sample_workspace bytes, or None."""
+    L = _i8._fns or lib_i8()
+    _tracked(logits, u, temperature, top_p, min_p)
+    dev = logits.get_device()
+    at = _elsewhere(logits, dev, stream)
+    if at is not None:
+        with at:
+            return sample(logits, u, temperature, top_k, top_p, min_p, out, logprob, workspace)
+    M, N = logits.shape
+    torch = _i8._torch
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty(M, dtype=torch.int64, device=logits.device)
+    if logprob is None:
+        logprob = torch.empty(M, dtype=f32, device=logits.device)
+    ws = _workspace(workspace, L.gemmq_sample_workspace(M, N), logits.device)
+    _check(L.gemmq_sample(
+        _type(logits.dtype, "logits"), logits.data_ptr(), _matrix(logits, "logits", None, M, N, dev),
+        None if temperature is None else _vector(temperature, "temperature", f32, M, dev),
+        None if top_k is None else _vector(top_k, "top_k", torch.int32, M, dev),
+        None if top_p is None else _vector(top_p, "top_p", f32, M, dev),
+        None if min_p is None else _vector(min_p, "min_p", f32, M, dev), _vector(u, "u", f32, M, dev),
+        _vector(out, "out", torch.int64, M, dev), _vector(logprob, "logprob", f32, M, dev), M, N,
+        ws.data_ptr(), ws.nbytes, _here(dev)), "gemmq_sample")
+    return out, logprob
+
+
+def sample_workspace(M, N):
+    """Bytes of sample's workspace for logits [M, N]."""
+    return lib_i8().gemmq_sample_workspace(M, N)

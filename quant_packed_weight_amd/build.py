@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libgemmq.so")
 SOURCES = ["abi.hip", "quantize.hip", "gemv.hip", "gemm.hip", "gemm_q4k.hip", "gemm_q6k.hip", "decode.hip",
            "repack.hip", "probe.hip", "skinny.hip", "skinny_q6k.hip", "i8_abi.hip", "i8_quantize.hip",
            "i8_gemm.hip", "i8_skinny.hip", "i8_grad.hip", "i8_act.hip", "i8_act_grad.hip",
-           "i8_block_abi.hip", "i8_norm.hip"]
+           "i8_block_abi.hip", "i8_norm.hip", "i8_sample.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 CFLAGS = [

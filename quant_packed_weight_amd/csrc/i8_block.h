@@ -74,5 +74,31 @@ struct ActGradArgs {
 int act_grad_groups(int type, int64_t M, int64_t N);  // with sums over rows
 int launch_act_grad(ActGradArgs a, hipStream_t st);
 
+// i8_sample.hip: one token a row.  What the first launch leaves of a part of a row:
+struct SamplePart {
+  unsigned long long top;  // its largest logit's order and index
+  uint32_t low;            // its lowest finite logit's order
+  uint32_t bad;            // a NaN or +inf
+};
+struct SampleArgs {
+  const void* Z;
+  int64_t ldz;
+  const float *temperature, *top_p, *min_p;  // may be null
+  const int32_t* top_k;                      // may be null
+  const float* u;
+  int64_t* token;
+  float* logprob;  // may be null
+  int N;
+  bool wide;
+  // set by the launcher: a part's logits and their number, the bits of a weight, and the
+  // workspace
+  int chunk, chunks, bits;
+  SamplePart* part;
+  uint32_t *count, *listed;
+  unsigned long long *weight, *list;
+};
+size_t sample_workspace(int64_t M, int64_t N);
+int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st);
+
 }  // namespace i8
 }  // namespace gemmq

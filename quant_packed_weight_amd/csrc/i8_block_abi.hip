@@ -286,4 +286,43 @@ int gemmq_act_grad(int act, int type, const void* Z, int64_t ldz, const void* U,
   return rc;
 }
 
+size_t gemmq_sample_workspace(int64_t M, int64_t N) {
+  if (check_shape(M, N, 1) != GEMMQ_OK || M == 0 || N == 0) return 0;
+  return sample_workspace(M, N);
+}
+
+int gemmq_sample(int type, const void* Z, int64_t ldz, const float* temperature,
+                 const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                 int64_t* token, float* logprob, int64_t M, int64_t N, void* ws, size_t ws_bytes,
+                 void* stream) {
+  int rc = check_shape(M, N, 1);
+  if (rc != GEMMQ_OK) return rc;
+  if (!known(type)) return GEMMQ_E_INVALID_ARG;
+  if (N == 0) return GEMMQ_E_SHAPE;
+  if (M == 0) return GEMMQ_OK;
+  rc = check_rows(type, Z, ldz, N);
+  if (rc != GEMMQ_OK) return rc;
+  if (!u || !token) return GEMMQ_E_INVALID_ARG;
+  if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) ||
+      !aligned(u, 4) || !aligned(token, 8) || !aligned(logprob, 4))
+    return GEMMQ_E_ALIGNMENT;
+  rc = check_ws(ws, ws_bytes, gemmq_sample_workspace(M, N));
+  if (rc == GEMMQ_OK) rc = check_device();
+  if (rc != GEMMQ_OK) return rc;
+  SampleArgs a{};
+  a.Z = Z;
+  a.ldz = ldz;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.token = token;
+  a.logprob = logprob;
+  a.N = (int)N;
+  a.wide = wide_rows(Z, ldz, type);
+  clear_pending();
+  return launched(launch_sample(a, type, M, ws, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

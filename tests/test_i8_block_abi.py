@@ -34,7 +34,9 @@ LGATE = dict(W=A, ldw=112, sw=A, Wu=A, ldwu=112, swu=A, xtype=1, X=A, ldx=100, X
              K=100)
 AGRAD = dict(act=1, type=1, Z=A, ldz=50, U=A, ldu=50, dY=A, lddy=50, dZ=B, lddz=50, dU=2 * B,
              lddu=50, db=A, dbu=A, M=4, N=50, ws=A, bytes=1 << 40)
-ENTRIES = {"rms_i8": RMS, "rms_i8_grad": RGRAD, "gemm_i8_act": GEMM, "linear_i8_act": LINEAR,
+SAMPLE = dict(type=1, Z=A, ldz=50, temperature=A, top_k=A, top_p=A, min_p=A, u=A, token=A, logprob=A,
+              M=4, N=50, ws=A, bytes=1 << 40)
+ENTRIES = {"sample": SAMPLE, "rms_i8": RMS, "rms_i8_grad": RGRAD, "gemm_i8_act": GEMM, "linear_i8_act": LINEAR,
            "gemm_i8_gate": GATE, "linear_i8_gate": LGATE, "act_grad": AGRAD}
 _Y = [("Y", "ldy", "N", False), ("Z", "ldz", "N", True)]
 _X = [("X", "ldx", "K", False)]
@@ -46,6 +48,7 @@ MATRICES = {"rms_i8": [("X", "ldx", "K", False), ("R", "ldr", "K", True), ("H", 
             "linear_i8_act": _X + _Y + [("R", "ldr", "N", True)],
             "gemm_i8_gate": _Y + [("U", "ldu", "N", True)],
             "linear_i8_gate": _X + _Y + [("U", "ldu", "N", True)],
+            "sample": [("Z", "ldz", "N", False)],
             "act_grad": [("Z", "ldz", "N", False), ("dY", "lddy", "N", False),
                          ("dZ", "lddz", "N", False), ("U", "ldu", "N", True),
                          ("dU", "lddu", "N", True)]}
@@ -58,11 +61,14 @@ VECTORS = {"rms_i8": [("w", False), ("s", False)], "rms_i8_grad": [("w", False),
            "gemm_i8_act": _V, "linear_i8_act": _V,
            "gemm_i8_gate": _V + [("swu", False), ("biasu", True)],
            "linear_i8_gate": _V + [("swu", False), ("biasu", True)],
-           "act_grad": [("db", True), ("dbu", True)]}
+           "act_grad": [("db", True), ("dbu", True)],
+           "sample": [("temperature", True), ("top_k", True), ("top_p", True), ("min_p", True),
+                      ("u", False), ("token", False), ("logprob", True)]}
 OWN = {"rms_i8": [(dict(H=A, ldh=104, R=B), INVALID),            # X, but not as X lies
                   (dict(H=B, ldh=104, R=B), INVALID)],
        "rms_i8_grad": [(dict(dX=A, lddx=104, dH=B), INVALID), (dict(dX=B, lddx=104, dH=B), INVALID)],
        "gemm_i8_act": [(dict(R=B, ldr=52), INVALID)], "linear_i8_act": [(dict(R=B, ldr=52), INVALID)],
+       "sample": [(dict(N=0), SHAPE), (dict(token=A + 4), ALIGN)],
        "act_grad": [(dict(U=None), INVALID), (dict(dU=None), INVALID),
                     (dict(U=None, dU=None), INVALID),   # a dbu without a pair
                     (dict(dZ=A, lddz=52), INVALID), (dict(dU=A, lddu=52), INVALID),
@@ -133,6 +139,7 @@ def test_empty_calls(L):
         assert getattr(L, "gemmq_" + entry)(*dict(ENTRIES[entry], N=0).values(), None) == 0
     assert L.gemmq_act_grad(*dict(AGRAD, M=0, db=None, dbu=None).values(), None) == 0
     assert L.gemmq_act_grad(*dict(AGRAD, N=0).values(), None) == 0
+    assert L.gemmq_sample(*dict(SAMPLE, M=0).values(), None) == 0
 
 
 def test_products_that_no_launch_holds(L):
@@ -161,6 +168,16 @@ def test_workspace_sizes(L):
         assert L.gemmq_act_grad_workspace(*bad) == 0
 
 
+def test_sample_workspace(L):
+    need = L.gemmq_sample_workspace(4, 50)
+    assert need > 0 and gq.sample_workspace(4, 50) == need
+    assert L.gemmq_sample(*dict(SAMPLE, bytes=need - 1).values(), None) == INVALID
+    for bad in ((0, 50), (4, 0), (-1, 50), (4, -1), (gq.I8_MAX_ROWS + 1, 4), (4, gq.I8_MAX_ROWS + 1)):
+        assert L.gemmq_sample_workspace(*bad) == 0
+    # bounded for any number of rows
+    assert L.gemmq_sample_workspace(1 << 24, 151936) < 64 << 20
+
+
 def test_binding_refusals(L):
     import torch
 
@@ -181,7 +198,8 @@ def test_binding_refusals(L):
               lambda: gq.gemm_i8_gate(i, one, i, one, i4, o4, bias_up=l1),
               lambda: gq.linear_i8_gate(i, one, i, one, leaf),
               lambda: gq.act_grad(1, leaf, o), lambda: gq.act_grad(1, o, leaf),
-              lambda: gq.act_grad(1, o, o, up=leaf)]
+              lambda: gq.act_grad(1, o, o, up=leaf), lambda: gq.sample(leaf, o4),
+              lambda: gq.sample(o, l1[:4]), lambda: gq.sample(o, o4, temperature=l1[:4])]
     for call in calls:
         with pytest.raises(ValueError, match="record no gradient"):
             call()
