@@ -76,9 +76,8 @@ int launch_act_grad(ActGradArgs a, hipStream_t st);
 
 // i8_sample.hip: one token a row.  What the first launch leaves of a part of a row:
 struct SamplePart {
-  unsigned long long top;  // its largest logit's order and index
-  uint32_t low;            // its lowest finite logit's order
-  uint32_t bad;            // a NaN or +inf
+  float top, low;  // its largest logit, its lowest finite one (-inf, +inf: none)
+  uint32_t bad;    // a NaN or +inf
 };
 struct SampleArgs {
   const void* Z;
@@ -94,7 +93,7 @@ struct SampleArgs {
   // workspace
   int chunk, chunks, bits;
   SamplePart* part;
-  uint32_t *count, *listed;
+  uint32_t *count, *listed, *first;
   unsigned long long *weight, *list;
 };
 size_t sample_workspace(int64_t M, int64_t N);

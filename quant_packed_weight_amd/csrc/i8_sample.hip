@@ -6,17 +6,22 @@
 // count reaches k, where the sum of the weights reaches p of what that leaves, where the
 // weights fall below min_p, and where the sum passes u of what all of them leave.  A
 // histogram over the distance from the largest logit (a function of the logit that never
-// rises, so its bins are in that order) gives each place's bin; only those bins' tokens
-// are gathered and sorted.  Bounds of the sums that a limit leaves give a range of
-// bins where the one before it has not been resolved within its bin yet.
+// rises, so its bins are in that order) says which bins' tokens matter, and only those are
+// gathered and sorted:
+//   with a k of at most kListedK, all down to the k-th, by a histogram of counts: only those
+//   tokens' weights are ever computed;
+//   else by a histogram of weights, the bins that the places lie in.  Bounds of the sum that
+//   one limit leaves give the next one a range of bins.
 //
-// Four launches: the rows' maxima; the histograms; the gathering; the draw.  A row is
+// Four launches: the rows' largest logits; the histograms; the gathering; the draw.  A row is
 // spread over as many workgroups as fill the chip, but for the draw.
 //
-// Weights are integers, e = exp((z - max) / t) in units of 2^-s: their sums are exact, so
+// Weights are integers, e = exp((z - max) / t) in units of 2^-bits: their sums are exact, so
 // atomics may add them in any order.  e is computed in f64, to 10^-14: with f32's 10^-7 one
 // row in a few hundred of a flat distribution would draw the neighbour of the token that
 // the definition draws.
+#include <float.h>
+
 #include "i8_block.h"
 #include "i8_common.h"
 
@@ -29,6 +34,7 @@ typedef unsigned long long u64;
 constexpr int kBins = 1024;   // of a row's histogram
 constexpr int kList = 4096;   // tokens that are sorted; a row whose bins hold more is searched
                               // by its logits' bits instead (as where all logits are equal)
+constexpr int kListedK = kList / 2;
 constexpr int kThreads = 256; // of a workgroup that goes through a part of a row
 constexpr int kDraw = 512;    // of one that draws
 
@@ -45,83 +51,132 @@ __device__ __forceinline__ u64 entry_of(float z, uint32_t index) {
   return (u64)key_of(z) << 32 | (uint32_t)~index;
 }
 
-__device__ __forceinline__ u64 shuffle_xor(u64 v, int d) {
-  return (u64)__shfl_xor((long long)v, d, 64);
+// goes through logits [begin, end) of row m in 16-byte pieces, the loads of kAhead of them
+// under way at a time: piece(v, index of v[0], how many of v there are)
+constexpr int kAhead = 4;
+template <int TYPE, int T, class Piece>
+__device__ __forceinline__ void for_pieces(const SampleArgs& a, int64_t m, int begin, int end, int t,
+                                           Piece piece) {
+  constexpr int V = kValues<TYPE>, kSpan = V * T;
+  for (int n0 = begin; n0 < end; n0 += kSpan * kAhead) {
+    uint4 raw[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int n = n0 + kSpan * i + V * t;
+      raw[i] = load_raw<TYPE>(a.Z, m * a.ldz + n, end - n, a.wide);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int n = n0 + kSpan * i + V * t;
+      float v[V];
+      unpack<TYPE, V>(raw[i], v);
+      if (n < end) piece(v, n, min(V, end - n));
+    }
+  }
 }
-
-// goes through logits [begin, end) of row m in 16-byte pieces; each(z, index)
+// each(z, index)
 template <int TYPE, int T, class Each>
 __device__ __forceinline__ void for_logits(const SampleArgs& a, int64_t m, int begin, int end, int t,
                                            Each each) {
   constexpr int V = kValues<TYPE>;
-  for (int n = begin + V * t; n < end; n += V * T) {
-    float v[V];
-    load_values<TYPE, V>(a.Z, m * a.ldz + n, end - n, a.wide, v);
+  for_pieces<TYPE, T>(a, m, begin, end, t, [&](const float(&v)[V], int n, int count) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (n + e < end) each(v[e], n + e);
-  }
+      if (e < count) each(v[e], n + e);
+  });
 }
 
-// What a row's launches after the first know of it, from the parts' maxima and the row's
+struct Limits {
+  int k;      // 0: none
+  double p;   // 1: none
+  double y;   // log2 of min_p; below -100: none
+  double u;
+};
+
+__device__ __forceinline__ Limits limits_of(const SampleArgs& a, int64_t m) {
+  Limits l;
+  const int k = a.top_k ? a.top_k[m] : 0;
+  l.k = k > 0 && k < a.N ? k : 0;
+  const float p = a.top_p ? a.top_p[m] : 1.0f, q = a.min_p ? a.min_p[m] : 0.0f;
+  l.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
+  l.y = q > 0.0f ? log2((double)fminf(q, 1.0f)) : -1000.0;
+  const float u = a.u[m];
+  l.u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+  return l;
+}
+
+// What a row's launches after the first know of it, from the parts' results and the row's
 // settings (in every thread)
 struct Row {
-  double top;     // the largest logit
-  double rate;    // log2 e / temperature
-  double scale;   // bins per unit of distance
-  int64_t token;  // of the largest logit
+  Limits l;
+  double rate;  // log2 e / temperature
+  float top;    // the largest logit
+  float floor;  // tokens below it count nowhere: their weights are zero, or min_p is the only
+                // limit to a sum and takes them out
+  float least;  // min_p's limit: kept from here on
+  float scale;  // bins per unit of distance
   bool bad, greedy;
+  // the kinds of rows: down to the k-th token, or by sums
+  __device__ bool listed() const { return l.k > 0 && l.k <= kListedK; }
+  __device__ bool by_p() const { return l.p > 0.0 && l.p < 1.0; }
+  __device__ bool by_q() const { return least > floor; }
 };
+
+// log2 of a token's weight relative to the largest
+__device__ __forceinline__ double log2_weight(const Row& r, float z) {
+  return ((double)z - (double)r.top) * r.rate;
+}
+// for z >= r.floor; never rises with z
+__device__ __forceinline__ int bin_of(const Row& r, float z) {
+  return (int)fminf((r.top - z) * r.scale, (float)(kBins - 1));
+}
 
 template <int T>
 __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t m, int t) {
-  __shared__ u64 tops[T / 64];
-  __shared__ uint32_t lows[T / 64], bads[T / 64];
-  u64 top = 0;
-  uint32_t low = 0xffffffffu, bad = 0;
-  for (int c = t; c < a.chunks; c += T) {
-    const SamplePart p = a.part[m * a.chunks + c];
-    top = max(top, p.top);
-    low = min(low, p.low);
-    bad |= p.bad;
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    top = max(top, shuffle_xor(top, d));
-    low = min(low, (uint32_t)__shfl_xor((int)low, d, 64));
-    bad |= (uint32_t)__shfl_xor((int)bad, d, 64);
-  }
-  if ((t & 63) == 0) tops[t >> 6] = top, lows[t >> 6] = low, bads[t >> 6] = bad;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < T / 64; ++w) {
-    top = max(top, tops[w]);
-    low = min(low, lows[w]);
-    bad |= bads[w];
-  }
+  __shared__ SamplePart parts[T / 64];
+  SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
+  auto join = [&](const SamplePart& o) {
+    s.top = fmaxf(s.top, o.top);
+    s.low = fminf(s.low, o.low);
+    s.bad |= o.bad;
+  };
   const float temperature = a.temperature ? a.temperature[m] : 1.0f;
   Row r;
-  const float z = value_of((uint32_t)(top >> 32));
-  r.token = (uint32_t)~(uint32_t)top;
-  r.top = z;
+  r.l = limits_of(a, m);
+  for (int c = t; c < a.chunks; c += T) join(a.part[m * a.chunks + c]);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2)
+    join(SamplePart{__shfl_xor(s.top, d, 64), __shfl_xor(s.low, d, 64),
+                    (uint32_t)__shfl_xor((int)s.bad, d, 64)});
+  if ((t & 63) == 0) parts[t >> 6] = s;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) join(parts[w]);
+  r.top = s.top;
   // (a row without a finite logit has no lowest one)
-  r.bad = bad || low == 0xffffffffu || !(temperature < __builtin_inff());
+  r.bad = s.bad || s.low > FLT_MAX || !(temperature < __builtin_inff());
   r.greedy = temperature <= 0.0f;
   r.rate = 1.4426950408889634 / (double)temperature;
-  // from the largest logit to the lowest, or to where the weights are zero
-  const double range =
-      fmin(r.top - (double)value_of(low), (double)(a.bits + 1) / r.rate);
-  r.scale = range > 0.0 ? kBins / range : 0.0;
+  r.floor = fmaxf((float)((double)s.top - (double)(a.bits + 1) / r.rate), -FLT_MAX);
+  r.least = -FLT_MAX;
+  if (r.l.y > -(double)(a.bits + 1)) {
+    // the lowest f32 whose weight is min_p or more: a step or two from the rounded one
+    float z = fmaxf((float)((double)s.top + r.l.y / r.rate), -FLT_MAX);
+    for (int i = 0; i < 4 && log2_weight(r, z) < r.l.y; ++i) z = nextafterf(z, FLT_MAX);
+    for (int i = 0; i < 4 && z > -FLT_MAX; ++i) {
+      const float below = nextafterf(z, -FLT_MAX);
+      if (log2_weight(r, below) < r.l.y) break;
+      z = below;
+    }
+    r.least = z;
+  }
+  // without a top-p nothing below min_p's limit enters a sum that decides
+  if (r.l.p >= 1.0) r.floor = fmaxf(r.floor, r.least);
+  const float range = fminf(r.top - fmaxf(s.low, r.floor), FLT_MAX);
+  r.scale = range > 0.0f ? kBins / range : 0.0f;
+  // a range so small that the quotient is infinite: one bin
+  if (r.scale > FLT_MAX) r.scale = 0.0f;
   return r;
-}
-
-// log2 of a token's weight relative to the largest, <= 0; below -(bits + 1) the weight is
-// zero and the token counts nowhere
-__device__ __forceinline__ double log2_weight(const Row& r, double distance) {
-  return -distance * r.rate;
-}
-__device__ __forceinline__ int bin_of(const Row& r, double distance) {
-  return (int)fmin(distance * r.scale, (double)(kBins - 1));
 }
 
 // 2^y for y in [-(bits + 1), 0] in units of 2^-bits, rounded; 2^r by its series, r in
@@ -145,12 +200,11 @@ __device__ __forceinline__ u64 weight_of(double y, int bits) {
   return __builtin_bit_cast(u64, s) & 0xfffffffffffffull;
 }
 
-// ---- launch 1: the largest logit and its place, the lowest finite one, and whether the
-// row cannot be drawn from, of a part of a row; and its share of what the next launches add to
+// ---- launch 1: the largest logit of a part of a row, the lowest finite one, and whether
+// the row cannot be drawn from; and its share of what the next launches add to
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
-  __shared__ u64 tops[kThreads / 64];
-  __shared__ uint32_t lows[kThreads / 64], bads[kThreads / 64];
+  __shared__ SamplePart parts[kThreads / 64];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
@@ -158,33 +212,32 @@ __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
     a.count[m * kBins + b] = 0;
     a.weight[m * kBins + b] = 0;
   }
-  if (blockIdx.x == 0 && t == 0) a.listed[m] = 0;
-  u64 top = 0;
-  uint32_t low = 0xffffffffu, bad = 0;
-  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int n) {
-    top = max(top, entry_of(z, n));
-    if (z > -__builtin_inff()) low = min(low, key_of(z));
-    bad |= !(z < __builtin_inff());
+  if (blockIdx.x == 0 && t == 0) a.listed[m] = 0, a.first[m] = 0xffffffffu;
+  SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
+  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+    s.top = fmaxf(s.top, z);
+    s.low = fminf(s.low, z > -__builtin_inff() ? z : __builtin_inff());
+    s.bad |= !(z < __builtin_inff());
   });
+  auto join = [&](const SamplePart& o) {
+    s.top = fmaxf(s.top, o.top);
+    s.low = fminf(s.low, o.low);
+    s.bad |= o.bad;
+  };
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    top = max(top, shuffle_xor(top, d));
-    low = min(low, (uint32_t)__shfl_xor((int)low, d, 64));
-    bad |= (uint32_t)__shfl_xor((int)bad, d, 64);
-  }
-  if ((t & 63) == 0) tops[t >> 6] = top, lows[t >> 6] = low, bads[t >> 6] = bad;
+  for (int d = 1; d < 64; d *= 2)
+    join(SamplePart{__shfl_xor(s.top, d, 64), __shfl_xor(s.low, d, 64),
+                    (uint32_t)__shfl_xor((int)s.bad, d, 64)});
+  if ((t & 63) == 0) parts[t >> 6] = s;
   __syncthreads();
   if (t != 0) return;
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) {
-    top = max(top, tops[w]);
-    low = min(low, lows[w]);
-    bad |= bads[w];
-  }
-  a.part[m * a.chunks + blockIdx.x] = SamplePart{top, low, bad};
+  for (int w = 1; w < kThreads / 64; ++w) join(parts[w]);
+  a.part[m * a.chunks + blockIdx.x] = s;
 }
 
-// ---- launch 2: the histograms of tokens and of weights
+// ---- launch 2: the histograms: of tokens where a k decides, of weights where it is not
+// small; one atomic a token for nearly all rows
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   __shared__ uint32_t count[kBins];
@@ -195,23 +248,44 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   for (int b = t; b < kBins; b += kThreads) count[b] = 0, weight[b] = 0;
   const Row r = row_of<kThreads>(a, m, t);  // synchronizes
   if (r.bad || r.greedy) return;            // all of the row's workgroups
-  const double least = -(double)(a.bits + 1);
-  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
-    const double d = r.top - (double)z, y = log2_weight(r, d);
-    if (!(y >= least)) return;
-    const int b = bin_of(r, d);
-    atomicAdd(&count[b], 1u);
-    atomicAdd(&weight[b], weight_of(y, a.bits));
-  });
+  const bool counts = r.l.k > 0, weights = !r.listed();
+  // bins and weights of a piece side by side, the atomics behind them
+  constexpr int V = kValues<TYPE>;
+  if (!weights) {
+    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int, int n) {
+      int b[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) b[e] = bin_of(r, v[e]);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < n && v[e] >= r.floor) atomicAdd(&count[b[e]], 1u);
+    });
+  } else {
+    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int, int n) {
+      int b[V];
+      u64 w[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        b[e] = bin_of(r, v[e]);
+        w[e] = weight_of(log2_weight(r, v[e]), a.bits);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (e < n && v[e] >= r.floor) {
+          if (counts) atomicAdd(&count[b[e]], 1u);
+          atomicAdd(&weight[b[e]], w[e]);
+        }
+      }
+    });
+  }
   __syncthreads();
   for (int b = t; b < kBins; b += kThreads) {
-    if (count[b] == 0) continue;
-    atomicAdd(a.count + m * kBins + b, count[b]);
-    atomicAdd(a.weight + m * kBins + b, weight[b]);
+    if (counts && count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
+    if (weights && weight[b]) atomicAdd(a.weight + m * kBins + b, weight[b]);
   }
 }
 
-// ---- what the histogram says, in launches 3 and 4
+// ---- what the histograms say
 
 // inclusive sums over the workgroup's threads, in their order
 template <int T>
@@ -231,143 +305,170 @@ __device__ __forceinline__ void scan(uint32_t& c, u64& w, int t) {
   for (int i = 0; i < t >> 6; ++i) c += cs[i], w += ws[i];
 }
 
-// Tokens and weights of a row before each bin, with the whole row's behind the last
+// Weights of a row before each bin, with the whole row's behind the last
 struct Sums {
-  uint32_t count[kBins + 1];
   u64 weight[kBins + 1];
 };
-// the bins whose tokens are gathered, by bits, and how many tokens they hold
-struct Needed {
-  uint32_t mask[kBins / 32];
-  uint32_t total;
-  __device__ bool has(int b) const { return mask[b >> 5] >> (b & 31) & 1; }
-};
-
-struct Limits {
-  int k;          // 0: none
-  double p;       // 1: none
-  double y;       // log2 of min_p; below -(bits + 1): none
-  double u;
-};
-
-__device__ __forceinline__ Limits limits_of(const SampleArgs& a, int64_t m) {
-  Limits l;
-  const int k = a.top_k ? a.top_k[m] : 0;
-  l.k = k > 0 && k < a.N ? k : 0;
-  const float p = a.top_p ? a.top_p[m] : 1.0f, q = a.min_p ? a.min_p[m] : 0.0f;
-  l.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;
-  l.y = q > 0.0f ? log2((double)fminf(q, 1.0f)) : -1e30;
-  const float u = a.u[m];
-  l.u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
-  return l;
-}
 
 // where a sum's bounds [lo, hi] put the place that it decides
 struct Bounds {
   u64 lo, hi;
 };
 
-// Reads the row's histogram into s and marks the bins that decide its token.
+// The bin that holds the k-th token, and the tokens ahead of the bin; where there are fewer
+// than k the last bin, and kFewer.
+constexpr uint32_t kFewer = 0xffffffffu;
 template <int T>
-__device__ __forceinline__ void plan(const SampleArgs& a, const Row& r, const Limits& l, int64_t m,
-                                     int t, Sums& s, Needed& n) {
+__device__ __forceinline__ int kth_bin(const SampleArgs& a, int64_t m, int t, uint32_t k,
+                                       uint32_t& ahead) {
   constexpr int B = kBins / T;
-  __shared__ int at[8];
-  uint32_t c[B], cs = 0;
+  __shared__ int at;
+  __shared__ uint32_t before;
+  uint32_t c[B], sum = 0;
+  u64 none = 0;
+#pragma unroll
+  for (int i = 0; i < B; ++i) sum += c[i] = a.count[m * kBins + B * t + i];
+  uint32_t past = sum;
+  if (t == 0) at = kBins - 1, before = kFewer;
+  scan<T>(past, none, t);  // synchronizes
+  past -= sum;
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    if (past < k && past + c[i] >= k) at = B * t + i, before = past;
+    past += c[i];
+  }
+  __syncthreads();
+  ahead = before;
+  return at;
+}
+
+// The bins whose tokens decide a row by sums: a range for each place.
+struct Needed {
+  int lo[4], hi[4];
+  int kth;         // with a k: its bin
+  uint32_t ahead;  // and the tokens ahead of that bin
+  __device__ bool has(int b) const {
+    return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]) ||
+           (b >= lo[3] && b <= hi[3]);
+  }
+};
+
+// Reads the row's histogram into s and says which bins decide its token.
+template <int T>
+__device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_t m, int t, Sums& s) {
+  constexpr int B = kBins / T;
+  __shared__ int at[4];
+  const Limits& l = r.l;
   u64 w[B], ws = 0;
+  uint32_t none = 0;
 #pragma unroll
-  for (int i = 0; i < B; ++i) {
-    cs += c[i] = a.count[m * kBins + B * t + i];
-    ws += w[i] = a.weight[m * kBins + B * t + i];
-  }
-  uint32_t ci = cs;
+  for (int i = 0; i < B; ++i) ws += w[i] = a.weight[m * kBins + B * t + i];
   u64 wi = ws;
-  scan<T>(ci, wi, t);
-  ci -= cs, wi -= ws;
+  scan<T>(none, wi, t);
+  wi -= ws;
 #pragma unroll
   for (int i = 0; i < B; ++i) {
-    s.count[B * t + i] = ci, s.weight[B * t + i] = wi;
-    ci += c[i], wi += w[i];
+    s.weight[B * t + i] = wi;
+    wi += w[i];
   }
-  if (t == T - 1) s.count[kBins] = ci, s.weight[kBins] = wi;
-  if (t < kBins / 32) n.mask[t] = 0;
-  if (t == 0) n.total = 0;
-  if (t < 8) at[t] = 0;
+  if (t == T - 1) s.weight[kBins] = wi;
+  if (t < 4) at[t] = 0;
+  Needed n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n.lo[i] = 1, n.hi[i] = 0;  // none
+  n.kth = 0;
+  if (l.k > 0) n.kth = kth_bin<T>(a, m, t, (uint32_t)l.k, n.ahead);
   __syncthreads();
 
-  // at[2 i], at[2 i + 1]: the bins of step i's bounds
   const u64 all = s.weight[kBins];
   Bounds k{all, all};
-  const bool by_k = l.k > 0 && (uint32_t)l.k < s.count[kBins];
-  if (by_k) {
-    for (int b = B * t; b < B * t + B; ++b)
-      if (s.count[b] < (uint32_t)l.k && s.count[b + 1] >= (uint32_t)l.k) at[0] = b;
-    __syncthreads();
-    k = Bounds{s.weight[at[0]], s.weight[at[0] + 1]};
+  if (l.k > 0) {
+    n.lo[0] = n.hi[0] = n.kth;
+    k = Bounds{s.weight[n.kth], s.weight[n.kth + 1]};
   }
   Bounds p = k;
-  const bool by_p = l.p > 0.0 && l.p < 1.0;
-  if (by_p) {
+  if (r.by_p()) {
     const double lo = l.p * (double)k.lo, hi = l.p * (double)k.hi;
     for (int b = B * t; b < B * t + B; ++b) {
       const double before = (double)s.weight[b], past = (double)s.weight[b + 1];
-      if (before < lo && past >= lo) at[2] = b;  // (none where lo is 0: bin 0)
-      if (before < hi && past >= hi) at[3] = b;
+      if (before < lo && past >= lo) at[0] = b;  // (none where lo is 0: bin 0)
+      if (before < hi && past >= hi) at[1] = b;
     }
     __syncthreads();
-    p = Bounds{s.weight[at[2]], min(s.weight[at[3] + 1], k.hi)};
+    n.lo[1] = at[0], n.hi[1] = at[1];
+    p = Bounds{s.weight[n.lo[1]], min(s.weight[n.hi[1] + 1], k.hi)};
   } else if (l.p <= 0.0) {
     p.lo = p.hi = 1ull << a.bits;  // the first token alone
   }
   Bounds q = p;
-  const bool by_q = l.y >= -(double)(a.bits + 1);
-  int q0 = 0, q1 = 0;
-  if (by_q) {
-    // the bin of that distance; one to either side for the roundings on the way
-    const int b = bin_of(r, -l.y / r.rate);
-    q0 = max(b - 1, 0), q1 = min(b + 1, kBins - 1);
-    q = Bounds{min(p.lo, s.weight[q0]), min(p.hi, s.weight[q1 + 1])};
+  if (r.by_q()) {
+    n.lo[2] = n.hi[2] = bin_of(r, r.least);
+    q = Bounds{min(p.lo, s.weight[n.lo[2]]), min(p.hi, s.weight[n.lo[2] + 1])};
   }
-  {
-    const double lo = l.u * (double)q.lo, hi = l.u * (double)q.hi;
-    for (int b = B * t; b < B * t + B; ++b) {
-      const double before = (double)s.weight[b], past = (double)s.weight[b + 1];
-      if (before <= lo && past > lo) at[4] = b;
-      if (before <= hi && past > hi) at[5] = b;
-    }
-    __syncthreads();
-  }
-  uint32_t mine = 0;
+  const double lo = l.u * (double)q.lo, hi = l.u * (double)q.hi;
   for (int b = B * t; b < B * t + B; ++b) {
-    const bool need = (by_k && b == at[0]) || (by_p && b >= at[2] && b <= at[3]) ||
-                      (by_q && b >= q0 && b <= q1) || (b >= at[4] && b <= at[5]);
-    if (!need) continue;
-    atomicOr(&n.mask[b >> 5], 1u << (b & 31));
-    mine += s.count[b + 1] - s.count[b];
+    const double before = (double)s.weight[b], past = (double)s.weight[b + 1];
+    if (before <= lo && past > lo) at[2] = b;
+    if (before <= hi && past > hi) at[3] = b;
   }
-  if (mine) atomicAdd(&n.total, mine);
   __syncthreads();
+  n.lo[3] = at[2], n.hi[3] = at[3];
+  return n;
 }
 
 // ---- launch 3: the tokens of those bins
+// The workgroup's are listed in LDS first, a place there for all of a thread's piece at a
+// time, and then behind the row's others: one atomic in memory for all of them (with one for
+// each token 128 rows took 38 us).
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
+  constexpr int V = kValues<TYPE>;
   __shared__ Sums s;
-  __shared__ Needed need;
+  __shared__ u64 mine[kList];
+  __shared__ uint32_t taken, base;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
-  const Row r = row_of<kThreads>(a, m, t);
-  if (r.bad || r.greedy) return;
-  plan<kThreads>(a, r, limits_of(a, m), m, t, s, need);
-  if (need.total > kList) return;
-  const double least = -(double)(a.bits + 1);
-  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int n) {
-    const double d = r.top - (double)z;
-    if (!(log2_weight(r, d) >= least) || !need.has(bin_of(r, d))) return;
-    // all of them are need.total <= kList
-    a.list[m * kList + atomicAdd(a.listed + m, 1u)] = entry_of(z, n);
-  });
+  if (t == 0) taken = 0;
+  const Row r = row_of<kThreads>(a, m, t);  // synchronizes
+  if (r.bad) return;
+  // those of a piece that `is` says
+  auto take = [&](auto is) {
+    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n, int count) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) mask |= (uint32_t)(e < count && v[e] >= r.floor && is(v[e])) << e;
+      if (!mask) return;
+      uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (mask >> e & 1) {
+          if (at < kList) mine[at] = entry_of(v[e], n + e);
+          ++at;
+        }
+    });
+  };
+  if (r.greedy) {
+    uint32_t first = 0xffffffffu;
+    for_logits<TYPE, kThreads>(a, m, begin, end, t,
+                               [&](float z, int n) { if (z == r.top) first = min(first, (uint32_t)n); });
+    if (first != 0xffffffffu) atomicMin(a.first + m, first);
+    return;
+  }
+  if (r.listed()) {
+    uint32_t ahead;
+    const int last = kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead);
+    take([&](float z) { return bin_of(r, z) <= last; });
+  } else {
+    const Needed need = plan<kThreads>(a, r, m, t, s);
+    take([&](float z) { return need.has(bin_of(r, z)); });
+  }
+  __syncthreads();
+  if (t == 0) base = taken ? atomicAdd(a.listed + m, taken) : 0;
+  __syncthreads();
+  const uint32_t count = min(taken, (uint32_t)kList);
+  for (uint32_t i = t; i < count; i += kThreads)
+    if (base + i < kList) a.list[m * kList + base + i] = mine[i];
 }
 
 // ---- launch 4: the draw
@@ -400,19 +501,17 @@ __device__ __forceinline__ Found search(const SampleArgs& a, const Row& r, int64
                                         Search how, uint32_t k, double to) {
   __shared__ uint32_t count[256], digit, found_before, found_ties;
   __shared__ u64 weight[256], found_sum, found_weight;
-  const double least = -(double)(a.bits + 1);
   uint32_t prefix = 0, before = 0;
   u64 sum = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (t < 256) count[t] = 0, weight[t] = 0;
     __syncthreads();
     for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
-      const double y = log2_weight(r, r.top - (double)z);
       const uint32_t key = key_of(z);
-      if (!(y >= least) || (shift < 24 && key >> (shift + 8) != prefix)) return;
+      if (!(z >= r.floor) || (shift < 24 && key >> (shift + 8) != prefix)) return;
       const int b = 255 - (key >> shift & 255);  // the largest first
       atomicAdd(&count[b], 1u);
-      atomicAdd(&weight[b], weight_of(y, a.bits));
+      atomicAdd(&weight[b], weight_of(log2_weight(r, z), a.bits));
     });
     __syncthreads();
     const uint32_t mine = t < 256 ? count[t] : 0;
@@ -459,93 +558,37 @@ __device__ __forceinline__ int64_t index_of(const SampleArgs& a, int64_t m, int 
   return result;
 }
 
-template <int TYPE>
-__global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
-  constexpr int E = kList / kDraw;
-  __shared__ Sums s;
-  __shared__ Needed need;
-  __shared__ uint32_t start[kBins];  // a needed bin's first place in the list
-  __shared__ u64 list[kList], ahead[kList + 1];
-  __shared__ u64 found, below;
-  __shared__ int which;
-  const int t = threadIdx.x;
-  const int64_t m = blockIdx.y;
-  const Row r = row_of<kDraw>(a, m, t);
-  if (r.bad || r.greedy) {
-    if (t == 0) {
-      a.token[m] = r.bad ? -1 : r.token;
-      if (a.logprob) a.logprob[m] = r.bad ? __builtin_nanf("") : 0.0f;
+// the draw's LDS
+struct Draw {
+  Sums s;
+  uint32_t start[kBins];  // a needed bin's first place in the list
+  u64 list[kList], ahead[kList + 1];
+  u64 found, below;
+  uint32_t tokens;
+  int which;
+};
+
+// list[0 .. size) in descending order, size a power of two from 64 on: a bitonic sort, its
+// steps across less than 64 places in the lanes of a wave
+__device__ __forceinline__ void sort(u64* list, int size, int t) {
+  const int lane = t & 63, wave = t >> 6;
+  // the steps j = from, from / 2 .. 1 of level k on the wave's 64 places from `at` on
+  auto within = [&](u64 v, int at, int k, int from) {
+    const bool down = ((at + lane) & k) == 0;
+    for (int j = from; j > 0; j /= 2) {
+      const u64 o = (u64)__shfl_xor((long long)v, j, 64);
+      const bool first = (lane & j) == 0;
+      v = (first == down) == (v > o) ? v : o;  // (equal entries are zeros)
     }
-    return;
-  }
-  const Limits l = limits_of(a, m);
-  plan<kDraw>(a, r, l, m, t, s, need);
-  const u64 all = s.weight[kBins];
-  const bool by_k = l.k > 0 && (uint32_t)l.k < s.count[kBins];
-  const bool by_p = l.p > 0.0 && l.p < 1.0, by_q = l.y >= -(double)(a.bits + 1);
-  auto finish = [&](int64_t token, float z, u64 whole) {
-    a.token[m] = token;
-    if (a.logprob)
-      a.logprob[m] = (float)(0.6931471805599453 *
-                             (log2_weight(r, r.top - (double)z) -
-                              (log2((double)whole) - (double)a.bits)));
+    return v;
   };
-
-  if (need.total > kList) {  // all of the workgroup
-    u64 whole = all;
-    if (by_k) {
-      const Found f = search<TYPE>(a, r, m, t, kByCount, (uint32_t)l.k, 0.0);
-      whole = f.sum + (l.k - f.before) * f.weight;
-    }
-    if (by_p) {
-      const double to = l.p * (double)whole;
-      const Found f = search<TYPE>(a, r, m, t, kBySum, 0, to);
-      whole = min(whole, f.sum + place_among(f.sum, f.weight, f.ties, to, false) * f.weight);
-    } else if (l.p <= 0.0) {
-      whole = 1ull << a.bits;
-    }
-    if (by_q) {
-      if (t == 0) below = 0;
-      __syncthreads();
-      u64 mine = 0;
-      for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
-        const double y = log2_weight(r, r.top - (double)z);
-        if (y >= l.y) mine += weight_of(y, a.bits);
-      });
-      atomicAdd(&below, mine);
-      __syncthreads();
-      whole = min(whole, below);
-    }
-    const double to = l.u * (double)whole;
-    const Found f = search<TYPE>(a, r, m, t, kPastSum, 0, to);
-    const uint32_t place = place_among(f.sum, f.weight, f.ties, to, true);
-    const int64_t token = index_of<TYPE>(a, m, t, f.key, place);
-    if (t == 0) finish(token, value_of(f.key), whole);
-    return;
+  for (int at = 64 * wave; at < size; at += kDraw) {
+    u64 v = list[at + lane];
+    for (int k = 2; k <= 64; k *= 2) v = within(v, at, k, k / 2);
+    list[at + lane] = v;
   }
-
-  // the list sorted, in descending order, zeros (no token's entry) behind it
-  const int count = (int)need.total;
-  int size = 2;
-  while (size < count) size *= 2;
-  for (int i = t; i < size; i += kDraw) list[i] = i < count ? a.list[m * kList + i] : 0;
-  {
-    constexpr int B = kBins / kDraw;
-    uint32_t c[B], at = 0;
-    u64 none = 0;
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int b = B * t + i;
-      at += c[i] = need.has(b) ? s.count[b + 1] - s.count[b] : 0;
-    }
-    const uint32_t mine = at;
-    scan<kDraw>(at, none, t);
-    at -= mine;
-#pragma unroll
-    for (int i = 0; i < B; ++i) start[B * t + i] = at, at += c[i];
-  }
-  for (int k = 2; k <= size; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
+  for (int k = 128; k <= size; k *= 2) {
+    for (int j = k / 2; j >= 64; j /= 2) {
       __syncthreads();
       for (int i = t; i < size / 2; i += kDraw) {
         const int lo = 2 * (i - (i & (j - 1))) + (i & (j - 1)), hi = lo + j;
@@ -553,22 +596,41 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
         if ((x < y) == ((lo & k) == 0)) list[lo] = y, list[hi] = x;
       }
     }
-  if (t == 0) found = all, below = 0, which = 0;
+    __syncthreads();
+    for (int at = 64 * wave; at < size; at += kDraw)
+      list[at + lane] = within(list[at + lane], at, k, 32);
+  }
   __syncthreads();
+}
 
+struct Drawn {
+  u64 entry, whole;  // the token's, and the sum of the weights it was drawn from
+};
+
+// The token from the sorted list of `count` tokens, at most E of each thread.
+template <int E>
+__device__ __forceinline__ Drawn resolve(const SampleArgs& a, const Row& r, const Needed& need,
+                                         Draw& d, int count, int t) {
+  const Limits& l = r.l;
+  const bool listed = r.listed();
+  if (t == 0) d.below = 0, d.which = 0;
   // weights of places E t .. E t + E - 1 of the list, and the sums ahead of them
   u64 w[E], sum = 0;
   int bin[E];
-  double y[E];
+  float z[E];
+  int previous = -1;
+  if (!listed && t > 0 && E * t < count)
+    previous = bin_of(r, value_of((uint32_t)(d.list[E * t - 1] >> 32)));
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = E * t + e;
-    w[e] = 0, bin[e] = 0, y[e] = 0.0;
+    w[e] = 0, bin[e] = 0, z[e] = 0.0f;
     if (i < count) {
-      const double d = r.top - (double)value_of((uint32_t)(list[i] >> 32));
-      y[e] = log2_weight(r, d);
-      bin[e] = bin_of(r, d);
-      w[e] = weight_of(y[e], a.bits);
+      z[e] = value_of((uint32_t)(d.list[i] >> 32));
+      w[e] = weight_of(log2_weight(r, z[e]), a.bits);
+      bin[e] = bin_of(r, z[e]);
+      if (!listed && bin[e] != previous) d.start[bin[e]] = i;
+      previous = bin[e];
     }
     sum += w[e];
   }
@@ -578,70 +640,138 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   u64 before = total - sum;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    ahead[E * t + e] = before;
+    d.ahead[E * t + e] = before;
     before += w[e];
   }
-  if (t == kDraw - 1) ahead[kList] = before;
+  if (t == kDraw - 1) d.ahead[E * kDraw] = before;
   __syncthreads();
-  // the sum of all weights of the row ahead of place i
-  auto before_place = [&](int e) {
+  // the sum of all weights of the row ahead of the thread's places (by sums: its bin's, and the
+  // list's ahead of it in the bin)
+  u64 from[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
     const int i = E * t + e;
-    return s.weight[bin[e]] + (ahead[i] - ahead[start[bin[e]]]);
-  };
-
-  u64 whole = all;
-  if (by_k) {
-    // the k-th token's bin: every thread finds it
-    int b = 0;
-    for (int step = kBins / 2; step > 0; step /= 2)
-      if (s.count[b + step] < (uint32_t)l.k) b += step;
-    const uint32_t first = start[b];
-    whole = s.weight[b] + ahead[first + (l.k - s.count[b])] - ahead[first];
+    from[e] = 0;
+    if (i < count)
+      from[e] = listed ? d.ahead[i]
+                       : d.s.weight[bin[e]] + (d.ahead[i] - d.ahead[d.start[bin[e]]]);
   }
-  if (by_p) {
+
+  u64 whole = listed ? d.ahead[min(l.k, count)] : d.s.weight[kBins];
+  if (!listed && l.k > 0 && need.ahead != kFewer) {
+    const uint32_t first = d.start[need.kth];
+    whole = d.s.weight[need.kth] + (d.ahead[first + (l.k - need.ahead)] - d.ahead[first]);
+  }
+  if (r.by_p()) {
     const double to = l.p * (double)whole;
-    if (t == 0) found = whole;
+    if (t == 0) d.found = whole;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (E * t + e >= count) break;
-      const u64 b = before_place(e);
-      if ((double)b < to && (double)(b + w[e]) >= to) found = min(whole, b + w[e]);
-    }
+    for (int e = 0; e < E; ++e)
+      if (E * t + e < count && (double)from[e] < to && (double)(from[e] + w[e]) >= to)
+        d.found = min(whole, from[e] + w[e]);
     __syncthreads();
-    whole = found;
+    whole = d.found;
   } else if (l.p <= 0.0) {
     whole = 1ull << a.bits;
   }
-  if (by_q) {
-    const int q = bin_of(r, -l.y / r.rate), q0 = max(q - 1, 0), q1 = min(q + 1, kBins - 1);
+  if (r.by_q()) {
+    // (all of a list down to the k-th; else those of the limit's bin and all ahead of it)
     u64 mine = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (E * t + e < count && bin[e] >= q0 && bin[e] <= q1 && y[e] >= l.y) mine += w[e];
-    if (mine) atomicAdd(&below, mine);
+      if (E * t + e < count && z[e] >= r.least && (listed || bin[e] == need.lo[2])) mine += w[e];
+    if (mine) atomicAdd(&d.below, mine);
     __syncthreads();
-    whole = min(whole, s.weight[q0] + below);
+    whole = min(whole, listed ? d.below : d.s.weight[need.lo[2]] + d.below);
   }
   const double to = l.u * (double)whole;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (E * t + e >= count) break;
-    const u64 b = before_place(e);
-    if ((double)b <= to && (double)(b + w[e]) > to) which = E * t + e;
-  }
+  for (int e = 0; e < E; ++e)
+    if (E * t + e < count && (double)from[e] <= to && (double)(from[e] + w[e]) > to)
+      d.which = E * t + e;
   __syncthreads();
-  if (t == 0) {
-    const u64 it = list[which];
-    finish((uint32_t)~(uint32_t)it, value_of((uint32_t)(it >> 32)), whole);
+  return Drawn{d.list[d.which], whole};
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
+  __shared__ Draw d;
+  const int t = threadIdx.x;
+  const int64_t m = blockIdx.y;
+  const Row r = row_of<kDraw>(a, m, t);
+  const Limits& l = r.l;
+  if (r.bad || r.greedy) {
+    if (t == 0) {
+      a.token[m] = r.bad ? -1 : (int64_t)a.first[m];
+      if (a.logprob) a.logprob[m] = r.bad ? __builtin_nanf("") : 0.0f;
+    }
+    return;
   }
+  auto finish = [&](int64_t token, float z, u64 whole) {
+    a.token[m] = token;
+    if (a.logprob)
+      a.logprob[m] = (float)(0.6931471805599453 *
+                             (log2_weight(r, z) - (log2((double)whole) - (double)a.bits)));
+  };
+  const int count = (int)min(a.listed[m], (uint32_t)kList + 1);
+
+  if (count > kList) {  // all of the workgroup
+    // how many tokens there are, and the sums of all and of those from min_p on
+    if (t == 0) d.found = 0, d.below = 0, d.tokens = 0;
+    __syncthreads();
+    u64 mine = 0, kept = 0;
+    uint32_t some = 0;
+    for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
+      if (!(z >= r.floor)) return;
+      const u64 w = weight_of(log2_weight(r, z), a.bits);
+      some += 1;
+      mine += w;
+      kept += z >= r.least ? w : 0;
+    });
+    atomicAdd(&d.tokens, some);
+    atomicAdd(&d.found, mine);
+    atomicAdd(&d.below, kept);
+    __syncthreads();
+    u64 whole = d.found;
+    if (l.k > 0 && (uint32_t)l.k < d.tokens) {
+      const Found f = search<TYPE>(a, r, m, t, kByCount, (uint32_t)l.k, 0.0);
+      whole = f.sum + (l.k - f.before) * f.weight;
+    }
+    if (r.by_p()) {
+      const double to = l.p * (double)whole;
+      const Found f = search<TYPE>(a, r, m, t, kBySum, 0, to);
+      whole = min(whole, f.sum + place_among(f.sum, f.weight, f.ties, to, false) * f.weight);
+    } else if (l.p <= 0.0) {
+      whole = 1ull << a.bits;
+    }
+    if (r.by_q()) whole = min(whole, d.below);
+    const double to = l.u * (double)whole;
+    const Found f = search<TYPE>(a, r, m, t, kPastSum, 0, to);
+    const uint32_t place = place_among(f.sum, f.weight, f.ties, to, true);
+    const int64_t token = index_of<TYPE>(a, m, t, f.key, place);
+    if (t == 0) finish(token, value_of(f.key), whole);
+    return;
+  }
+
+  // the list sorted, in descending order, zeros (no token's entry) behind it
+  int size = 64;
+  while (size < count) size *= 2;
+  for (int i = t; i < size; i += kDraw) d.list[i] = i < count ? a.list[m * kList + i] : 0;
+  Needed need;
+  if (!r.listed()) need = plan<kDraw>(a, r, m, t, d.s);
+  __syncthreads();
+  sort(d.list, size, t);
+  const Drawn it = count <= kDraw ? resolve<1>(a, r, need, d, count, t)
+                                  : resolve<kList / kDraw>(a, r, need, d, count, t);
+  if (t == 0) finish((uint32_t)~(uint32_t)it.entry, value_of((uint32_t)(it.entry >> 32)), it.whole);
 }
 
 constexpr int64_t kRows = 1024;  // of a set of launches: bounds the workspace
 
 struct Layout {
   int64_t rows, chunks, chunk;
-  size_t weight, list, part, count, listed, bytes;
+  size_t weight, list, part, count, listed, first, bytes;
 };
 
 // A row is split until the launch has 1024 workgroups, into parts of 4096 logits at least
@@ -663,6 +793,7 @@ Layout layout(int64_t M, int64_t N) {
   l.part = take((int64_t)sizeof(SamplePart) * l.rows * l.chunks);
   l.count = take(4 * l.rows * kBins);
   l.listed = take(4 * l.rows);
+  l.first = take(4 * l.rows);
   l.bytes = at;
   return l;
 }
@@ -688,6 +819,7 @@ int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st) {
   a.part = reinterpret_cast<SamplePart*>(p + l.part);
   a.count = reinterpret_cast<uint32_t*>(p + l.count);
   a.listed = reinterpret_cast<uint32_t*>(p + l.listed);
+  a.first = reinterpret_cast<uint32_t*>(p + l.first);
   a.chunk = (int)l.chunk;
   a.chunks = (int)l.chunks;
   int log = 0;

@@ -149,6 +149,30 @@ def test_many_ties_at_every_place(N, dtype):
     check(z, u, t=t, k=k, p=p, q=q)
 
 
+@pytest.mark.parametrize("N", [4500, 9000, 30000])
+def test_large_k(N):
+    # k beyond what is listed down to the k-th, around the number of tokens with a weight, and
+    # more of those than are sorted
+    g = gen(N + 1)
+    M = 40
+    k = torch.cat([torch.arange(2044, 2054), torch.arange(4090, 4100), N - torch.arange(1, 11),
+                   torch.randint(2049, N, (10,))]).int().cuda()
+    u = torch.rand(M, generator=g, device="cuda")
+    u[::4] = 0.99999
+    p = torch.where(torch.arange(M, device="cuda") % 3 == 0, 0.97, 1.0)
+    q = torch.where(torch.arange(M, device="cuda") % 5 == 0, 0.01, 0.0)
+    for kind in ("flat", "ties", "peaked", "far"):
+        z = logits(kind, M, N, g)
+        check(z, u, k=k)
+        check(z, u, k=k, p=p)
+        check(z, u, k=k, p=p, q=q, t=p + q)
+    # 4200 tokens with a weight and k above that
+    z = torch.full((M, N), -1e5, device="cuda")
+    z[:, :4200] = torch.randn((M, 4200), generator=g, device="cuda").mul(3).round() / 3
+    check(z, u, k=torch.full((M,), 4400, device="cuda").int(), p=p)
+    check(z, u, k=torch.full((M,), 4100, device="cuda").int(), p=p)
+
+
 def test_frequencies():
     # u on a grid: a token's count is its share of the grid, to one point at each end
     g = gen(1)
