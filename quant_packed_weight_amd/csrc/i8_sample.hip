@@ -52,7 +52,7 @@ __device__ __forceinline__ u64 entry_of(float z, uint32_t index) {
 }
 
 // goes through logits [begin, end) of row m in 16-byte pieces, the loads of kAhead of them
-// under way at a time: piece(v, index of v[0], how many of v there are)
+// under way at a time: piece(v, index of v[0]), with -inf, which counts nowhere, past the end
 constexpr int kAhead = 4;
 template <int TYPE, int T, class Piece>
 __device__ __forceinline__ void for_pieces(const SampleArgs& a, int64_t m, int begin, int end, int t,
@@ -68,9 +68,15 @@ __device__ __forceinline__ void for_pieces(const SampleArgs& a, int64_t m, int b
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int n = n0 + kSpan * i + V * t;
+      if (n >= end) break;
       float v[V];
       unpack<TYPE, V>(raw[i], v);
-      if (n < end) piece(v, n, min(V, end - n));
+      if (n + V > end) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (n + e >= end) v[e] = -__builtin_inff();
+      }
+      piece(v, n);
     }
   }
 }
@@ -79,10 +85,9 @@ template <int TYPE, int T, class Each>
 __device__ __forceinline__ void for_logits(const SampleArgs& a, int64_t m, int begin, int end, int t,
                                            Each each) {
   constexpr int V = kValues<TYPE>;
-  for_pieces<TYPE, T>(a, m, begin, end, t, [&](const float(&v)[V], int n, int count) {
+  for_pieces<TYPE, T>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < count) each(v[e], n + e);
+    for (int e = 0; e < V; ++e) each(v[e], n + e);
   });
 }
 
@@ -126,9 +131,15 @@ struct Row {
 __device__ __forceinline__ double log2_weight(const Row& r, float z) {
   return ((double)z - (double)r.top) * r.rate;
 }
-// for z >= r.floor; never rises with z
+// the distance from the largest logit in bins (0 <= , infinite where z is -inf), which never
+// rises with z, and for z >= r.floor the bin: the last one holds all that lies behind it too
+__device__ __forceinline__ float place_of(const Row& r, float z) { return (r.top - z) * r.scale; }
 __device__ __forceinline__ int bin_of(const Row& r, float z) {
-  return (int)fminf((r.top - z) * r.scale, (float)(kBins - 1));
+  return (int)fminf(place_of(r, z), (float)(kBins - 1));
+}
+// places of bins lo .. hi: from first(lo) to below past(hi)
+__device__ __forceinline__ float past(int hi) {
+  return hi == kBins - 1 ? __builtin_inff() : (float)(hi + 1);
 }
 
 template <int T>
@@ -179,25 +190,32 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t m, int t) {
   return r;
 }
 
-// 2^y for y in [-(bits + 1), 0] in units of 2^-bits, rounded; 2^r by its series, r in
-// [-1/2, 1/2], to r^12 (ln 2)^12 / 12! < 10^-14
-__device__ __forceinline__ u64 weight_of(double y, int bits) {
-  const double n = rint(y), r = (y - n) * 0.6931471805599453;
-  double p = 1.0 / 39916800.0;
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
+// 2^(j / 32), j < 32, in LDS: what weight_of multiplies by.  The caller synchronizes.
+constexpr int kRoots = 32;
+__device__ __forceinline__ void set_roots(double* roots, int t) {
+  if (t < kRoots) roots[t] = exp2((double)t / kRoots);
+}
+// 2^(x / 32) for x in [-32 (bits + 2), 0] in units of 2^-bits, rounded: x = n + f with f in
+// [-1/2, 1/2], 2^(n / 32) from the roots, and 2^(f / 32) by its series, with c = ln 2 / 32 to
+// (c / 2)^6 / 6! < 10^-14.  (The series of 2^f alone, to f^11, cost twice as much.)
+__device__ __forceinline__ u64 weight_of(double x, const double* roots, int bits) {
+  const double n = rint(x), f = x - n;
+  constexpr double c = 0.6931471805599453 / kRoots;
+  double p = c * c * c * c * c / 120.0;
+  p = fma(p, f, c * c * c * c / 24.0);
+  p = fma(p, f, c * c * c / 6.0);
+  p = fma(p, f, c * c / 2.0);
+  p = fma(p, f, c);
+  const int i = (int)n;
+  const double root = roots[i & (kRoots - 1)];
+  p = fma(p * f, root, root);
   // at most 2^50: the sum with 2^52 holds the integer in its low bits
-  const double s = __builtin_ldexp(p, (int)n + bits) + 4503599627370496.0;
+  const double s = __builtin_ldexp(p, (i >> 5) + bits) + 4503599627370496.0;
   return __builtin_bit_cast(u64, s) & 0xfffffffffffffull;
+}
+
+__device__ __forceinline__ u64 weight_of(const Row& r, float z, const double* roots, int bits) {
+  return weight_of(((double)z - (double)r.top) * (r.rate * kRoots), roots, bits);
 }
 
 // ---- launch 1: the largest logit of a part of a row, the lowest finite one, and whether
@@ -214,11 +232,14 @@ __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
   }
   if (blockIdx.x == 0 && t == 0) a.listed[m] = 0, a.first[m] = 0xffffffffu;
   SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
+  bool nan = false;
   for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+    nan |= z != z;
+    z = __builtin_canonicalizef(z);  // once, not for each of the two
     s.top = fmaxf(s.top, z);
-    s.low = fminf(s.low, z > -__builtin_inff() ? z : __builtin_inff());
-    s.bad |= !(z < __builtin_inff());
+    s.low = fminf(s.low, z == -__builtin_inff() ? __builtin_inff() : z);
   });
+  s.bad = nan || s.top == __builtin_inff();
   auto join = [&](const SamplePart& o) {
     s.top = fmaxf(s.top, o.top);
     s.low = fminf(s.low, o.low);
@@ -242,40 +263,25 @@ template <int TYPE>
 __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   __shared__ uint32_t count[kBins];
   __shared__ u64 weight[kBins];
+  __shared__ double roots[kRoots];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
   for (int b = t; b < kBins; b += kThreads) count[b] = 0, weight[b] = 0;
+  set_roots(roots, t);
   const Row r = row_of<kThreads>(a, m, t);  // synchronizes
   if (r.bad || r.greedy) return;            // all of the row's workgroups
   const bool counts = r.l.k > 0, weights = !r.listed();
-  // bins and weights of a piece side by side, the atomics behind them
-  constexpr int V = kValues<TYPE>;
   if (!weights) {
-    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int, int n) {
-      int b[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) b[e] = bin_of(r, v[e]);
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < n && v[e] >= r.floor) atomicAdd(&count[b[e]], 1u);
+    for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+      if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
     });
   } else {
-    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int, int n) {
-      int b[V];
-      u64 w[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        b[e] = bin_of(r, v[e]);
-        w[e] = weight_of(log2_weight(r, v[e]), a.bits);
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (e < n && v[e] >= r.floor) {
-          if (counts) atomicAdd(&count[b[e]], 1u);
-          atomicAdd(&weight[b[e]], w[e]);
-        }
-      }
+    for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+      if (!(z >= r.floor)) return;
+      const int b = bin_of(r, z);
+      if (counts) atomicAdd(&count[b], 1u);
+      atomicAdd(&weight[b], weight_of(r, z, roots, a.bits));
     });
   }
   __syncthreads();
@@ -347,10 +353,6 @@ struct Needed {
   int lo[4], hi[4];
   int kth;         // with a k: its bin
   uint32_t ahead;  // and the tokens ahead of that bin
-  __device__ bool has(int b) const {
-    return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]) ||
-           (b >= lo[3] && b <= hi[3]);
-  }
 };
 
 // Reads the row's histogram into s and says which bins decide its token.
@@ -419,12 +421,13 @@ __device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_
 // ---- launch 3: the tokens of those bins
 // The workgroup's are listed in LDS first, a place there for all of a thread's piece at a
 // time, and then behind the row's others: one atomic in memory for all of them (with one for
-// each token 128 rows took 38 us).
+// each token 128 rows took 38 us).  What does not fit there goes to the row's list at once.
+constexpr int kMine = kList / 2;
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   constexpr int V = kValues<TYPE>;
   __shared__ Sums s;
-  __shared__ u64 mine[kList];
+  __shared__ u64 mine[kMine];
   __shared__ uint32_t taken, base;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
@@ -432,22 +435,6 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   if (t == 0) taken = 0;
   const Row r = row_of<kThreads>(a, m, t);  // synchronizes
   if (r.bad) return;
-  // those of a piece that `is` says
-  auto take = [&](auto is) {
-    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n, int count) {
-      uint32_t mask = 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) mask |= (uint32_t)(e < count && v[e] >= r.floor && is(v[e])) << e;
-      if (!mask) return;
-      uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (mask >> e & 1) {
-          if (at < kList) mine[at] = entry_of(v[e], n + e);
-          ++at;
-        }
-    });
-  };
   if (r.greedy) {
     uint32_t first = 0xffffffffu;
     for_logits<TYPE, kThreads>(a, m, begin, end, t,
@@ -455,18 +442,46 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
     if (first != 0xffffffffu) atomicMin(a.first + m, first);
     return;
   }
+  // the places of what is taken: ranges [lo, hi), some empty
+  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (r.listed()) {
     uint32_t ahead;
-    const int last = kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead);
-    take([&](float z) { return bin_of(r, z) <= last; });
+    hi[0] = past(kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead));
   } else {
     const Needed need = plan<kThreads>(a, r, m, t, s);
-    take([&](float z) { return need.has(bin_of(r, z)); });
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (need.lo[i] <= need.hi[i]) lo[i] = (float)need.lo[i], hi[i] = past(need.hi[i]);
   }
+  for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+    float x[V];
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = v[e] >= r.floor ? place_of(r, v[e]) : -1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lo[i] < hi[i]) {  // the same in all lanes
+#pragma unroll
+        for (int e = 0; e < V; ++e) mask |= x[e] >= lo[i] && x[e] < hi[i] ? 1u << e : 0u;
+      }
+    if (!mask) return;
+    uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (mask >> e & 1) {
+        if (at < kMine) {
+          mine[at] = entry_of(v[e], n + e);
+        } else {
+          const uint32_t i = atomicAdd(a.listed + m, 1u);
+          if (i < kList) a.list[m * kList + i] = entry_of(v[e], n + e);
+        }
+        ++at;
+      }
+  });
   __syncthreads();
-  if (t == 0) base = taken ? atomicAdd(a.listed + m, taken) : 0;
+  const uint32_t count = min(taken, (uint32_t)kMine);
+  if (t == 0) base = count ? atomicAdd(a.listed + m, count) : 0;
   __syncthreads();
-  const uint32_t count = min(taken, (uint32_t)kList);
   for (uint32_t i = t; i < count; i += kThreads)
     if (base + i < kList) a.list[m * kList + base + i] = mine[i];
 }
@@ -497,8 +512,8 @@ struct Found {
 enum Search { kByCount, kBySum, kPastSum };
 
 template <int TYPE>
-__device__ __forceinline__ Found search(const SampleArgs& a, const Row& r, int64_t m, int t,
-                                        Search how, uint32_t k, double to) {
+__device__ __forceinline__ Found search(const SampleArgs& a, const Row& r, const double* roots,
+                                        int64_t m, int t, Search how, uint32_t k, double to) {
   __shared__ uint32_t count[256], digit, found_before, found_ties;
   __shared__ u64 weight[256], found_sum, found_weight;
   uint32_t prefix = 0, before = 0;
@@ -511,7 +526,7 @@ __device__ __forceinline__ Found search(const SampleArgs& a, const Row& r, int64
       if (!(z >= r.floor) || (shift < 24 && key >> (shift + 8) != prefix)) return;
       const int b = 255 - (key >> shift & 255);  // the largest first
       atomicAdd(&count[b], 1u);
-      atomicAdd(&weight[b], weight_of(log2_weight(r, z), a.bits));
+      atomicAdd(&weight[b], weight_of(r, z, roots, a.bits));
     });
     __syncthreads();
     const uint32_t mine = t < 256 ? count[t] : 0;
@@ -563,6 +578,7 @@ struct Draw {
   Sums s;
   uint32_t start[kBins];  // a needed bin's first place in the list
   u64 list[kList], ahead[kList + 1];
+  double roots[kRoots];
   u64 found, below;
   uint32_t tokens;
   int which;
@@ -627,7 +643,7 @@ __device__ __forceinline__ Drawn resolve(const SampleArgs& a, const Row& r, cons
     w[e] = 0, bin[e] = 0, z[e] = 0.0f;
     if (i < count) {
       z[e] = value_of((uint32_t)(d.list[i] >> 32));
-      w[e] = weight_of(log2_weight(r, z[e]), a.bits);
+      w[e] = weight_of(r, z[e], d.roots, a.bits);
       bin[e] = bin_of(r, z[e]);
       if (!listed && bin[e] != previous) d.start[bin[e]] = i;
       previous = bin[e];
@@ -699,6 +715,7 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   __shared__ Draw d;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
+  set_roots(d.roots, t);
   const Row r = row_of<kDraw>(a, m, t);
   const Limits& l = r.l;
   if (r.bad || r.greedy) {
@@ -724,7 +741,7 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
     uint32_t some = 0;
     for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
       if (!(z >= r.floor)) return;
-      const u64 w = weight_of(log2_weight(r, z), a.bits);
+      const u64 w = weight_of(r, z, d.roots, a.bits);
       some += 1;
       mine += w;
       kept += z >= r.least ? w : 0;
@@ -735,19 +752,19 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
     __syncthreads();
     u64 whole = d.found;
     if (l.k > 0 && (uint32_t)l.k < d.tokens) {
-      const Found f = search<TYPE>(a, r, m, t, kByCount, (uint32_t)l.k, 0.0);
+      const Found f = search<TYPE>(a, r, d.roots, m, t, kByCount, (uint32_t)l.k, 0.0);
       whole = f.sum + (l.k - f.before) * f.weight;
     }
     if (r.by_p()) {
       const double to = l.p * (double)whole;
-      const Found f = search<TYPE>(a, r, m, t, kBySum, 0, to);
+      const Found f = search<TYPE>(a, r, d.roots, m, t, kBySum, 0, to);
       whole = min(whole, f.sum + place_among(f.sum, f.weight, f.ties, to, false) * f.weight);
     } else if (l.p <= 0.0) {
       whole = 1ull << a.bits;
     }
     if (r.by_q()) whole = min(whole, d.below);
     const double to = l.u * (double)whole;
-    const Found f = search<TYPE>(a, r, m, t, kPastSum, 0, to);
+    const Found f = search<TYPE>(a, r, d.roots, m, t, kPastSum, 0, to);
     const uint32_t place = place_among(f.sum, f.weight, f.ties, to, true);
     const int64_t token = index_of<TYPE>(a, m, t, f.key, place);
     if (t == 0) finish(token, value_of(f.key), whole);
