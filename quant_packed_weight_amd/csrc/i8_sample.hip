@@ -31,7 +31,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kBins = 1024;   // of a row's histogram
+constexpr int kBins = 2048;   // of a row's histogram
 constexpr int kList = 4096;   // tokens that are sorted; a row whose bins hold more is searched
                               // by its logits' bits instead (as where all logits are equal)
 constexpr int kListedK = kList / 2;
@@ -110,8 +110,8 @@ __device__ __forceinline__ Limits limits_of(const SampleArgs& a, int64_t m) {
   return l;
 }
 
-// What a row's launches after the first know of it, from the parts' results and the row's
-// settings (in every thread)
+// What the launches after the first know of a row, from the parts' results and the row's
+// settings: worked out by the second one's workgroups, and kept for the others
 struct Row {
   Limits l;
   double rate;  // log2 e / temperature
@@ -126,6 +126,8 @@ struct Row {
   __device__ bool by_p() const { return l.p > 0.0 && l.p < 1.0; }
   __device__ bool by_q() const { return least > floor; }
 };
+
+__device__ __forceinline__ Row* rows_of(const SampleArgs& a) { return static_cast<Row*>(a.rows); }
 
 // log2 of a token's weight relative to the largest
 __device__ __forceinline__ double log2_weight(const Row& r, float z) {
@@ -197,20 +199,23 @@ __device__ __forceinline__ void set_roots(double* roots, int t) {
 }
 // 2^(x / 32) for x in [-32 (bits + 2), 0] in units of 2^-bits, rounded: x = n + f with f in
 // [-1/2, 1/2], 2^(n / 32) from the roots, and 2^(f / 32) by its series, with c = ln 2 / 32 to
-// (c / 2)^6 / 6! < 10^-14.  (The series of 2^f alone, to f^11, cost twice as much.)
+// (c / 2)^6 / 6! < 10^-14.  (The series of 2^f alone, to f^11, cost twice as much.)  Sums
+// with powers of two stand for conversions, which take four times an addition's time.
 __device__ __forceinline__ u64 weight_of(double x, const double* roots, int bits) {
-  const double n = rint(x), f = x - n;
+  constexpr double kWhole = 6755399441055744.0;  // 1.5 2^52: n in the sum's low bits
+  const double shifted = x + kWhole, f = x - (shifted - kWhole);
+  const int i = (int)__builtin_bit_cast(u64, shifted);
   constexpr double c = 0.6931471805599453 / kRoots;
   double p = c * c * c * c * c / 120.0;
   p = fma(p, f, c * c * c * c / 24.0);
   p = fma(p, f, c * c * c / 6.0);
   p = fma(p, f, c * c / 2.0);
   p = fma(p, f, c);
-  const int i = (int)n;
-  const double root = roots[i & (kRoots - 1)];
-  p = fma(p * f, root, root);
+  const u64 power = (u64)(uint32_t)((i >> 5) + bits) << 52;  // added to the exponent
+  const double root =
+      __builtin_bit_cast(double, __builtin_bit_cast(u64, roots[i & (kRoots - 1)]) + power);
   // at most 2^50: the sum with 2^52 holds the integer in its low bits
-  const double s = __builtin_ldexp(p, (i >> 5) + bits) + 4503599627370496.0;
+  const double s = fma(p * f, root, root) + 4503599627370496.0;
   return __builtin_bit_cast(u64, s) & 0xfffffffffffffull;
 }
 
@@ -258,37 +263,38 @@ __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
 }
 
 // ---- launch 2: the histograms: of tokens where a k decides, of weights where it is not
-// small; one atomic a token for nearly all rows
+// small (both, one after the other, for the few rows of a large k)
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
-  __shared__ uint32_t count[kBins];
-  __shared__ u64 weight[kBins];
+  __shared__ u64 bins[kBins];
   __shared__ double roots[kRoots];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
-  for (int b = t; b < kBins; b += kThreads) count[b] = 0, weight[b] = 0;
+  for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
   set_roots(roots, t);
   const Row r = row_of<kThreads>(a, m, t);  // synchronizes
-  if (r.bad || r.greedy) return;            // all of the row's workgroups
-  const bool counts = r.l.k > 0, weights = !r.listed();
-  if (!weights) {
+  if (blockIdx.x == 0 && t == 0) rows_of(a)[m] = r;
+  if (r.bad || r.greedy) return;  // all of the row's workgroups
+  if (r.l.k > 0) {
+    uint32_t* count = reinterpret_cast<uint32_t*>(bins);
     for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
       if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
     });
-  } else {
-    for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
-      if (!(z >= r.floor)) return;
-      const int b = bin_of(r, z);
-      if (counts) atomicAdd(&count[b], 1u);
-      atomicAdd(&weight[b], weight_of(r, z, roots, a.bits));
-    });
+    __syncthreads();
+    for (int b = t; b < kBins; b += kThreads)
+      if (count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
+    if (r.listed()) return;
+    __syncthreads();
+    for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
+    __syncthreads();
   }
+  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+    if (z >= r.floor) atomicAdd(&bins[bin_of(r, z)], weight_of(r, z, roots, a.bits));
+  });
   __syncthreads();
-  for (int b = t; b < kBins; b += kThreads) {
-    if (counts && count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
-    if (weights && weight[b]) atomicAdd(a.weight + m * kBins + b, weight[b]);
-  }
+  for (int b = t; b < kBins; b += kThreads)
+    if (bins[b]) atomicAdd(a.weight + m * kBins + b, bins[b]);
 }
 
 // ---- what the histograms say
@@ -426,15 +432,19 @@ constexpr int kMine = kList / 2;
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   constexpr int V = kValues<TYPE>;
-  __shared__ Sums s;
-  __shared__ u64 mine[kMine];
+  __shared__ union {
+    Sums sums;  // until the places are known
+    u64 mine[kMine];
+  } lds;
   __shared__ uint32_t taken, base;
+  u64* mine = lds.mine;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
-  if (t == 0) taken = 0;
-  const Row r = row_of<kThreads>(a, m, t);  // synchronizes
+  const Row r = rows_of(a)[m];
   if (r.bad) return;
+  if (t == 0) taken = 0;
+  __syncthreads();
   if (r.greedy) {
     uint32_t first = 0xffffffffu;
     for_logits<TYPE, kThreads>(a, m, begin, end, t,
@@ -442,28 +452,8 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
     if (first != 0xffffffffu) atomicMin(a.first + m, first);
     return;
   }
-  // the places of what is taken: ranges [lo, hi), some empty
-  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (r.listed()) {
-    uint32_t ahead;
-    hi[0] = past(kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead));
-  } else {
-    const Needed need = plan<kThreads>(a, r, m, t, s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (need.lo[i] <= need.hi[i]) lo[i] = (float)need.lo[i], hi[i] = past(need.hi[i]);
-  }
-  for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
-    float x[V];
-    uint32_t mask = 0;
-#pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = v[e] >= r.floor ? place_of(r, v[e]) : -1.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lo[i] < hi[i]) {  // the same in all lanes
-#pragma unroll
-        for (int e = 0; e < V; ++e) mask |= x[e] >= lo[i] && x[e] < hi[i] ? 1u << e : 0u;
-      }
+  // takes those of a piece whose bits are set
+  auto take = [&](const float(&v)[V], int n, uint32_t mask) {
     if (!mask) return;
     uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
 #pragma unroll
@@ -477,7 +467,48 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
         }
         ++at;
       }
-  });
+  };
+  // the places of what is taken: ranges [lo, hi), some empty
+  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (r.listed()) {
+    uint32_t ahead;
+    hi[0] = past(kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead));
+  } else {
+    const Needed need = plan<kThreads>(a, r, m, t, lds.sums);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (need.lo[i] <= need.hi[i]) lo[i] = (float)need.lo[i], hi[i] = past(need.hi[i]);
+  }
+  __syncthreads();
+  const float far = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+  if (r.listed() && far < __builtin_inff()) {
+    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) mask |= place_of(r, v[e]) < far ? 1u << e : 0u;
+      take(v, n, mask);
+    });
+  } else {
+    // what lies below the floor has places from about kBins on
+    const float floor = far < __builtin_inff() ? -__builtin_inff() : r.floor;
+    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+      float x[V];
+      uint32_t mask = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = place_of(r, v[e]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lo[i] < hi[i]) {  // the same in all lanes
+#pragma unroll
+          for (int e = 0; e < V; ++e) mask |= x[e] >= lo[i] && x[e] < hi[i] ? 1u << e : 0u;
+        }
+      if (floor > -__builtin_inff()) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) mask &= v[e] >= floor ? ~0u : ~(1u << e);
+      }
+      take(v, n, mask);
+    });
+  }
   __syncthreads();
   const uint32_t count = min(taken, (uint32_t)kMine);
   if (t == 0) base = count ? atomicAdd(a.listed + m, count) : 0;
@@ -715,8 +746,7 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   __shared__ Draw d;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  set_roots(d.roots, t);
-  const Row r = row_of<kDraw>(a, m, t);
+  const Row r = rows_of(a)[m];
   const Limits& l = r.l;
   if (r.bad || r.greedy) {
     if (t == 0) {
@@ -732,8 +762,10 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
                              (log2_weight(r, z) - (log2((double)whole) - (double)a.bits)));
   };
   const int count = (int)min(a.listed[m], (uint32_t)kList + 1);
+  set_roots(d.roots, t);
 
   if (count > kList) {  // all of the workgroup
+    __syncthreads();    // the roots are there
     // how many tokens there are, and the sums of all and of those from min_p on
     if (t == 0) d.found = 0, d.below = 0, d.tokens = 0;
     __syncthreads();
@@ -788,14 +820,14 @@ constexpr int64_t kRows = 1024;  // of a set of launches: bounds the workspace
 
 struct Layout {
   int64_t rows, chunks, chunk;
-  size_t weight, list, part, count, listed, first, bytes;
+  size_t weight, list, rows_at, part, count, listed, first, bytes;
 };
 
-// A row is split until the launch has 1024 workgroups, into parts of 4096 logits at least
+// A row is split until the launch has 2048 workgroups, into parts of 4096 logits at least
 Layout layout(int64_t M, int64_t N) {
   Layout l;
   l.rows = M < kRows ? M : kRows;
-  int64_t c = ceil_div(1024, l.rows), most = ceil_div(N, 4096);
+  int64_t c = ceil_div(2048, l.rows), most = ceil_div(N, 4096);
   if (c > most) c = most;
   l.chunk = ceil_div(ceil_div(N, c), 2048) * 2048;
   l.chunks = ceil_div(N, l.chunk);
@@ -807,6 +839,7 @@ Layout layout(int64_t M, int64_t N) {
   };
   l.weight = take(8 * l.rows * kBins);
   l.list = take(8 * l.rows * kList);
+  l.rows_at = take((int64_t)sizeof(Row) * l.rows);
   l.part = take((int64_t)sizeof(SamplePart) * l.rows * l.chunks);
   l.count = take(4 * l.rows * kBins);
   l.listed = take(4 * l.rows);
@@ -833,6 +866,7 @@ int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   a.weight = reinterpret_cast<u64*>(p + l.weight);
   a.list = reinterpret_cast<u64*>(p + l.list);
+  a.rows = p + l.rows_at;
   a.part = reinterpret_cast<SamplePart*>(p + l.part);
   a.count = reinterpret_cast<uint32_t*>(p + l.count);
   a.listed = reinterpret_cast<uint32_t*>(p + l.listed);
