@@ -307,6 +307,52 @@ __device__ __forceinline__ void quantize_values(const float (&v)[V], float s, fl
   }
 }
 
+// ---- sums and maxima over a wave, in every lane: within rows of 16 lanes by moves between
+// lanes, across them by exchanged halves (through ds_bpermute a sum in f64 took 12 trips to LDS)
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
+
+// op(own value, the other lane's), for lanes 1, 2, 4, 8, 16 and 32 apart (4 and 8 as mirror
+// images: the lanes of what is joined already hold the same value)
+template <int CTRL, class Op>
+__device__ __forceinline__ double join_lanes(double v, Op op) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t o = (uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b);
+  return op(v, __builtin_bit_cast(double, o));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  auto add = [](double a, double b) { return a + b; };
+  v = join_lanes<kXor1>(v, add);
+  v = join_lanes<kXor2>(v, add);
+  v = join_lanes<kHalfMirror>(v, add);
+  v = join_lanes<kMirror>(v, add);
+  auto halves = [](auto lo, auto hi) {
+    return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) +
+           __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  };
+  uint64_t b = __builtin_bit_cast(uint64_t, v);
+  v = halves(__builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false),
+             __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+  b = __builtin_bit_cast(uint64_t, v);
+  return halves(
+      __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false),
+      __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
 // Workgroup index -> position in the work list such that each of the eight XCDs
 // (consecutive workgroups go to consecutive XCDs) takes one contiguous stretch
 // of it, and neighbours in the list share an L2.

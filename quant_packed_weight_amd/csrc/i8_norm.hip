@@ -30,9 +30,7 @@ __device__ __forceinline__ void load_vector(const float* w, int k, int end, bool
 template <int T, int N>
 __device__ __forceinline__ void sum_all(double (&v)[N], double* at, int t) {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d, 64);
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if ((t & 63) == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) at[N * (t >> 6) + i] = v[i];
@@ -46,110 +44,121 @@ __device__ __forceinline__ void sum_all(double (&v)[N], double* at, int t) {
     for (int i = 0; i < N; ++i) v[i] += at[N * w + i];
 }
 
-// One workgroup per row, which is kept in registers (kHeld 16-byte pieces a thread) as
-// quantize_kernel keeps it; what is beyond them is read twice.
-constexpr int kHeld = 8;
-
-template <int TYPE, int T>
+// The norm, workgroup g of G the rows g, g + G, ...: a row is read once (HELD 16-byte pieces
+// a thread), the next one's loads under way while it is worked on, and the weights stay in
+// registers.  HELD == 0: rows of any width, read twice.
+template <int TYPE, int T, int HELD>
 __global__ __launch_bounds__(T) void rms_kernel(RmsArgs a) {
-  constexpr int V = kValues<TYPE>, kSpan = T * V;
-  __shared__ uint32_t tops[T / 64];
-  __shared__ double sums[T / 64];
-  const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
-  if (m >= a.M) return;  // all of the workgroup
+  constexpr int V = kValues<TYPE>, kSpan = T * V, kKeep = HELD > 0 ? HELD : 1;
+  __shared__ uint32_t tops[2][T / 64];
+  __shared__ double sums[2][T / 64];
   const int t = threadIdx.x, K = a.K;
-  const int64_t x0 = m * a.ldx, r0 = m * a.ldr, h0 = m * a.ldh;
-
-  uint4 held[kHeld], add[kHeld];
+  float w[kKeep][V];
+  uint4 x[kKeep], r[kKeep];
+  auto load = [&](int64_t m) {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int k = kSpan * i + V * t;
-    if (kSpan * i < K) {
-      held[i] = load_raw<TYPE>(a.X, x0 + k, K - k, a.wide_x);
-      if (a.R) add[i] = load_raw<TYPE>(a.R, r0 + k, K - k, a.wide_r);
+    for (int i = 0; i < HELD; ++i) {
+      const int k = kSpan * i + V * t;
+      if (kSpan * i < K) {
+        x[i] = load_raw<TYPE>(a.X, m * a.ldx + k, K - k, a.wide_x);
+        if (a.R) r[i] = load_raw<TYPE>(a.R, m * a.ldr + k, K - k, a.wide_r);
+      }
     }
-  }
-  uint32_t top = 0;
-  double ss[1] = {0.0};
-  // h of 16 bytes, its share of the two statistics taken and H written
-  auto take = [&](int k, uint4 x, uint4 r) {
-    float v[V], w[V];
-    unpack<TYPE, V>(x, v);
-    if (a.R) {
-      float o[V];
-      unpack<TYPE, V>(r, o);
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[e] += o[e];
-      x = pack<TYPE, V>(v);
-      unpack<TYPE, V>(x, v);
-    }
-    if (a.H) store_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h, x);
-    load_vector<V>(a.w, k, K, a.wide_w, w);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      top = max(top, abs_bits(v[e] * w[e]));
-      ss[0] = fma((double)v[e], (double)v[e], ss[0]);
-    }
-    return x;
   };
+  // h of 16 bytes
+  auto add = [&](uint4 xw, uint4 rw) {
+    if (!a.R) return xw;
+    float v[V], o[V];
+    unpack<TYPE, V>(xw, v);
+    unpack<TYPE, V>(rw, o);
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (kSpan * i < K) held[i] = take(kSpan * i + V * t, held[i], add[i]);
-  for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
-    const uint4 x = load_raw<TYPE>(a.X, x0 + k, K - k, a.wide_x);
-    take(k, x, a.R ? load_raw<TYPE>(a.R, r0 + k, K - k, a.wide_r) : x);
-  }
+    for (int e = 0; e < V; ++e) v[e] += o[e];
+    return pack<TYPE, V>(v);
+  };
+  load(blockIdx.x);
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-  if ((t & 63) == 0) tops[t >> 6] = top;
-  sum_all<T>(ss, sums, t);
-  top = tops[0];
-#pragma unroll
-  for (int w = 1; w < T / 64; ++w) top = max(top, tops[w]);
-  const float sc = scale_of(top);
-  const float inv = 1.0f / sc;
-  // (a row of zeros has the scale 0 whatever eps is)
-  if (t == 0)
-    a.s[m] = sc == 0.0f ? 0.0f : (float)((double)sc / sqrt(ss[0] / K + (double)a.eps));
+  for (int i = 0; i < HELD; ++i)
+    if (kSpan * i < K) load_vector<V>(a.w, kSpan * i + V * t, K, a.wide_w, w[i]);
 
-  auto store = [&](int k, uint4 x) {
-    float v[V], w[V];
-    unpack<TYPE, V>(x, v);
-    load_vector<V>(a.w, k, K, a.wide_w, w);
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    uint32_t top = 0;
+    double ss[1] = {0.0};
+    // the share of 16 bytes of h in the two statistics, and H written
+    auto take = [&](int k, uint4 h, const float(&wv)[V]) {
+      if (a.H) store_raw<TYPE>(a.H, m * a.ldh + k, K - k, a.wide_h, h);
+      float v[V];
+      unpack<TYPE, V>(h, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] *= w[e];
-    uint32_t q[V / 4];
-    quantize_values<V>(v, sc, inv, q);
-    int8_t* to = a.Q + m * a.ldq + k;
-    if (k + V <= K) {
+      for (int e = 0; e < V; ++e) {
+        top = max(top, abs_bits(v[e] * wv[e]));
+        ss[0] = fma((double)v[e], (double)v[e], ss[0]);
+      }
+    };
+    uint4 held[kKeep];
+    if constexpr (HELD > 0) {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) reinterpret_cast<uint32_t*>(to)[i] = q[i];
+      for (int i = 0; i < HELD; ++i)
+        if (kSpan * i < K) held[i] = add(x[i], r[i]);
+      if (m + gridDim.x < a.M) load(m + gridDim.x);
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (kSpan * i < K) take(kSpan * i + V * t, held[i], w[i]);
     } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (k + e < K) to[e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+      for (int k = V * t; k < K; k += kSpan) {
+        const uint4 xw = load_raw<TYPE>(a.X, m * a.ldx + k, K - k, a.wide_x);
+        const uint4 h = add(xw, a.R ? load_raw<TYPE>(a.R, m * a.ldr + k, K - k, a.wide_r) : xw);
+        load_vector<V>(a.w, k, K, a.wide_w, w[0]);
+        take(k, h, w[0]);
+      }
     }
-  };
+    top = wave_max(top);
+    if ((t & 63) == 0) tops[turn][t >> 6] = top;
+    // (two sets of LDS: a wave may be a row ahead of one that still reads them)
+    sum_all<T>(ss, sums[turn], t);
+    top = tops[turn][0];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (kSpan * i < K) store(kSpan * i + V * t, held[i]);
-  // what was not kept: h where it was written (by this thread: X or R may be H), else
-  // x + r once more
-  for (int k = kSpan * kHeld + V * t; k < K; k += kSpan) {
-    if (a.H) {
-      store(k, load_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h));
-      continue;
-    }
-    uint4 x = load_raw<TYPE>(a.X, x0 + k, K - k, a.wide_x);
-    if (a.R) {
-      float v[V], o[V];
-      unpack<TYPE, V>(x, v);
-      load_values<TYPE, V>(a.R, r0 + k, K - k, a.wide_r, o);
+    for (int i = 1; i < T / 64; ++i) top = max(top, tops[turn][i]);
+    const float sc = scale_of(top);
+    const float inv = 1.0f / sc;
+    // (a row of zeros has the scale 0 whatever eps is)
+    if (t == 0)
+      a.s[m] = sc == 0.0f ? 0.0f : (float)((double)sc / sqrt(ss[0] / K + (double)a.eps));
+    auto store = [&](int k, uint4 h, const float(&wv)[V]) {
+      float v[V];
+      unpack<TYPE, V>(h, v);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] += o[e];
-      x = pack<TYPE, V>(v);
+      for (int e = 0; e < V; ++e) v[e] *= wv[e];
+      uint32_t q[V / 4];
+      quantize_values<V>(v, sc, inv, q);
+      int8_t* to = a.Q + m * a.ldq + k;
+      if (k + V <= K) {
+        if constexpr (V == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
+        else
+          *reinterpret_cast<uint32_t*>(to) = q[0];
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (k + e < K) to[e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+      }
+    };
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (kSpan * i < K) store(kSpan * i + V * t, held[i], w[i]);
+    } else {
+      // h where it was written (by this thread: X or R may be H), else x + r once more
+      for (int k = V * t; k < K; k += kSpan) {
+        load_vector<V>(a.w, k, K, a.wide_w, w[0]);
+        if (a.H) {
+          store(k, load_raw<TYPE>(a.H, m * a.ldh + k, K - k, a.wide_h), w[0]);
+          continue;
+        }
+        const uint4 xw = load_raw<TYPE>(a.X, m * a.ldx + k, K - k, a.wide_x);
+        store(k, add(xw, a.R ? load_raw<TYPE>(a.R, m * a.ldr + k, K - k, a.wide_r) : xw), w[0]);
+      }
     }
-    store(k, x);
   }
 }
 
@@ -176,10 +185,24 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
       }
     }
   }
+  // the next row's pieces
+  uint4 hn[kKeep], yn[kKeep], dn[kKeep];
+  auto load = [&](int64_t m) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int k = kSpan * i + V * t;
+      if (kSpan * i < K) {
+        hn[i] = load_raw<TYPE>(a.H, m * a.ldh + k, K - k, a.wide_h);
+        yn[i] = load_raw<TYPE>(a.dY, m * a.lddy + k, K - k, a.wide_dy);
+        if (a.dH) dn[i] = load_raw<TYPE>(a.dH, m * a.lddh + k, K - k, a.wide_dh);
+      }
+    }
+  };
+  load(blockIdx.x);
   int turn = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
     const int64_t h0 = m * a.ldh, y0 = m * a.lddy, d0 = m * a.lddh, x0 = m * a.lddx;
-    uint4 hr[kKeep], yr[kKeep];
+    uint4 hr[kKeep], yr[kKeep], dr[kKeep];
     double s[2] = {0.0, 0.0};  // of h^2 and of d h
     auto take = [&](uint4 hw, uint4 yw, const float(&wv)[V]) {
       float h[V], y[V];
@@ -193,13 +216,8 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
     };
     if constexpr (HELD > 0) {
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
-        const int k = kSpan * i + V * t;
-        if (kSpan * i < K) {
-          hr[i] = load_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h);
-          yr[i] = load_raw<TYPE>(a.dY, y0 + k, K - k, a.wide_dy);
-        }
-      }
+      for (int i = 0; i < HELD; ++i) hr[i] = hn[i], yr[i] = yn[i], dr[i] = dn[i];
+      if (m + gridDim.x < a.M) load(m + gridDim.x);
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
         if (kSpan * i < K) take(hr[i], yr[i], w[i]);
@@ -214,7 +232,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
     sum_all<T>(s, sums[turn], t);
     const double r = 1.0 / sqrt(s[0] / K + (double)a.eps);
     const float rstd = (float)r, mean = (float)(s[1] * r / K);
-    auto give = [&](int k, uint4 hw, uint4 yw, const float(&wv)[V], float(&dwv)[V]) {
+    auto give = [&](int k, uint4 hw, uint4 yw, uint4 dw4, const float(&wv)[V], float(&dwv)[V]) {
       float h[V], y[V], dx[V];
       unpack<TYPE, V>(hw, h);
       unpack<TYPE, V>(yw, y);
@@ -226,7 +244,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
       }
       if (a.dH) {
         float o[V];
-        load_values<TYPE, V>(a.dH, d0 + k, K - k, a.wide_dh, o);
+        unpack<TYPE, V>(dw4, o);
 #pragma unroll
         for (int e = 0; e < V; ++e) dx[e] += o[e];
       }
@@ -235,7 +253,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
     if constexpr (HELD > 0) {
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
-        if (kSpan * i < K) give(kSpan * i + V * t, hr[i], yr[i], w[i], dw[DW ? i : 0]);
+        if (kSpan * i < K) give(kSpan * i + V * t, hr[i], yr[i], dr[i], w[i], dw[DW ? i : 0]);
     } else {
       for (int k = V * t; k < K; k += kSpan) {
         load_vector<V>(a.w, k, K, a.wide_w, w[0]);
@@ -244,8 +262,9 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
           for (int e = 0; e < V; ++e)
             dw[0][e] = m < gridDim.x || k + e >= a.kp ? 0.0f : part[k + e];
         }
-        give(k, load_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h),
-             load_raw<TYPE>(a.dY, y0 + k, K - k, a.wide_dy), w[0], dw[0]);
+        const uint4 h = load_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h);
+        give(k, h, load_raw<TYPE>(a.dY, y0 + k, K - k, a.wide_dy),
+             a.dH ? load_raw<TYPE>(a.dH, d0 + k, K - k, a.wide_dh) : h, w[0], dw[0]);
         if constexpr (DW) {
 #pragma unroll
           for (int e = 0; e < V; ++e)
@@ -267,14 +286,15 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
   }
 }
 
-// out[k] = the sum of part[g][k] over g < count, 64 columns a workgroup, its four waves a
-// quarter of the rows each
-__global__ __launch_bounds__(256) void join_kernel(const float* part, int64_t pitch, int count,
-                                                   float* out, int K) {
-  __shared__ float sums[4][64];
+// out[k] = the sum of part[g][k] over g < count: 64 columns a workgroup, its waves a
+// sixteenth of the rows each
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const float* part, int64_t pitch,
+                                                               int count, float* out, int K) {
+  __shared__ float sums[kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t k = (int64_t)blockIdx.x * 64 + lane;
-  const int each = (count + 3) / 4, end = min(count, each * (wave + 1));
+  const int each = (count + kJoinWaves - 1) / kJoinWaves, end = min(count, each * (wave + 1));
   float s = 0.0f;
   if (k < K) {
 #pragma unroll 8
@@ -282,9 +302,13 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int64_t pi
   }
   sums[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && k < K)
-    out[k] = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+  if (wave > 0 || k >= K) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWaves; ++w) s += sums[w][lane];
+  out[k] = s;
 }
+
+constexpr int kRmsGroups = 1024;
 
 template <int TYPE, bool DW>
 void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
@@ -297,16 +321,24 @@ void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
     rms_grad_kernel<TYPE, 1024, 0, DW><<<groups, 1024, 0, st>>>(a);
 }
 
+template <int TYPE>
+void launch_type(const RmsArgs& a, hipStream_t st) {
+  constexpr int V = kValues<TYPE>;
+  const uint32_t g = a.M < kRmsGroups ? a.M : kRmsGroups;
+  if (a.K <= 256 * 2 * V)
+    rms_kernel<TYPE, 256, 2><<<g, 256, 0, st>>>(a);
+  else if (a.K <= 512 * 4 * V)
+    rms_kernel<TYPE, 512, 4><<<g, 512, 0, st>>>(a);
+  else
+    rms_kernel<TYPE, 1024, 0><<<g, 1024, 0, st>>>(a);
+}
+
 }  // namespace
 
 int launch_rms(const RmsArgs& a, hipStream_t st) {
-  const dim3 g = rows_grid(1, a.M);
-  if (a.type == GEMMQ_F32)
-    rms_kernel<GEMMQ_F32, 256><<<g, 256, 0, st>>>(a);
-  else if (a.type == GEMMQ_BF16)
-    rms_kernel<GEMMQ_BF16, 256><<<g, 256, 0, st>>>(a);
-  else
-    rms_kernel<GEMMQ_F16, 256><<<g, 256, 0, st>>>(a);
+  a.type == GEMMQ_F32    ? launch_type<GEMMQ_F32>(a, st)
+  : a.type == GEMMQ_BF16 ? launch_type<GEMMQ_BF16>(a, st)
+                         : launch_type<GEMMQ_F16>(a, st);
   return 0;
 }
 
@@ -325,7 +357,7 @@ int launch_rms_grad(const RmsGradArgs& a, hipStream_t st) {
 }
 
 int launch_join(const float* part, int64_t pitch, int count, float* out, int K, hipStream_t st) {
-  join_kernel<<<(uint32_t)ceil_div(K, 64), 256, 0, st>>>(part, pitch, count, out, K);
+  join_kernel<<<(uint32_t)ceil_div(K, 64), 64 * kJoinWaves, 0, st>>>(part, pitch, count, out, K);
   return 0;
 }
 

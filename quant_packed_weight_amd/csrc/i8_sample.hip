@@ -51,27 +51,42 @@ __device__ __forceinline__ u64 entry_of(float z, uint32_t index) {
   return (u64)key_of(z) << 32 | (uint32_t)~index;
 }
 
-// goes through logits [begin, end) of row m in 16-byte pieces, the loads of kAhead of them
-// under way at a time: piece(v, index of v[0]), with -inf, which counts nowhere, past the end
-constexpr int kAhead = 4;
-template <int TYPE, int T, class Piece>
-__device__ __forceinline__ void for_pieces(const SampleArgs& a, int64_t m, int begin, int end, int t,
-                                           Piece piece) {
-  constexpr int V = kValues<TYPE>, kSpan = V * T;
-  for (int n0 = begin; n0 < end; n0 += kSpan * kAhead) {
-    uint4 raw[kAhead];
+// A workgroup's part of a row in registers: kPieces 16-byte pieces a thread at most.  Launches
+// 1 to 3 load it whole before they look at anything else, so that what they work out of the
+// row first overlaps the loads.
+constexpr int kPieces = 8;
+template <int TYPE>
+struct Part {
+  static constexpr int V = kValues<TYPE>, kSpan = V * kThreads;
+  uint4 raw[kPieces];
+  int begin, end, t;
+
+  __device__ __forceinline__ Part(const SampleArgs& a, int64_t m, int part, int thread) {
+    t = thread;
+    begin = part * a.chunk;
+    end = min(begin + a.chunk, a.N);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int n = n0 + kSpan * i + V * t;
-      raw[i] = load_raw<TYPE>(a.Z, m * a.ldz + n, end - n, a.wide);
+    for (int i = 0; i < kPieces; ++i) {
+      const int n0 = begin + kSpan * i, n = n0 + V * t;
+      if (n0 >= end) break;
+      // (the same way in all lanes wherever the piece is whole)
+      if (a.wide && n0 + kSpan <= end)
+        raw[i] = load_raw<TYPE>(a.Z, m * a.ldz + n, V, true);
+      else
+        raw[i] = load_raw<TYPE>(a.Z, m * a.ldz + n, end - n, a.wide);
     }
+    asm volatile("" ::: "memory");  // or the compiler moves each load to its use
+  }
+  // piece(v, index of v[0]) for each, with -inf, which counts nowhere, past the end
+  template <class Piece>
+  __device__ __forceinline__ void pieces(Piece piece) const {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int n = n0 + kSpan * i + V * t;
-      if (n >= end) break;
+    for (int i = 0; i < kPieces; ++i) {
+      const int n0 = begin + kSpan * i, n = n0 + V * t;
+      if (n0 >= end) break;
       float v[V];
       unpack<TYPE, V>(raw[i], v);
-      if (n + V > end) {
+      if (n0 + kSpan > end) {
 #pragma unroll
         for (int e = 0; e < V; ++e)
           if (n + e >= end) v[e] = -__builtin_inff();
@@ -79,16 +94,27 @@ __device__ __forceinline__ void for_pieces(const SampleArgs& a, int64_t m, int b
       piece(v, n);
     }
   }
-}
-// each(z, index)
-template <int TYPE, int T, class Each>
-__device__ __forceinline__ void for_logits(const SampleArgs& a, int64_t m, int begin, int end, int t,
-                                           Each each) {
-  constexpr int V = kValues<TYPE>;
-  for_pieces<TYPE, T>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+  // each(z, index)
+  template <class Each>
+  __device__ __forceinline__ void logits(Each each) const {
+    pieces([&](const float(&v)[V], int n) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) each(v[e], n + e);
-  });
+      for (int e = 0; e < V; ++e) each(v[e], n + e);
+    });
+  }
+};
+
+// each(z, index) for a whole row, by a workgroup of T threads
+template <int TYPE, int T, class Each>
+__device__ __forceinline__ void for_row(const SampleArgs& a, int64_t m, int t, Each each) {
+  constexpr int V = kValues<TYPE>;
+  for (int n = V * t; n < a.N; n += V * T) {
+    float v[V];
+    load_values<TYPE, V>(a.Z, m * a.ldz + n, a.N - n, a.wide, v);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (n + e < a.N) each(v[e], n + e);
+  }
 }
 
 struct Limits {
@@ -230,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
   __shared__ SamplePart parts[kThreads / 64];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
+  const Part<TYPE> part(a, m, blockIdx.x, t);
   for (int b = blockIdx.x * kThreads + t; b < kBins; b += gridDim.x * kThreads) {
     a.count[m * kBins + b] = 0;
     a.weight[m * kBins + b] = 0;
@@ -238,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
   if (blockIdx.x == 0 && t == 0) a.listed[m] = 0, a.first[m] = 0xffffffffu;
   SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
   bool nan = false;
-  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+  part.logits([&](float z, int) {
     nan |= z != z;
     z = __builtin_canonicalizef(z);  // once, not for each of the two
     s.top = fmaxf(s.top, z);
@@ -270,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   __shared__ double roots[kRoots];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
+  const Part<TYPE> part(a, m, blockIdx.x, t);
   for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
   set_roots(roots, t);
   const Row r = row_of<kThreads>(a, m, t);  // synchronizes
@@ -278,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   if (r.bad || r.greedy) return;  // all of the row's workgroups
   if (r.l.k > 0) {
     uint32_t* count = reinterpret_cast<uint32_t*>(bins);
-    for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+    part.logits([&](float z, int) {
       if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
     });
     __syncthreads();
@@ -289,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
     for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
     __syncthreads();
   }
-  for_logits<TYPE, kThreads>(a, m, begin, end, t, [&](float z, int) {
+  part.logits([&](float z, int) {
     if (z >= r.floor) atomicAdd(&bins[bin_of(r, z)], weight_of(r, z, roots, a.bits));
   });
   __syncthreads();
@@ -440,15 +466,14 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   u64* mine = lds.mine;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.N);
+  const Part<TYPE> part(a, m, blockIdx.x, t);
   const Row r = rows_of(a)[m];
   if (r.bad) return;
   if (t == 0) taken = 0;
   __syncthreads();
   if (r.greedy) {
     uint32_t first = 0xffffffffu;
-    for_logits<TYPE, kThreads>(a, m, begin, end, t,
-                               [&](float z, int n) { if (z == r.top) first = min(first, (uint32_t)n); });
+    part.logits([&](float z, int n) { first = z == r.top ? min(first, (uint32_t)n) : first; });
     if (first != 0xffffffffu) atomicMin(a.first + m, first);
     return;
   }
@@ -482,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   __syncthreads();
   const float far = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
   if (r.listed() && far < __builtin_inff()) {
-    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+    part.pieces([&](const float(&v)[V], int n) {
       uint32_t mask = 0;
 #pragma unroll
       for (int e = 0; e < V; ++e) mask |= place_of(r, v[e]) < far ? 1u << e : 0u;
@@ -491,7 +516,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   } else {
     // what lies below the floor has places from about kBins on
     const float floor = far < __builtin_inff() ? -__builtin_inff() : r.floor;
-    for_pieces<TYPE, kThreads>(a, m, begin, end, t, [&](const float(&v)[V], int n) {
+    part.pieces([&](const float(&v)[V], int n) {
       float x[V];
       uint32_t mask = 0;
 #pragma unroll
@@ -552,7 +577,7 @@ __device__ __forceinline__ Found search(const SampleArgs& a, const Row& r, const
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (t < 256) count[t] = 0, weight[t] = 0;
     __syncthreads();
-    for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
+    for_row<TYPE, kDraw>(a, m, t, [&](float z, int) {
       const uint32_t key = key_of(z);
       if (!(z >= r.floor) || (shift < 24 && key >> (shift + 8) != prefix)) return;
       const int b = 255 - (key >> shift & 255);  // the largest first
@@ -771,7 +796,7 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
     __syncthreads();
     u64 mine = 0, kept = 0;
     uint32_t some = 0;
-    for_logits<TYPE, kDraw>(a, m, 0, a.N, t, [&](float z, int) {
+    for_row<TYPE, kDraw>(a, m, t, [&](float z, int) {
       if (!(z >= r.floor)) return;
       const u64 w = weight_of(r, z, d.roots, a.bits);
       some += 1;
@@ -823,13 +848,15 @@ struct Layout {
   size_t weight, list, rows_at, part, count, listed, first, bytes;
 };
 
-// A row is split until the launch has 2048 workgroups, into parts of 4096 logits at least
-Layout layout(int64_t M, int64_t N) {
+// Parts of a row: the largest that leave a launch 1024 workgroups, of eight pieces a thread to
+// two
+Layout layout(int type, int64_t M, int64_t N) {
   Layout l;
   l.rows = M < kRows ? M : kRows;
-  int64_t c = ceil_div(2048, l.rows), most = ceil_div(N, 4096);
-  if (c > most) c = most;
-  l.chunk = ceil_div(ceil_div(N, c), 2048) * 2048;
+  const int64_t span = (type == GEMMQ_F32 ? 4 : 8) * kThreads;
+  int64_t pieces = kPieces;
+  while (pieces > 2 && l.rows * ceil_div(N, pieces * span) < 1024) pieces /= 2;
+  l.chunk = pieces * span;
   l.chunks = ceil_div(N, l.chunk);
   size_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -859,10 +886,12 @@ void launch_type(const SampleArgs& a, int rows, hipStream_t st) {
 
 }  // namespace
 
-size_t sample_workspace(int64_t M, int64_t N) { return layout(M, N).bytes; }
+size_t sample_workspace(int64_t M, int64_t N) {
+  return layout(GEMMQ_F32, M, N).bytes;  // whose parts are the smaller ones
+}
 
 int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st) {
-  const Layout l = layout(M, a.N);
+  const Layout l = layout(type, M, a.N);
   uint8_t* p = static_cast<uint8_t*>(ws);
   a.weight = reinterpret_cast<u64*>(p + l.weight);
   a.list = reinterpret_cast<u64*>(p + l.list);
