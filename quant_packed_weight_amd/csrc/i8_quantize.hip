@@ -6,16 +6,14 @@ namespace gemmq {
 namespace i8 {
 namespace {
 
-// One workgroup per row; a thread keeps up to kHeld 16-byte loads of it in
+// One workgroup of T threads per row; a thread keeps up to kHeld 16-byte loads of it in
 // registers between the two passes (rows of up to 8192 f32 or 16384 bf16 and f16
 // values are read once), and reads what is beyond them again.
-constexpr int kHeld = 8;
-
-template <int TYPE>
-__global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ldx, bool wide,
-                                                       int8_t* Q, int64_t ldq, float* s, int M, int K) {
-  constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8, kSpan = 256 * V;
-  __shared__ uint32_t tops[4];
+template <int TYPE, int T>
+__global__ __launch_bounds__(T) void quantize_kernel(const void* X, int64_t ldx, bool wide,
+                                                     int8_t* Q, int64_t ldq, float* s, int M, int K) {
+  constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8, kSpan = T * V, kHeld = 2048 / T;
+  __shared__ uint32_t tops[T / 64];
   const int64_t m = blockIdx.y + (int64_t)gridDim.y * blockIdx.z, x0 = m * ldx;
   if (m >= M) return;  // all of the workgroup
   const int t = threadIdx.x;
@@ -40,11 +38,12 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
 #pragma unroll
     for (int e = 0; e < V; ++e) top = max(top, abs_bits(v[e]));
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  top = wave_max(top);
   if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
-  const float sc = scale_of(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) top = max(top, tops[w]);
+  const float sc = scale_of(top);
   const float inv = 1.0f / sc;
   if (t == 0) s[m] = sc;
   auto store = [&](int k, const float (&v)[V]) {
@@ -74,18 +73,27 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t ld
   }
 }
 
+template <int TYPE>
+void launch_type(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M, int K,
+                 hipStream_t st) {
+  const dim3 g = rows_grid(1, M);
+  const bool wide = wide_rows(X, ldx, TYPE);
+  // 512 threads where a row is more than one piece a thread of 256 (us, 256 / 512 threads:
+  // bf16, M = 16, K = 2048 2.8 / 3.0, 4096 3.3 / 2.8, 12288 5.1 / 4.1; M = 2048, K = 4096 7.1 /
+  // 7.0, 12288 16.8 / 14.9; f32, M = 2048, K = 4096 7.5 / 8.4, 12288 24.3 / 23.1)
+  if (K > 256 * kValues<TYPE>)
+    quantize_kernel<TYPE, 512><<<g, 512, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
+  else
+    quantize_kernel<TYPE, 256><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
+}
+
 }  // namespace
 
 int launch_quantize(int type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* s, int M,
                     int K, hipStream_t st) {
-  const dim3 g = rows_grid(1, M);
-  const bool wide = wide_rows(X, ldx, type);
-  if (type == GEMMQ_F32)
-    quantize_kernel<GEMMQ_F32><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
-  else if (type == GEMMQ_BF16)
-    quantize_kernel<GEMMQ_BF16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
-  else
-    quantize_kernel<GEMMQ_F16><<<g, 256, 0, st>>>(X, ldx, wide, Q, ldq, s, M, K);
+  type == GEMMQ_F32    ? launch_type<GEMMQ_F32>(X, ldx, Q, ldq, s, M, K, st)
+  : type == GEMMQ_BF16 ? launch_type<GEMMQ_BF16>(X, ldx, Q, ldq, s, M, K, st)
+                       : launch_type<GEMMQ_F16>(X, ldx, Q, ldq, s, M, K, st);
   return 0;
 }
 
