@@ -13,8 +13,10 @@
 //   else by a histogram of weights, the bins that the places lie in.  Bounds of the sum that
 //   one limit leaves give the next one a range of bins.
 //
-// Four launches: the rows' largest logits; the histograms; the gathering; the draw.  A row is
-// spread over as many workgroups as fill the chip, but for the draw.
+// A row of up to 32768 f32 or 65536 16-bit logits is held by one workgroup's registers, and one
+// launch does all of it (whole_kernel).  Longer ones, and in some cases (is_whole) shorter ones,
+// are spread over as many workgroups as fill the chip, in four launches: the rows' largest
+// logits; the histograms; the gathering; the draw.
 //
 // Weights are integers, e = exp((z - max) / t) in units of 2^-bits: their sums are exact, so
 // atomics may add them in any order.  e is computed in f64, to 10^-14: with f32's 10^-7 one
@@ -55,18 +57,19 @@ __device__ __forceinline__ u64 entry_of(float z, uint32_t index) {
 // 1 to 3 load it whole before they look at anything else, so that what they work out of the
 // row first overlaps the loads.
 constexpr int kPieces = 8;
-template <int TYPE>
+template <int TYPE, int T = kThreads, int P = kPieces>
 struct Part {
-  static constexpr int V = kValues<TYPE>, kSpan = V * kThreads;
-  uint4 raw[kPieces];
+  static constexpr int V = kValues<TYPE>, kSpan = V * T;
+  uint4 raw[P];
   int begin, end, t;
 
-  __device__ __forceinline__ Part(const SampleArgs& a, int64_t m, int part, int thread) {
+  // logits [first, past) of row m, at most P * kSpan of them
+  __device__ __forceinline__ Part(const SampleArgs& a, int64_t m, int first, int past, int thread) {
     t = thread;
-    begin = part * a.chunk;
-    end = min(begin + a.chunk, a.N);
+    begin = first;
+    end = past;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       const int n0 = begin + kSpan * i, n = n0 + V * t;
       if (n0 >= end) break;
       // (the same way in all lanes wherever the piece is whole)
@@ -81,7 +84,7 @@ struct Part {
   template <class Piece>
   __device__ __forceinline__ void pieces(Piece piece) const {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < P; ++i) {
       const int n0 = begin + kSpan * i, n = n0 + V * t;
       if (n0 >= end) break;
       float v[V];
@@ -103,6 +106,13 @@ struct Part {
     });
   }
 };
+
+// the workgroup's part of its row
+template <int TYPE>
+__device__ __forceinline__ Part<TYPE> part_of(const SampleArgs& a, int64_t m, int t) {
+  const int begin = blockIdx.x * a.chunk;
+  return Part<TYPE>(a, m, begin, min(begin + a.chunk, a.N), t);
+}
 
 // each(z, index) for a whole row, by a workgroup of T threads
 template <int TYPE, int T, class Each>
@@ -170,27 +180,44 @@ __device__ __forceinline__ float past(int hi) {
   return hi == kBins - 1 ? __builtin_inff() : (float)(hi + 1);
 }
 
+__device__ __forceinline__ void join(SamplePart& s, const SamplePart& o) {
+  s.top = fmaxf(s.top, o.top);
+  s.low = fminf(s.low, o.low);
+  s.bad |= o.bad;
+}
+// over the workgroup's T threads, in every one
 template <int T>
-__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t m, int t) {
+__device__ __forceinline__ SamplePart join_all(SamplePart s, int t) {
   __shared__ SamplePart parts[T / 64];
-  SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
-  auto join = [&](const SamplePart& o) {
-    s.top = fmaxf(s.top, o.top);
-    s.low = fminf(s.low, o.low);
-    s.bad |= o.bad;
-  };
-  const float temperature = a.temperature ? a.temperature[m] : 1.0f;
-  Row r;
-  r.l = limits_of(a, m);
-  for (int c = t; c < a.chunks; c += T) join(a.part[m * a.chunks + c]);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2)
-    join(SamplePart{__shfl_xor(s.top, d, 64), __shfl_xor(s.low, d, 64),
-                    (uint32_t)__shfl_xor((int)s.bad, d, 64)});
+    join(s, SamplePart{__shfl_xor(s.top, d, 64), __shfl_xor(s.low, d, 64),
+                       (uint32_t)__shfl_xor((int)s.bad, d, 64)});
   if ((t & 63) == 0) parts[t >> 6] = s;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < T / 64; ++w) join(parts[w]);
+  for (int w = 0; w < T / 64; ++w) join(s, parts[w]);
+  return s;
+}
+// of a thread's logits
+template <class P>
+__device__ __forceinline__ SamplePart survey(const P& part) {
+  SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
+  bool nan = false;
+  part.logits([&](float z, int) {
+    nan |= z != z;
+    z = __builtin_canonicalizef(z);  // once, not for each of the two
+    s.top = fmaxf(s.top, z);
+    s.low = fminf(s.low, z == -__builtin_inff() ? __builtin_inff() : z);
+  });
+  s.bad = nan || s.top == __builtin_inff();
+  return s;
+}
+
+__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t m, const SamplePart& s) {
+  const float temperature = a.temperature ? a.temperature[m] : 1.0f;
+  Row r;
+  r.l = limits_of(a, m);
   r.top = s.top;
   // (a row without a finite logit has no lowest one)
   r.bad = s.bad || s.low > FLT_MAX || !(temperature < __builtin_inff());
@@ -253,39 +280,31 @@ __device__ __forceinline__ u64 weight_of(const Row& r, float z, const double* ro
 // the row cannot be drawn from; and its share of what the next launches add to
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a) {
-  __shared__ SamplePart parts[kThreads / 64];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const Part<TYPE> part(a, m, blockIdx.x, t);
+  const Part<TYPE> part = part_of<TYPE>(a, m, t);
   for (int b = blockIdx.x * kThreads + t; b < kBins; b += gridDim.x * kThreads) {
     a.count[m * kBins + b] = 0;
     a.weight[m * kBins + b] = 0;
   }
   if (blockIdx.x == 0 && t == 0) a.listed[m] = 0, a.first[m] = 0xffffffffu;
-  SamplePart s{-__builtin_inff(), __builtin_inff(), 0};
-  bool nan = false;
+  const SamplePart s = join_all<kThreads>(survey(part), t);
+  if (t == 0) a.part[m * a.chunks + blockIdx.x] = s;
+}
+
+// a thread's share of the histograms, in LDS
+template <class P>
+__device__ __forceinline__ void count_tokens(const P& part, const Row& r, uint32_t* count) {
   part.logits([&](float z, int) {
-    nan |= z != z;
-    z = __builtin_canonicalizef(z);  // once, not for each of the two
-    s.top = fmaxf(s.top, z);
-    s.low = fminf(s.low, z == -__builtin_inff() ? __builtin_inff() : z);
+    if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
   });
-  s.bad = nan || s.top == __builtin_inff();
-  auto join = [&](const SamplePart& o) {
-    s.top = fmaxf(s.top, o.top);
-    s.low = fminf(s.low, o.low);
-    s.bad |= o.bad;
-  };
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2)
-    join(SamplePart{__shfl_xor(s.top, d, 64), __shfl_xor(s.low, d, 64),
-                    (uint32_t)__shfl_xor((int)s.bad, d, 64)});
-  if ((t & 63) == 0) parts[t >> 6] = s;
-  __syncthreads();
-  if (t != 0) return;
-#pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) join(parts[w]);
-  a.part[m * a.chunks + blockIdx.x] = s;
+}
+template <class P>
+__device__ __forceinline__ void sum_weights(const P& part, const Row& r, u64* weight,
+                                            const double* roots, int bits) {
+  part.logits([&](float z, int) {
+    if (z >= r.floor) atomicAdd(&weight[bin_of(r, z)], weight_of(r, z, roots, bits));
+  });
 }
 
 // ---- launch 2: the histograms: of tokens where a k decides, of weights where it is not
@@ -296,17 +315,17 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   __shared__ double roots[kRoots];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const Part<TYPE> part(a, m, blockIdx.x, t);
+  const Part<TYPE> part = part_of<TYPE>(a, m, t);
   for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
   set_roots(roots, t);
-  const Row r = row_of<kThreads>(a, m, t);  // synchronizes
+  SamplePart all{-__builtin_inff(), __builtin_inff(), 0};
+  for (int c = t; c < a.chunks; c += kThreads) join(all, a.part[m * a.chunks + c]);
+  const Row r = row_of(a, m, join_all<kThreads>(all, t));  // synchronizes
   if (blockIdx.x == 0 && t == 0) rows_of(a)[m] = r;
   if (r.bad || r.greedy) return;  // all of the row's workgroups
   if (r.l.k > 0) {
     uint32_t* count = reinterpret_cast<uint32_t*>(bins);
-    part.logits([&](float z, int) {
-      if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
-    });
+    count_tokens(part, r, count);
     __syncthreads();
     for (int b = t; b < kBins; b += kThreads)
       if (count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
@@ -315,9 +334,7 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
     for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
     __syncthreads();
   }
-  part.logits([&](float z, int) {
-    if (z >= r.floor) atomicAdd(&bins[bin_of(r, z)], weight_of(r, z, roots, a.bits));
-  });
+  sum_weights(part, r, bins, roots, a.bits);
   __syncthreads();
   for (int b = t; b < kBins; b += kThreads)
     if (bins[b]) atomicAdd(a.weight + m * kBins + b, bins[b]);
@@ -357,15 +374,14 @@ struct Bounds {
 // than k the last bin, and kFewer.
 constexpr uint32_t kFewer = 0xffffffffu;
 template <int T>
-__device__ __forceinline__ int kth_bin(const SampleArgs& a, int64_t m, int t, uint32_t k,
-                                       uint32_t& ahead) {
+__device__ __forceinline__ int kth_bin(const uint32_t* count, int t, uint32_t k, uint32_t& ahead) {
   constexpr int B = kBins / T;
   __shared__ int at;
   __shared__ uint32_t before;
   uint32_t c[B], sum = 0;
   u64 none = 0;
 #pragma unroll
-  for (int i = 0; i < B; ++i) sum += c[i] = a.count[m * kBins + B * t + i];
+  for (int i = 0; i < B; ++i) sum += c[i] = count[B * t + i];
   uint32_t past = sum;
   if (t == 0) at = kBins - 1, before = kFewer;
   scan<T>(past, none, t);  // synchronizes
@@ -387,16 +403,18 @@ struct Needed {
   uint32_t ahead;  // and the tokens ahead of that bin
 };
 
-// Reads the row's histogram into s and says which bins decide its token.
+// Sums the row's histogram of weights (and with a k reads that of tokens), and says which
+// bins decide its token.
 template <int T>
-__device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_t m, int t, Sums& s) {
+__device__ __forceinline__ Needed plan(const Row& r, const uint32_t* count, const u64* weight,
+                                       int bits, int t, Sums& s) {
   constexpr int B = kBins / T;
   __shared__ int at[4];
   const Limits& l = r.l;
   u64 w[B], ws = 0;
   uint32_t none = 0;
 #pragma unroll
-  for (int i = 0; i < B; ++i) ws += w[i] = a.weight[m * kBins + B * t + i];
+  for (int i = 0; i < B; ++i) ws += w[i] = weight[B * t + i];
   u64 wi = ws;
   scan<T>(none, wi, t);
   wi -= ws;
@@ -411,7 +429,7 @@ __device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_
 #pragma unroll
   for (int i = 0; i < 4; ++i) n.lo[i] = 1, n.hi[i] = 0;  // none
   n.kth = 0;
-  if (l.k > 0) n.kth = kth_bin<T>(a, m, t, (uint32_t)l.k, n.ahead);
+  if (l.k > 0) n.kth = kth_bin<T>(count, t, (uint32_t)l.k, n.ahead);
   __syncthreads();
 
   const u64 all = s.weight[kBins];
@@ -432,7 +450,7 @@ __device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_
     n.lo[1] = at[0], n.hi[1] = at[1];
     p = Bounds{s.weight[n.lo[1]], min(s.weight[n.hi[1] + 1], k.hi)};
   } else if (l.p <= 0.0) {
-    p.lo = p.hi = 1ull << a.bits;  // the first token alone
+    p.lo = p.hi = 1ull << bits;  // the first token alone
   }
   Bounds q = p;
   if (r.by_q()) {
@@ -451,6 +469,56 @@ __device__ __forceinline__ Needed plan(const SampleArgs& a, const Row& r, int64_
 }
 
 // ---- launch 3: the tokens of those bins
+// places from lo to below hi, some of them none
+struct Ranges {
+  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  bool one = false;  // from the first place on
+  __device__ __forceinline__ void down_to(int bin) {
+    one = true;
+    hi[0] = past(bin);
+  }
+  __device__ __forceinline__ void of(const Needed& n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n.lo[i] <= n.hi[i]) lo[i] = (float)n.lo[i], hi[i] = past(n.hi[i]);
+  }
+};
+
+// take(v, index of v[0], which of them) for a thread's pieces with tokens in the ranges
+template <class P, class Take>
+__device__ __forceinline__ void select(const P& part, const Row& r, const Ranges& g, Take take) {
+  constexpr int V = P::V;
+  const float far = fmaxf(fmaxf(g.hi[0], g.hi[1]), fmaxf(g.hi[2], g.hi[3]));
+  if (g.one && far < __builtin_inff()) {
+    part.pieces([&](const float(&v)[V], int n) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) mask |= place_of(r, v[e]) < far ? 1u << e : 0u;
+      if (mask) take(v, n, mask);
+    });
+    return;
+  }
+  // what lies below the floor has places from about kBins on
+  const float floor = far < __builtin_inff() ? -__builtin_inff() : r.floor;
+  part.pieces([&](const float(&v)[V], int n) {
+    float x[V];
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = place_of(r, v[e]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (g.lo[i] < g.hi[i]) {  // the same in all lanes
+#pragma unroll
+        for (int e = 0; e < V; ++e) mask |= x[e] >= g.lo[i] && x[e] < g.hi[i] ? 1u << e : 0u;
+      }
+    if (floor > -__builtin_inff()) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) mask &= v[e] >= floor ? ~0u : ~(1u << e);
+    }
+    if (mask) take(v, n, mask);
+  });
+}
+
 // The workgroup's are listed in LDS first, a place there for all of a thread's piece at a
 // time, and then behind the row's others: one atomic in memory for all of them (with one for
 // each token 128 rows took 38 us).  What does not fit there goes to the row's list at once.
@@ -466,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   u64* mine = lds.mine;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const Part<TYPE> part(a, m, blockIdx.x, t);
+  const Part<TYPE> part = part_of<TYPE>(a, m, t);
   const Row r = rows_of(a)[m];
   if (r.bad) return;
   if (t == 0) taken = 0;
@@ -477,9 +545,15 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
     if (first != 0xffffffffu) atomicMin(a.first + m, first);
     return;
   }
-  // takes those of a piece whose bits are set
-  auto take = [&](const float(&v)[V], int n, uint32_t mask) {
-    if (!mask) return;
+  Ranges ranges;
+  if (r.listed()) {
+    uint32_t ahead;
+    ranges.down_to(kth_bin<kThreads>(a.count + m * kBins, t, (uint32_t)r.l.k, ahead));
+  } else {
+    ranges.of(plan<kThreads>(r, a.count + m * kBins, a.weight + m * kBins, a.bits, t, lds.sums));
+  }
+  __syncthreads();  // the sums' place is the list's
+  select(part, r, ranges, [&](const float(&v)[V], int n, uint32_t mask) {
     uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
 #pragma unroll
     for (int e = 0; e < V; ++e)
@@ -492,48 +566,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
         }
         ++at;
       }
-  };
-  // the places of what is taken: ranges [lo, hi), some empty
-  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (r.listed()) {
-    uint32_t ahead;
-    hi[0] = past(kth_bin<kThreads>(a, m, t, (uint32_t)r.l.k, ahead));
-  } else {
-    const Needed need = plan<kThreads>(a, r, m, t, lds.sums);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (need.lo[i] <= need.hi[i]) lo[i] = (float)need.lo[i], hi[i] = past(need.hi[i]);
-  }
-  __syncthreads();
-  const float far = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-  if (r.listed() && far < __builtin_inff()) {
-    part.pieces([&](const float(&v)[V], int n) {
-      uint32_t mask = 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) mask |= place_of(r, v[e]) < far ? 1u << e : 0u;
-      take(v, n, mask);
-    });
-  } else {
-    // what lies below the floor has places from about kBins on
-    const float floor = far < __builtin_inff() ? -__builtin_inff() : r.floor;
-    part.pieces([&](const float(&v)[V], int n) {
-      float x[V];
-      uint32_t mask = 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[e] = place_of(r, v[e]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lo[i] < hi[i]) {  // the same in all lanes
-#pragma unroll
-          for (int e = 0; e < V; ++e) mask |= x[e] >= lo[i] && x[e] < hi[i] ? 1u << e : 0u;
-        }
-      if (floor > -__builtin_inff()) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) mask &= v[e] >= floor ? ~0u : ~(1u << e);
-      }
-      take(v, n, mask);
-    });
-  }
+  });
   __syncthreads();
   const uint32_t count = min(taken, (uint32_t)kMine);
   if (t == 0) base = count ? atomicAdd(a.listed + m, count) : 0;
@@ -766,31 +799,19 @@ __device__ __forceinline__ Drawn resolve(const SampleArgs& a, const Row& r, cons
   return Drawn{d.list[d.which], whole};
 }
 
+// The token of a row that is neither greedy nor bad, from its list of `count` tokens in
+// d.list (more than kList: not all are there); the roots are set.
 template <int TYPE>
-__global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
-  __shared__ Draw d;
-  const int t = threadIdx.x;
-  const int64_t m = blockIdx.y;
-  const Row r = rows_of(a)[m];
+__device__ __forceinline__ void draw(const SampleArgs& a, const Row& r, const Needed& need,
+                                     int64_t m, int t, Draw& d, int count) {
   const Limits& l = r.l;
-  if (r.bad || r.greedy) {
-    if (t == 0) {
-      a.token[m] = r.bad ? -1 : (int64_t)a.first[m];
-      if (a.logprob) a.logprob[m] = r.bad ? __builtin_nanf("") : 0.0f;
-    }
-    return;
-  }
   auto finish = [&](int64_t token, float z, u64 whole) {
     a.token[m] = token;
     if (a.logprob)
       a.logprob[m] = (float)(0.6931471805599453 *
                              (log2_weight(r, z) - (log2((double)whole) - (double)a.bits)));
   };
-  const int count = (int)min(a.listed[m], (uint32_t)kList + 1);
-  set_roots(d.roots, t);
-
   if (count > kList) {  // all of the workgroup
-    __syncthreads();    // the roots are there
     // how many tokens there are, and the sums of all and of those from min_p on
     if (t == 0) d.found = 0, d.below = 0, d.tokens = 0;
     __syncthreads();
@@ -828,12 +849,11 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
     return;
   }
 
-  // the list sorted, in descending order, zeros (no token's entry) behind it
+
+  // sorted in descending order, zeros (no token's entry) behind them
   int size = 64;
   while (size < count) size *= 2;
-  for (int i = t; i < size; i += kDraw) d.list[i] = i < count ? a.list[m * kList + i] : 0;
-  Needed need;
-  if (!r.listed()) need = plan<kDraw>(a, r, m, t, d.s);
+  for (int i = count + t; i < size; i += kDraw) d.list[i] = 0;
   __syncthreads();
   sort(d.list, size, t);
   const Drawn it = count <= kDraw ? resolve<1>(a, r, need, d, count, t)
@@ -841,7 +861,96 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   if (t == 0) finish((uint32_t)~(uint32_t)it.entry, value_of((uint32_t)(it.entry >> 32)), it.whole);
 }
 
-constexpr int64_t kRows = 1024;  // of a set of launches: bounds the workspace
+// a greedy row's token, or none
+__device__ __forceinline__ void draw_first(const SampleArgs& a, const Row& r, int64_t m,
+                                           uint32_t first) {
+  a.token[m] = r.bad ? -1 : (int64_t)first;
+  if (a.logprob) a.logprob[m] = r.bad ? __builtin_nanf("") : 0.0f;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
+  __shared__ Draw d;
+  const int t = threadIdx.x;
+  const int64_t m = blockIdx.y;
+  const Row r = rows_of(a)[m];
+  if (r.bad || r.greedy) {
+    if (t == 0) draw_first(a, r, m, a.first[m]);
+    return;
+  }
+  const int count = (int)min(a.listed[m], (uint32_t)kList + 1);
+  set_roots(d.roots, t);
+  for (int i = t; i < count && count <= kList; i += kDraw) d.list[i] = a.list[m * kList + i];
+  Needed need;
+  if (!r.listed())
+    need = plan<kDraw>(r, a.count + m * kBins, a.weight + m * kBins, a.bits, t, d.s);
+  __syncthreads();
+  draw<TYPE>(a, r, need, m, t, d, count);
+}
+
+// ---- all of it in one launch, for rows that a workgroup holds in registers
+constexpr int kWhole = 16;  // 16-byte pieces a thread
+template <int TYPE>
+__global__ __launch_bounds__(kDraw) void whole_kernel(SampleArgs a) {
+  constexpr int V = kValues<TYPE>;
+  __shared__ Draw d;
+  __shared__ uint32_t taken, first;
+  const int t = threadIdx.x;
+  const int64_t m = blockIdx.y;
+  const Part<TYPE, kDraw, kWhole> part(a, m, 0, a.N, t);
+  // the histograms, in places that are used after them
+  uint32_t* count = d.start;
+  u64* weight = d.ahead;
+  static_assert(kBins <= kList, "a bin a place");
+  for (int b = t; b < kBins; b += kDraw) count[b] = 0, weight[b] = 0;
+  if (t == 0) taken = 0, first = 0xffffffffu;
+  set_roots(d.roots, t);
+  const Row r = row_of(a, m, join_all<kDraw>(survey(part), t));  // synchronizes
+  if (r.bad || r.greedy) {
+    uint32_t mine = 0xffffffffu;
+    part.logits([&](float z, int n) { mine = z == r.top ? min(mine, (uint32_t)n) : mine; });
+    if (mine != 0xffffffffu) atomicMin(&first, mine);
+    __syncthreads();
+    if (t == 0) draw_first(a, r, m, first);
+    return;
+  }
+  Needed need;
+  Ranges ranges;
+  if (r.l.k > 0) count_tokens(part, r, count);
+  if (!r.listed()) sum_weights(part, r, weight, d.roots, a.bits);
+  __syncthreads();
+  if (r.listed()) {
+    uint32_t ahead;
+    ranges.down_to(kth_bin<kDraw>(count, t, (uint32_t)r.l.k, ahead));
+  } else {
+    need = plan<kDraw>(r, count, weight, a.bits, t, d.s);
+    ranges.of(need);
+  }
+  select(part, r, ranges, [&](const float(&v)[V], int n, uint32_t mask) {
+    uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (mask >> e & 1) {
+        if (at < kList) d.list[at] = entry_of(v[e], n + e);
+        ++at;
+      }
+  });
+  __syncthreads();
+  draw<TYPE>(a, r, need, m, t, d, (int)min(taken, (uint32_t)kList + 1));
+}
+
+// Whether a row goes through one launch: as long as it fits, and where there are few rows
+// while one workgroup is not slower than the parts of a row (us, one launch / four, with a
+// top-p alone and replayed from a graph: one row of 16000 in f32 17 / 21, of 32000 26 / 21; 16
+// rows of 32000 26 / 26, of 40000 in bf16 33 / 27; 128 rows of 32000 28 / 44, of 65536 in bf16
+// 51 / 52; 512 of those 102 / 119)
+bool is_whole(int type, int64_t M, int64_t N) {
+  const int64_t fits = (type == GEMMQ_F32 ? 4 : 8) * kWhole * kDraw;
+  return N <= fits && (N <= 16384 || (M >= 16 && N <= 32768) || M >= 128);
+}
+
+// rows of a set of launches: bounds the workspace, and the grid
+constexpr int64_t kRows = 1024, kWholeRows = 32768;
 
 struct Layout {
   int64_t rows, chunks, chunk;
@@ -876,8 +985,12 @@ Layout layout(int type, int64_t M, int64_t N) {
 }
 
 template <int TYPE>
-void launch_type(const SampleArgs& a, int rows, hipStream_t st) {
+void launch_type(const SampleArgs& a, int rows, bool whole, hipStream_t st) {
   const dim3 grid((uint32_t)a.chunks, (uint32_t)rows), one(1, (uint32_t)rows);
+  if (whole) {
+    whole_kernel<TYPE><<<one, kDraw, 0, st>>>(a);
+    return;
+  }
   top_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
   histogram_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
   gather_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
@@ -887,37 +1000,43 @@ void launch_type(const SampleArgs& a, int rows, hipStream_t st) {
 }  // namespace
 
 size_t sample_workspace(int64_t M, int64_t N) {
-  return layout(GEMMQ_F32, M, N).bytes;  // whose parts are the smaller ones
+  // f32's parts are the smaller ones, and where its rows go through one launch all do
+  return is_whole(GEMMQ_F32, M, N) ? 256 : layout(GEMMQ_F32, M, N).bytes;
 }
 
 int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st) {
-  const Layout l = layout(type, M, a.N);
-  uint8_t* p = static_cast<uint8_t*>(ws);
-  a.weight = reinterpret_cast<u64*>(p + l.weight);
-  a.list = reinterpret_cast<u64*>(p + l.list);
-  a.rows = p + l.rows_at;
-  a.part = reinterpret_cast<SamplePart*>(p + l.part);
-  a.count = reinterpret_cast<uint32_t*>(p + l.count);
-  a.listed = reinterpret_cast<uint32_t*>(p + l.listed);
-  a.first = reinterpret_cast<uint32_t*>(p + l.first);
-  a.chunk = (int)l.chunk;
-  a.chunks = (int)l.chunks;
   int log = 0;
   while (((int64_t)1 << log) < a.N) ++log;
   a.bits = 62 - log < 50 ? 62 - log : 50;
-  for (int64_t m = 0; m < M; m += l.rows) {
-    const int rows = (int)(M - m < l.rows ? M - m : l.rows);
-    type == GEMMQ_F32    ? launch_type<GEMMQ_F32>(a, rows, st)
-    : type == GEMMQ_BF16 ? launch_type<GEMMQ_BF16>(a, rows, st)
-                         : launch_type<GEMMQ_F16>(a, rows, st);
-    a.Z = static_cast<const uint8_t*>(a.Z) + l.rows * a.ldz * type_bytes(type);
-    if (a.temperature) a.temperature += l.rows;
-    if (a.top_k) a.top_k += l.rows;
-    if (a.top_p) a.top_p += l.rows;
-    if (a.min_p) a.min_p += l.rows;
-    a.u += l.rows;
-    a.token += l.rows;
-    if (a.logprob) a.logprob += l.rows;
+  const bool whole = is_whole(type, M, a.N);
+  int64_t each = M < kWholeRows ? M : kWholeRows;
+  if (!whole) {
+    const Layout l = layout(type, M, a.N);
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    a.weight = reinterpret_cast<u64*>(p + l.weight);
+    a.list = reinterpret_cast<u64*>(p + l.list);
+    a.rows = p + l.rows_at;
+    a.part = reinterpret_cast<SamplePart*>(p + l.part);
+    a.count = reinterpret_cast<uint32_t*>(p + l.count);
+    a.listed = reinterpret_cast<uint32_t*>(p + l.listed);
+    a.first = reinterpret_cast<uint32_t*>(p + l.first);
+    a.chunk = (int)l.chunk;
+    a.chunks = (int)l.chunks;
+    each = l.rows;
+  }
+  for (int64_t m = 0; m < M; m += each) {
+    const int rows = (int)(M - m < each ? M - m : each);
+    type == GEMMQ_F32    ? launch_type<GEMMQ_F32>(a, rows, whole, st)
+    : type == GEMMQ_BF16 ? launch_type<GEMMQ_BF16>(a, rows, whole, st)
+                         : launch_type<GEMMQ_F16>(a, rows, whole, st);
+    a.Z = static_cast<const uint8_t*>(a.Z) + each * a.ldz * type_bytes(type);
+    if (a.temperature) a.temperature += each;
+    if (a.top_k) a.top_k += each;
+    if (a.top_p) a.top_p += each;
+    if (a.min_p) a.min_p += each;
+    a.u += each;
+    a.token += each;
+    if (a.logprob) a.logprob += each;
   }
   return 0;
 }

@@ -87,7 +87,8 @@ def logits(kind, M, N, g):
 
 
 # one part and several, both sides of the list, odd sizes
-WIDTHS = [1, 2, 3, 17, 255, 256, 257, 1000, 1025, 4095, 4096, 4097, 8193, 32003, 151936]
+WIDTHS = [1, 2, 3, 17, 255, 256, 257, 1000, 1025, 4095, 4096, 4097, 8193, 16384, 16385, 32003,
+          32768, 32769, 151936]
 
 
 @pytest.mark.parametrize("kind", ["peaked", "flat", "ties", "masked", "far"])
@@ -110,7 +111,20 @@ def test_sample(N, kind, dtype):
     check(z[:1], u[:1], k=k[:1], p=p[:1], q=q[:1])
 
 
-@pytest.mark.parametrize("N", [7, 5000, 40000])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("N", [16385, 32768, 32770, 50001, 65536, 65537])
+def test_many_rows(N, dtype):
+    # rows of one launch and of four by their number
+    g = gen(N)
+    for M in (1, 15, 16, 127, 130):
+        z = logits("peaked", M, N, g).to(dtype)
+        u = torch.rand(M, generator=g, device="cuda")
+        t, k, p, q = settings(M, g)
+        check(z, u, t, k, p, q)
+        check(z, u, p=p)
+
+
+@pytest.mark.parametrize("N", [7, 5000, 20000, 40000])
 def test_equal_logits(N):
     # the order is the index's: every place can be computed
     M = 64
@@ -149,7 +163,7 @@ def test_many_ties_at_every_place(N, dtype):
     check(z, u, t=t, k=k, p=p, q=q)
 
 
-@pytest.mark.parametrize("N", [4500, 9000, 30000])
+@pytest.mark.parametrize("N", [4500, 9000, 30000, 50000])
 def test_large_k(N):
     # k beyond what is listed down to the k-th, around the number of tokens with a weight, and
     # more of those than are sorted
@@ -223,10 +237,10 @@ def test_rows_that_cannot_be_drawn_from():
         assert token[[1, 2, 3, 6, 7]].tolist() == [-1] * 5
 
 
-@pytest.mark.parametrize("M", [1023, 1024, 1025, 2500])
-def test_more_rows_than_a_set_of_launches(M):
+@pytest.mark.parametrize("M,N", [(1023, 700), (1024, 40000), (1025, 40000), (2500, 34000), (32769, 40)])
+def test_more_rows_than_a_set_of_launches(M, N):
     g = gen(M)
-    z = logits("peaked", M, 700, g)
+    z = logits("peaked", M, N, g)
     u = torch.rand(M, generator=g, device="cuda")
     token = torch.full((M + 2,), 77, device="cuda")
     logp = torch.full((M + 2,), 77.0, device="cuda")
@@ -262,7 +276,7 @@ def test_rows_past_32_bits():
 def test_without_logprob_and_a_used_workspace():
     # whatever the workspace holds, the results are the same
     g = gen(8)
-    M, N = 5, 9000
+    M, N = 5, 40000
     z, u = logits("ties", M, N, g), torch.rand(M, generator=g, device="cuda")
     ref = check(z, u)[0]
     L = gq.lib_i8()
