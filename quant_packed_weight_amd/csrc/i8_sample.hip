@@ -53,11 +53,11 @@ __device__ __forceinline__ u64 entry_of(float z, uint32_t index) {
   return (u64)key_of(z) << 32 | (uint32_t)~index;
 }
 
-// A workgroup's part of a row in registers: kPieces 16-byte pieces a thread at most.  Launches
-// 1 to 3 load it whole before they look at anything else, so that what they work out of the
-// row first overlaps the loads.
-constexpr int kPieces = 8;
-template <int TYPE, int T = kThreads, int P = kPieces>
+// A workgroup's part of a row in registers: up to 16384 logits, P 16-byte pieces a thread.
+// Launches 1 to 3 load it whole before they look at anything else, so that what they work out
+// of the row first overlaps the loads.
+constexpr int kMostOfARow = 16384;
+template <int TYPE, int T = kThreads, int P = kMostOfARow / (kThreads * kValues<TYPE>)>
 struct Part {
   static constexpr int V = kValues<TYPE>, kSpan = V * T;
   uint4 raw[P];
@@ -163,7 +163,18 @@ struct Row {
   __device__ bool by_q() const { return least > floor; }
 };
 
-__device__ __forceinline__ Row* rows_of(const SampleArgs& a) { return static_cast<Row*>(a.rows); }
+// places from lo to below hi, some of them none
+struct Ranges {
+  float lo[4], hi[4];
+  bool one;  // from the first place on
+};
+struct RowAndRanges {
+  Row row;
+  Ranges ranges;
+};
+__device__ __forceinline__ RowAndRanges* rows_of(const SampleArgs& a) {
+  return static_cast<RowAndRanges*>(a.rows);
+}
 
 // log2 of a token's weight relative to the largest
 __device__ __forceinline__ double log2_weight(const Row& r, float z) {
@@ -307,39 +318,6 @@ __device__ __forceinline__ void sum_weights(const P& part, const Row& r, u64* we
   });
 }
 
-// ---- launch 2: the histograms: of tokens where a k decides, of weights where it is not
-// small (both, one after the other, for the few rows of a large k)
-template <int TYPE>
-__global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
-  __shared__ u64 bins[kBins];
-  __shared__ double roots[kRoots];
-  const int t = threadIdx.x;
-  const int64_t m = blockIdx.y;
-  const Part<TYPE> part = part_of<TYPE>(a, m, t);
-  for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
-  set_roots(roots, t);
-  SamplePart all{-__builtin_inff(), __builtin_inff(), 0};
-  for (int c = t; c < a.chunks; c += kThreads) join(all, a.part[m * a.chunks + c]);
-  const Row r = row_of(a, m, join_all<kThreads>(all, t));  // synchronizes
-  if (blockIdx.x == 0 && t == 0) rows_of(a)[m] = r;
-  if (r.bad || r.greedy) return;  // all of the row's workgroups
-  if (r.l.k > 0) {
-    uint32_t* count = reinterpret_cast<uint32_t*>(bins);
-    count_tokens(part, r, count);
-    __syncthreads();
-    for (int b = t; b < kBins; b += kThreads)
-      if (count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
-    if (r.listed()) return;
-    __syncthreads();
-    for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
-    __syncthreads();
-  }
-  sum_weights(part, r, bins, roots, a.bits);
-  __syncthreads();
-  for (int b = t; b < kBins; b += kThreads)
-    if (bins[b]) atomicAdd(a.weight + m * kBins + b, bins[b]);
-}
-
 // ---- what the histograms say
 
 // inclusive sums over the workgroup's threads, in their order
@@ -468,22 +446,78 @@ __device__ __forceinline__ Needed plan(const Row& r, const uint32_t* count, cons
   return n;
 }
 
-// ---- launch 3: the tokens of those bins
-// places from lo to below hi, some of them none
-struct Ranges {
-  float lo[4] = {0.0f, 1.0f, 1.0f, 1.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  bool one = false;  // from the first place on
-  __device__ __forceinline__ void down_to(int bin) {
-    one = true;
-    hi[0] = past(bin);
-  }
-  __device__ __forceinline__ void of(const Needed& n) {
+__device__ __forceinline__ Ranges ranges_down_to(int bin) {
+  return Ranges{{0.0f, 1.0f, 1.0f, 1.0f}, {past(bin), 0.0f, 0.0f, 0.0f}, true};
+}
+__device__ __forceinline__ Ranges ranges_of(const Needed& n) {
+  Ranges g;
+  g.one = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n.lo[i] <= n.hi[i]) lo[i] = (float)n.lo[i], hi[i] = past(n.hi[i]);
+  for (int i = 0; i < 4; ++i) {
+    const bool some = n.lo[i] <= n.hi[i];
+    g.lo[i] = some ? (float)n.lo[i] : 1.0f;
+    g.hi[i] = some ? past(n.hi[i]) : 0.0f;
   }
-};
+  return g;
+}
 
+// ---- launch 2: the histograms: of tokens where a k decides, of weights where it is not
+// small (both, one after the other, for the few rows of a large k)
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
+  __shared__ u64 bins[kBins];
+  __shared__ double roots[kRoots];
+  const int t = threadIdx.x;
+  const int64_t m = blockIdx.y;
+  const Part<TYPE> part = part_of<TYPE>(a, m, t);
+  for (int b = t; b < kBins; b += kThreads) bins[b] = 0;
+  set_roots(roots, t);
+  SamplePart all{-__builtin_inff(), __builtin_inff(), 0};
+  for (int c = t; c < a.chunks; c += kThreads) join(all, a.part[m * a.chunks + c]);
+  const Row r = row_of(a, m, join_all<kThreads>(all, t));  // synchronizes
+  if (blockIdx.x == 0 && t == 0) rows_of(a)[m].row = r;
+  if (r.bad || r.greedy) return;  // all of the row's workgroups
+  if (r.l.k > 0) {
+    uint32_t* count = reinterpret_cast<uint32_t*>(bins);
+    count_tokens(part, r, count);
+    __syncthreads();
+    for (int b = t; b < kBins; b += kThreads)
+      if (count[b]) atomicAdd(a.count + m * kBins + b, count[b]);
+    if (r.listed()) return;
+    __syncthreads();
+    for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
+    __syncthreads();
+  }
+  sum_weights(part, r, bins, roots, a.bits);
+  __syncthreads();
+  for (int b = t; b < kBins; b += kThreads)
+    if (bins[b]) atomicAdd(a.weight + m * kBins + b, bins[b]);
+}
+
+// What is gathered of a row that is neither greedy nor bad
+template <int T>
+__device__ __forceinline__ Ranges ranges_of(const SampleArgs& a, const Row& r, int64_t m, int t,
+                                            Sums& s) {
+  const uint32_t* count = a.count + m * kBins;
+  if (!r.listed()) return ranges_of(plan<T>(r, count, a.weight + m * kBins, a.bits, t, s));
+  uint32_t ahead;
+  return ranges_down_to(kth_bin<T>(count, t, (uint32_t)r.l.k, ahead));
+}
+
+// That in a launch of its own, for many rows (kPlanned): each workgroup of the gathering would
+// read the row's histogram again (rows of 151936 in f32 with a top-p, us, worked out there / by
+// a launch: one row 24.0 / 24.5, 16 rows 65 / 60, 32 rows 60 / 54, 128 rows 116 / 101).
+__global__ __launch_bounds__(kDraw) void plan_kernel(SampleArgs a) {
+  __shared__ Sums s;
+  const int t = threadIdx.x;
+  const int64_t m = blockIdx.y;
+  const Row r = rows_of(a)[m].row;
+  if (r.bad || r.greedy) return;
+  const Ranges g = ranges_of<kDraw>(a, r, m, t, s);
+  if (t == 0) rows_of(a)[m].ranges = g;
+}
+
+// ---- launch 3: the tokens of those bins
 // take(v, index of v[0], which of them) for a thread's pieces with tokens in the ranges
 template <class P, class Take>
 __device__ __forceinline__ void select(const P& part, const Row& r, const Ranges& g, Take take) {
@@ -523,11 +557,11 @@ __device__ __forceinline__ void select(const P& part, const Row& r, const Ranges
 // time, and then behind the row's others: one atomic in memory for all of them (with one for
 // each token 128 rows took 38 us).  What does not fit there goes to the row's list at once.
 constexpr int kMine = kList / 2;
-template <int TYPE>
+template <int TYPE, bool PLANNED>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   constexpr int V = kValues<TYPE>;
   __shared__ union {
-    Sums sums;  // until the places are known
+    Sums sums;  // not PLANNED: until the places are known
     u64 mine[kMine];
   } lds;
   __shared__ uint32_t taken, base;
@@ -535,7 +569,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const Part<TYPE> part = part_of<TYPE>(a, m, t);
-  const Row r = rows_of(a)[m];
+  const Row r = rows_of(a)[m].row;
   if (r.bad) return;
   if (t == 0) taken = 0;
   __syncthreads();
@@ -546,13 +580,12 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a) {
     return;
   }
   Ranges ranges;
-  if (r.listed()) {
-    uint32_t ahead;
-    ranges.down_to(kth_bin<kThreads>(a.count + m * kBins, t, (uint32_t)r.l.k, ahead));
+  if constexpr (PLANNED) {
+    ranges = rows_of(a)[m].ranges;
   } else {
-    ranges.of(plan<kThreads>(r, a.count + m * kBins, a.weight + m * kBins, a.bits, t, lds.sums));
+    ranges = ranges_of<kThreads>(a, r, m, t, lds.sums);
+    __syncthreads();  // the sums' place is the list's
   }
-  __syncthreads();  // the sums' place is the list's
   select(part, r, ranges, [&](const float(&v)[V], int n, uint32_t mask) {
     uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
 #pragma unroll
@@ -873,7 +906,7 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   __shared__ Draw d;
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
-  const Row r = rows_of(a)[m];
+  const Row r = rows_of(a)[m].row;
   if (r.bad || r.greedy) {
     if (t == 0) draw_first(a, r, m, a.first[m]);
     return;
@@ -921,10 +954,10 @@ __global__ __launch_bounds__(kDraw) void whole_kernel(SampleArgs a) {
   __syncthreads();
   if (r.listed()) {
     uint32_t ahead;
-    ranges.down_to(kth_bin<kDraw>(count, t, (uint32_t)r.l.k, ahead));
+    ranges = ranges_down_to(kth_bin<kDraw>(count, t, (uint32_t)r.l.k, ahead));
   } else {
     need = plan<kDraw>(r, count, weight, a.bits, t, d.s);
-    ranges.of(need);
+    ranges = ranges_of(need);
   }
   select(part, r, ranges, [&](const float(&v)[V], int n, uint32_t mask) {
     uint32_t at = atomicAdd(&taken, (uint32_t)__popc(mask));
@@ -951,19 +984,20 @@ bool is_whole(int type, int64_t M, int64_t N) {
 
 // rows of a set of launches: bounds the workspace, and the grid
 constexpr int64_t kRows = 1024, kWholeRows = 32768;
+constexpr int64_t kPlanned = 32;  // rows from which the plan has its own launch
 
 struct Layout {
   int64_t rows, chunks, chunk;
   size_t weight, list, rows_at, part, count, listed, first, bytes;
 };
 
-// Parts of a row: the largest that leave a launch 1024 workgroups, of eight pieces a thread to
-// two
+// Parts of a row: the largest that leave a launch 1024 workgroups, of two pieces a thread at
+// least
 Layout layout(int type, int64_t M, int64_t N) {
   Layout l;
   l.rows = M < kRows ? M : kRows;
   const int64_t span = (type == GEMMQ_F32 ? 4 : 8) * kThreads;
-  int64_t pieces = kPieces;
+  int64_t pieces = kMostOfARow / span;
   while (pieces > 2 && l.rows * ceil_div(N, pieces * span) < 1024) pieces /= 2;
   l.chunk = pieces * span;
   l.chunks = ceil_div(N, l.chunk);
@@ -975,7 +1009,7 @@ Layout layout(int type, int64_t M, int64_t N) {
   };
   l.weight = take(8 * l.rows * kBins);
   l.list = take(8 * l.rows * kList);
-  l.rows_at = take((int64_t)sizeof(Row) * l.rows);
+  l.rows_at = take((int64_t)sizeof(RowAndRanges) * l.rows);
   l.part = take((int64_t)sizeof(SamplePart) * l.rows * l.chunks);
   l.count = take(4 * l.rows * kBins);
   l.listed = take(4 * l.rows);
@@ -993,7 +1027,12 @@ void launch_type(const SampleArgs& a, int rows, bool whole, hipStream_t st) {
   }
   top_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
   histogram_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
-  gather_kernel<TYPE><<<grid, kThreads, 0, st>>>(a);
+  if (rows >= kPlanned) {
+    plan_kernel<<<one, kDraw, 0, st>>>(a);
+    gather_kernel<TYPE, true><<<grid, kThreads, 0, st>>>(a);
+  } else {
+    gather_kernel<TYPE, false><<<grid, kThreads, 0, st>>>(a);
+  }
   draw_kernel<TYPE><<<one, kDraw, 0, st>>>(a);
 }
 
