@@ -93,6 +93,7 @@ struct SampleArgs {
   // workspace
   int chunk, chunks, bits;
   SamplePart* part;
+  double* sum;
   void* rows;
   uint32_t *count, *listed, *first;
   unsigned long long *weight, *list;

@@ -353,6 +353,25 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return max(b[0], b[1]);
 }
 
+// the sum over the workgroup of T threads of v[0..N), in every thread and in a fixed
+// order; `at`: N * T / 64 doubles of LDS that nothing else uses
+template <int T, int N>
+__device__ __forceinline__ void sum_all(double (&v)[N], double* at, int t) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if ((t & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[N * (t >> 6) + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = at[i];
+#pragma unroll
+  for (int w = 1; w < T / 64; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += at[N * w + i];
+}
+
 // Workgroup index -> position in the work list such that each of the eight XCDs
 // (consecutive workgroups go to consecutive XCDs) takes one contiguous stretch
 // of it, and neighbours in the list share an L2.

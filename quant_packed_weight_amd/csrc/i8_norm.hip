@@ -25,25 +25,6 @@ __device__ __forceinline__ void load_vector(const float* w, int k, int end, bool
   }
 }
 
-// the sum over the workgroup of T threads of v[0..N), in every thread and in a fixed
-// order; `at`: N * T / 64 doubles of LDS that nothing else uses
-template <int T, int N>
-__device__ __forceinline__ void sum_all(double (&v)[N], double* at, int t) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if ((t & 63) == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) at[N * (t >> 6) + i] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = at[i];
-#pragma unroll
-  for (int w = 1; w < T / 64; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += at[N * w + i];
-}
-
 // The norm, workgroup g of G the rows g, g + G, ...: a row is read once (HELD 16-byte pieces
 // a thread), the next one's loads under way while it is worked on, and the weights stay in
 // registers.  HELD == 0: rows of any width, read twice.

@@ -161,6 +161,11 @@ struct Row {
   __device__ bool listed() const { return l.k > 0 && l.k <= kListedK; }
   __device__ bool by_p() const { return l.p > 0.0 && l.p < 1.0; }
   __device__ bool by_q() const { return least > floor; }
+  // Rows of which all tokens (from min_p on) are kept: one is nearly certain where the others'
+  // sum is next to nothing, which the logarithm of its share is then as exact as, so that
+  // sum is taken in f64 too (a unit for each of 150000 tokens is 4 10^-9).  Limits that keep
+  // more than the first token leave a sum that integers hold, or a list to add up.
+  __device__ bool exact() const { return l.k == 0 && l.p >= 1.0; }
 };
 
 // places from lo to below hi, some of them none
@@ -261,11 +266,11 @@ constexpr int kRoots = 32;
 __device__ __forceinline__ void set_roots(double* roots, int t) {
   if (t < kRoots) roots[t] = exp2((double)t / kRoots);
 }
-// 2^(x / 32) for x in [-32 (bits + 2), 0] in units of 2^-bits, rounded: x = n + f with f in
-// [-1/2, 1/2], 2^(n / 32) from the roots, and 2^(f / 32) by its series, with c = ln 2 / 32 to
+// 2^(x / 32) for x in [-32000, 0] in units of 2^-bits: x = n + f with f in [-1/2, 1/2],
+// 2^(n / 32) from the roots, and 2^(f / 32) by its series, with c = ln 2 / 32 to
 // (c / 2)^6 / 6! < 10^-14.  (The series of 2^f alone, to f^11, cost twice as much.)  Sums
 // with powers of two stand for conversions, which take four times an addition's time.
-__device__ __forceinline__ u64 weight_of(double x, const double* roots, int bits) {
+__device__ __forceinline__ double weight_of(double x, const double* roots, int bits) {
   constexpr double kWhole = 6755399441055744.0;  // 1.5 2^52: n in the sum's low bits
   const double shifted = x + kWhole, f = x - (shifted - kWhole);
   const int i = (int)__builtin_bit_cast(u64, shifted);
@@ -278,13 +283,19 @@ __device__ __forceinline__ u64 weight_of(double x, const double* roots, int bits
   const u64 power = (u64)(uint32_t)((i >> 5) + bits) << 52;  // added to the exponent
   const double root =
       __builtin_bit_cast(double, __builtin_bit_cast(u64, roots[i & (kRoots - 1)]) + power);
-  // at most 2^50: the sum with 2^52 holds the integer in its low bits
-  const double s = fma(p * f, root, root) + 4503599627370496.0;
-  return __builtin_bit_cast(u64, s) & 0xfffffffffffffull;
+  return fma(p * f, root, root);
 }
-
+// as an integer, for a weight of at most 2^50: the low bits of its sum with 2^52
+__device__ __forceinline__ u64 rounded(double weight) {
+  return __builtin_bit_cast(u64, weight + 4503599627370496.0) & 0xfffffffffffffull;
+}
+// that of a token from the floor on
 __device__ __forceinline__ u64 weight_of(const Row& r, float z, const double* roots, int bits) {
-  return weight_of(((double)z - (double)r.top) * (r.rate * kRoots), roots, bits);
+  return rounded(weight_of(((double)z - (double)r.top) * (r.rate * kRoots), roots, bits));
+}
+// that of any token, not rounded, nothing that counts where z is -inf
+__device__ __forceinline__ double exact_weight(const Row& r, float z, const double* roots, int bits) {
+  return weight_of(fmax(((double)z - (double)r.top) * (r.rate * kRoots), -32000.0), roots, bits);
 }
 
 // ---- launch 1: the largest logit of a part of a row, the lowest finite one, and whether
@@ -310,12 +321,24 @@ __device__ __forceinline__ void count_tokens(const P& part, const Row& r, uint32
     if (z >= r.floor) atomicAdd(&count[bin_of(r, z)], 1u);
   });
 }
+// and the thread's exact sum of a row's weights where the logarithm of a share needs it
 template <class P>
-__device__ __forceinline__ void sum_weights(const P& part, const Row& r, u64* weight,
-                                            const double* roots, int bits) {
-  part.logits([&](float z, int) {
-    if (z >= r.floor) atomicAdd(&weight[bin_of(r, z)], weight_of(r, z, roots, bits));
-  });
+__device__ __forceinline__ double sum_weights(const P& part, const Row& r, u64* weight,
+                                              const double* roots, int bits) {
+  double sum = 0.0;
+  if (r.exact()) {
+    const float from = r.l.y < -100.0 ? -__builtin_inff() : r.least;
+    part.logits([&](float z, int) {
+      const double w = exact_weight(r, z, roots, bits);
+      sum += z >= from ? w : 0.0;
+      if (z >= r.floor) atomicAdd(&weight[bin_of(r, z)], rounded(w));
+    });
+  } else {
+    part.logits([&](float z, int) {
+      if (z >= r.floor) atomicAdd(&weight[bin_of(r, z)], weight_of(r, z, roots, bits));
+    });
+  }
+  return sum;
 }
 
 // ---- what the histograms say
@@ -466,7 +489,7 @@ __device__ __forceinline__ Ranges ranges_of(const Needed& n) {
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
   __shared__ u64 bins[kBins];
-  __shared__ double roots[kRoots];
+  __shared__ double roots[kRoots], sums[kThreads / 64];
   const int t = threadIdx.x;
   const int64_t m = blockIdx.y;
   const Part<TYPE> part = part_of<TYPE>(a, m, t);
@@ -488,7 +511,11 @@ __global__ __launch_bounds__(kThreads) void histogram_kernel(SampleArgs a) {
     for (int b = t; b < kBins / 2; b += kThreads) bins[b] = 0;
     __syncthreads();
   }
-  sum_weights(part, r, bins, roots, a.bits);
+  double sum[1] = {sum_weights(part, r, bins, roots, a.bits)};
+  if (r.exact()) {
+    sum_all<kThreads>(sum, sums, t);
+    if (t == 0) a.sum[m * a.chunks + blockIdx.x] = sum[0];
+  }
   __syncthreads();
   for (int b = t; b < kBins; b += kThreads)
     if (bins[b]) atomicAdd(a.weight + m * kBins + b, bins[b]);
@@ -700,7 +727,7 @@ struct Draw {
   Sums s;
   uint32_t start[kBins];  // a needed bin's first place in the list
   u64 list[kList], ahead[kList + 1];
-  double roots[kRoots];
+  double roots[kRoots], sums[kDraw / 64];
   u64 found, below;
   uint32_t tokens;
   int which;
@@ -741,8 +768,14 @@ __device__ __forceinline__ void sort(u64* list, int size, int t) {
   __syncthreads();
 }
 
+// What a sum of weights has beyond the first token's, in units of that
+__device__ __forceinline__ double beyond_first(u64 whole, int bits) {
+  return __builtin_ldexp((double)(whole - (1ull << bits)), -bits);
+}
+
 struct Drawn {
-  u64 entry, whole;  // the token's, and the sum of the weights it was drawn from
+  u64 entry;      // the token's
+  double others;  // beyond_first of what it was drawn from
 };
 
 // The token from the sorted list of `count` tokens, at most E of each thread.
@@ -829,20 +862,30 @@ __device__ __forceinline__ Drawn resolve(const SampleArgs& a, const Row& r, cons
     if (E * t + e < count && (double)from[e] <= to && (double)(from[e] + w[e]) > to)
       d.which = E * t + e;
   __syncthreads();
-  return Drawn{d.list[d.which], whole};
+  double others[1] = {0.0};
+  if (listed) {
+    // those of the list, exactly
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (E * t + e > 0 && E * t + e < count && from[e] + w[e] <= whole)
+        others[0] += exact_weight(r, z[e], d.roots, 0);
+    sum_all<kDraw>(others, d.sums, t);
+  } else {
+    others[0] = beyond_first(whole, a.bits);
+  }
+  return Drawn{d.list[d.which], others[0]};
 }
 
 // The token of a row that is neither greedy nor bad, from its list of `count` tokens in
-// d.list (more than kList: not all are there); the roots are set.
+// d.list (more than kList: not all are there); the roots are set.  `sum`: an exact() row's.
 template <int TYPE>
 __device__ __forceinline__ void draw(const SampleArgs& a, const Row& r, const Needed& need,
-                                     int64_t m, int t, Draw& d, int count) {
+                                     int64_t m, int t, Draw& d, int count, double sum) {
   const Limits& l = r.l;
-  auto finish = [&](int64_t token, float z, u64 whole) {
+  auto finish = [&](int64_t token, float z, double others) {
+    if (r.exact()) others = __builtin_ldexp(sum, -a.bits) - 1.0;
     a.token[m] = token;
-    if (a.logprob)
-      a.logprob[m] = (float)(0.6931471805599453 *
-                             (log2_weight(r, z) - (log2((double)whole) - (double)a.bits)));
+    if (a.logprob) a.logprob[m] = (float)(0.6931471805599453 * log2_weight(r, z) - log1p(others));
   };
   if (count > kList) {  // all of the workgroup
     // how many tokens there are, and the sums of all and of those from min_p on
@@ -878,7 +921,7 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Row& r, const Ne
     const Found f = search<TYPE>(a, r, d.roots, m, t, kPastSum, 0, to);
     const uint32_t place = place_among(f.sum, f.weight, f.ties, to, true);
     const int64_t token = index_of<TYPE>(a, m, t, f.key, place);
-    if (t == 0) finish(token, value_of(f.key), whole);
+    if (t == 0) finish(token, value_of(f.key), beyond_first(whole, a.bits));
     return;
   }
 
@@ -891,7 +934,7 @@ __device__ __forceinline__ void draw(const SampleArgs& a, const Row& r, const Ne
   sort(d.list, size, t);
   const Drawn it = count <= kDraw ? resolve<1>(a, r, need, d, count, t)
                                   : resolve<kList / kDraw>(a, r, need, d, count, t);
-  if (t == 0) finish((uint32_t)~(uint32_t)it.entry, value_of((uint32_t)(it.entry >> 32)), it.whole);
+  if (t == 0) finish((uint32_t)~(uint32_t)it.entry, value_of((uint32_t)(it.entry >> 32)), it.others);
 }
 
 // a greedy row's token, or none
@@ -917,8 +960,11 @@ __global__ __launch_bounds__(kDraw) void draw_kernel(SampleArgs a) {
   Needed need;
   if (!r.listed())
     need = plan<kDraw>(r, a.count + m * kBins, a.weight + m * kBins, a.bits, t, d.s);
-  __syncthreads();
-  draw<TYPE>(a, r, need, m, t, d, count);
+  double sum[1] = {0.0};
+  if (r.exact())
+    for (int c = t; c < a.chunks; c += kDraw) sum[0] += a.sum[m * a.chunks + c];
+  sum_all<kDraw>(sum, d.sums, t);  // synchronizes
+  draw<TYPE>(a, r, need, m, t, d, count, sum[0]);
 }
 
 // ---- all of it in one launch, for rows that a workgroup holds in registers
@@ -950,8 +996,9 @@ __global__ __launch_bounds__(kDraw) void whole_kernel(SampleArgs a) {
   Needed need;
   Ranges ranges;
   if (r.l.k > 0) count_tokens(part, r, count);
-  if (!r.listed()) sum_weights(part, r, weight, d.roots, a.bits);
-  __syncthreads();
+  double sum[1] = {0.0};
+  if (!r.listed()) sum[0] = sum_weights(part, r, weight, d.roots, a.bits);
+  sum_all<kDraw>(sum, d.sums, t);  // synchronizes
   if (r.listed()) {
     uint32_t ahead;
     ranges = ranges_down_to(kth_bin<kDraw>(count, t, (uint32_t)r.l.k, ahead));
@@ -969,7 +1016,7 @@ __global__ __launch_bounds__(kDraw) void whole_kernel(SampleArgs a) {
       }
   });
   __syncthreads();
-  draw<TYPE>(a, r, need, m, t, d, (int)min(taken, (uint32_t)kList + 1));
+  draw<TYPE>(a, r, need, m, t, d, (int)min(taken, (uint32_t)kList + 1), sum[0]);
 }
 
 // Whether a row goes through one launch: as long as it fits, and where there are few rows
@@ -988,7 +1035,7 @@ constexpr int64_t kPlanned = 32;  // rows from which the plan has its own launch
 
 struct Layout {
   int64_t rows, chunks, chunk;
-  size_t weight, list, rows_at, part, count, listed, first, bytes;
+  size_t weight, list, sum, rows_at, part, count, listed, first, bytes;
 };
 
 // Parts of a row: the largest that leave a launch 1024 workgroups, of two pieces a thread at
@@ -1009,6 +1056,7 @@ Layout layout(int type, int64_t M, int64_t N) {
   };
   l.weight = take(8 * l.rows * kBins);
   l.list = take(8 * l.rows * kList);
+  l.sum = take(8 * l.rows * l.chunks);
   l.rows_at = take((int64_t)sizeof(RowAndRanges) * l.rows);
   l.part = take((int64_t)sizeof(SamplePart) * l.rows * l.chunks);
   l.count = take(4 * l.rows * kBins);
@@ -1054,6 +1102,7 @@ int launch_sample(SampleArgs a, int type, int64_t M, void* ws, hipStream_t st) {
     uint8_t* p = static_cast<uint8_t*>(ws);
     a.weight = reinterpret_cast<u64*>(p + l.weight);
     a.list = reinterpret_cast<u64*>(p + l.list);
+    a.sum = reinterpret_cast<double*>(p + l.sum);
     a.rows = p + l.rows_at;
     a.part = reinterpret_cast<SamplePart*>(p + l.part);
     a.count = reinterpret_cast<uint32_t*>(p + l.count);

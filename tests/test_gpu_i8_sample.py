@@ -45,7 +45,10 @@ def reference(z, u, t=None, k=None, p=None, q=None):
     total = torch.cumsum(e, 1)
     at = (total <= u[:, None] * total[:, -1:]).sum(1, keepdim=True).clamp(max=N - 1)
     token = torch.where(bad, -1, order.gather(1, at)[:, 0])
-    logp = torch.where(bad, math.nan, torch.log(e.gather(1, at) / total[:, -1:])[:, 0])
+    # the first token's share by what the others have: log(1 / (1 + others))
+    others = e[:, 1:].sum(1)
+    drawn = (v.gather(1, at) - v[:, :1])[:, 0] / torch.where(t > 0, t, 1.0)
+    logp = torch.where(bad, math.nan, torch.where(greedy[:, 0], 0.0, drawn) - torch.log1p(others))
     return token, logp
 
 
@@ -198,6 +201,24 @@ def test_frequencies():
     ref = torch.softmax(z[0].double(), 0)
     assert bool(((share - ref).abs() <= 1.0 / n + 1e-6).all())
     assert bool(((logp.double() - torch.log(ref[token])).abs() <= 1e-5).all())
+
+
+@pytest.mark.parametrize("N", [300, 5000, 40000, 151936])
+def test_nearly_certain(N):
+    # the logarithm of a share near one is as exact as the others' sum: to a rounding, and
+    # to what a sum with 1 in 64 bits leaves; the settings keep all, or lists
+    g = gen(N)
+    gap = torch.linspace(0, 60, 41, device="cuda")
+    z = torch.randn((41, N), generator=g, device="cuda")
+    z[:, N // 3] = z.amax(1) + gap
+    u = torch.full((41,), 0.3, device="cuda")
+    k, q = torch.full((41,), 40, device="cuda").int(), torch.full((41,), 1e-9, device="cuda")
+    for kw in (dict(), dict(k=k), dict(q=q), dict(t=torch.full((41,), 0.7, device="cuda"))):
+        token, logp = check(z, u, **kw)
+        rt, rl = reference(z, u, **kw)
+        # (a list leaves out weights below 2^-(62 - 18))
+        slack = 2.0 ** -52 * 8 + (40 * 2.0 ** -44 if "k" in kw else 0)
+        assert bool(((logp.double() - rl).abs() <= U * (1 + 1e-6) * rl.abs() + slack).all()), kw.keys()
 
 
 def test_settings_at_their_ends():
