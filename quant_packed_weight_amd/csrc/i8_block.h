@@ -33,7 +33,7 @@ struct RmsGradArgs {
   float eps;
   bool wide_h, wide_dy, wide_dh, wide_dx, wide_w;
 };
-int rms_grad_groups(int64_t M);
+int rms_grad_groups(int64_t M, int64_t K);
 int launch_rms_grad(const RmsGradArgs& a, hipStream_t st);
 
 // out[k] = the sum of `count` rows of part, in a fixed order (count 0: zeros)

@@ -136,7 +136,7 @@ int gemmq_rms_i8(int type, const void* X, int64_t ldx, const void* R, int64_t ld
 
 size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K) {
   if (!known(type) || check_shape(M, 0, K) != GEMMQ_OK || M == 0) return 0;
-  return align_up(4 * rms_grad_groups(M) * (int64_t)align_up(K, 4), 256);
+  return align_up(4 * rms_grad_groups(M, K) * (int64_t)align_up(K, 4), 256);
 }
 
 int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, float eps,
@@ -176,7 +176,7 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
   clear_pending();
   rc = launched(launch_rms_grad(a, st));
   if (rc != GEMMQ_OK || !dw) return rc;
-  return launched(launch_join(part, kp, rms_grad_groups(M), dw, (int)K, st));
+  return launched(launch_join(part, kp, rms_grad_groups(M, K), dw, (int)K, st));
 }
 
 int gemmq_gemm_i8_act(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,

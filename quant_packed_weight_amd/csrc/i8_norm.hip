@@ -289,6 +289,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const float* part
   out[k] = s;
 }
 
+// Rows in flight: four workgroups a CU (2048 x 4096 in bf16 with 512 / 1024 / 2048 workgroups
+// 18.7 / 16.0 / 17.0 us).  A row of up to 4096 16-bit values is shared by 256 threads, of more
+// by 512 (us, 512 / 256 threads: 1024 x 5120 in bf16 13.2 / 15.8, 2048 x 4096 in f32 21 / 31), of
+// f32 beyond 4096 by 1024 (1024 x 8192 26.9, by 512 29.5); of more than 16384 16-bit or 8192
+// f32 values it is read twice.
 constexpr int kRmsGroups = 1024;
 
 template <int TYPE, bool DW>
@@ -296,8 +301,10 @@ void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
   constexpr int V = kValues<TYPE>;
   if (a.K <= 256 * 2 * V)
     rms_grad_kernel<TYPE, 256, 2, DW><<<groups, 256, 0, st>>>(a);
-  else if (a.K <= 256 * 4 * V)
-    rms_grad_kernel<TYPE, 256, 4, DW><<<groups, 256, 0, st>>>(a);
+  else if (a.K <= 512 * 2 * V)
+    rms_grad_kernel<TYPE, 512, 2, DW><<<groups, 512, 0, st>>>(a);
+  else if (a.K <= 512 * 4 * V)
+    rms_grad_kernel<TYPE, 512, 4, DW><<<groups, 512, 0, st>>>(a);
   else
     rms_grad_kernel<TYPE, 1024, 0, DW><<<groups, 1024, 0, st>>>(a);
 }
@@ -308,6 +315,10 @@ void launch_type(const RmsArgs& a, hipStream_t st) {
   const uint32_t g = a.M < kRmsGroups ? a.M : kRmsGroups;
   if (a.K <= 256 * 2 * V)
     rms_kernel<TYPE, 256, 2><<<g, 256, 0, st>>>(a);
+  else if (a.K <= 512 * 2 * V)
+    rms_kernel<TYPE, 512, 2><<<g, 512, 0, st>>>(a);
+  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
+    rms_kernel<GEMMQ_F32, 1024, 2><<<g, 1024, 0, st>>>(a);
   else if (a.K <= 512 * 4 * V)
     rms_kernel<TYPE, 512, 4><<<g, 512, 0, st>>>(a);
   else
@@ -323,10 +334,17 @@ int launch_rms(const RmsArgs& a, hipStream_t st) {
   return 0;
 }
 
-int rms_grad_groups(int64_t M) { return (int)(M < 512 ? M : 512); }
+// As many workgroups as the CUs hold: two each, of rows beyond 4096 one, whose threads keep
+// twice as much (us with 512 and 256 workgroups: bf16, 2048 x 4096 17.0 / 19.6, 1024 x 8192 24.8
+// / 19.6, 680 x 12288 27.8 / 22.6; f32, 2048 x 4096 27.9 / 31.5, 1024 x 8192 37.8 / 33.9).  Without
+// partial sums two are never slower by more than 6% (f32, 2048 x 4096 23.9 / 28.7).
+int rms_grad_groups(int64_t M, int64_t K) {
+  const int64_t most = K <= 4096 ? 512 : 256;
+  return (int)(M < most ? M : most);
+}
 
 int launch_rms_grad(const RmsGradArgs& a, hipStream_t st) {
-  const int g = rms_grad_groups(a.M);
+  const int g = a.part ? rms_grad_groups(a.M, a.K) : a.M < 512 ? a.M : 512;
   const bool dw = a.part != nullptr;
   if (a.type == GEMMQ_F32)
     dw ? launch_grad<GEMMQ_F32, true>(a, g, st) : launch_grad<GEMMQ_F32, false>(a, g, st);

@@ -40,7 +40,8 @@ def check(got, x, r, w, eps):
 
 
 SHAPES = [(1, 1), (1, 16), (3, 17), (5, 255), (2, 256), (7, 1000), (4, 4096), (2, 12289), (1, 8193),
-          (300, 64), (2, 16385), (3, 40001), (1, 131071)]
+          (300, 64), (2, 8192), (3, 4097), (2, 16384), (2, 16385), (3, 40001),
+          (1, 131071)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
@@ -150,7 +151,7 @@ def check_grad(got, h, w, dy, dh, eps):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
-@pytest.mark.parametrize("M,K", SHAPES + [(513, 130), (1100, 40), (2, 2049), (5, 4097), (600, 16400)])
+@pytest.mark.parametrize("M,K", SHAPES + [(513, 130), (1100, 40), (2, 2049), (5, 4097), (300, 5000), (600, 16400)])
 @pytest.mark.parametrize("extra", [0, 3, 8])
 def test_rms_grad(M, K, dtype, extra):
     g = gen(M * 31 + K)
