@@ -195,8 +195,9 @@ int gemmq_rms_i8(int type, const void *X, int64_t ldx, const void *R, int64_t ld
                  int64_t ldh, const float *w, float eps, int8_t *Q, int64_t ldq, float *s,
                  int64_t M, int64_t K, void *stream);
 
-/* Workspace bytes of gemmq_rms_i8_grad with a dw (0 for arguments it refuses; without
-   a dw no workspace is needed). */
+/* Workspace bytes of gemmq_rms_i8_grad with a dw (without one none is needed).  Here and for
+   the two entries below 0 is also the size for arguments that the entry refuses, and where it
+   needs no workspace: ws may be NULL then. */
 size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K);
 
 /*
@@ -267,8 +268,7 @@ int gemmq_linear_i8_gate(const int8_t *W, int64_t ldw, const float *sw, const in
                          int act, int ytype, void *Y, int64_t ldy, void *Z, int64_t ldz, void *U,
                          int64_t ldu, int64_t M, int64_t N, int64_t K, void *stream);
 
-/* Workspace bytes of gemmq_act_grad with a db or dbu (0 for arguments it refuses;
-   without them no workspace is needed). */
+/* Workspace bytes of gemmq_act_grad with a db or dbu (without them none is needed). */
 size_t gemmq_act_grad_workspace(int type, int64_t M, int64_t N);
 
 /*
@@ -285,14 +285,15 @@ size_t gemmq_act_grad_workspace(int type, int64_t M, int64_t N);
  *         only with U.
  *   ws    may be NULL where db and dbu are.
  * Errors: as gemmq_quantize_i8, and GEMMQ_E_INVALID_ARG for an unknown act, one of U
- *         and dU alone, a dbu without U, or a workspace that is too small.
+ *         and dU alone, a dbu without U, db and dbu the same vector, or a workspace that
+ *         is too small.
  */
 int gemmq_act_grad(int act, int type, const void *Z, int64_t ldz, const void *U, int64_t ldu,
                    const void *dY, int64_t lddy, void *dZ, int64_t lddz, void *dU, int64_t lddu,
                    float *db, float *dbu, int64_t M, int64_t N, void *ws, size_t ws_bytes,
                    void *stream);
 
-/* Workspace bytes of gemmq_sample (0 for arguments it refuses). */
+/* Workspace bytes of gemmq_sample. */
 size_t gemmq_sample_workspace(int64_t M, int64_t N);
 
 /*

@@ -22,6 +22,11 @@ def _optional(t, name, dtype, rows, cols, index):
     return (None, 0) if t is None else (t.data_ptr(), _matrix(t, name, dtype, rows, cols, index))
 
 
+def _needed(workspace, need, device):
+    """The workspace of a call that may need none"""
+    return None if workspace is None and not need else _workspace(workspace, need, device)
+
+
 def rms_i8(x, w, eps=1e-6, residual=None, hidden=None, out=None, scale=None, stream=None):
     """h = x + residual and the root-mean-square norm of h's rows, times w, as int8 rows
     with one f32 scale each (gemmq_rms_i8): x, residual f32, bf16 or f16 [M, K], w f32
@@ -76,7 +81,7 @@ def rms_i8_grad(h, w, dy, dh=None, eps=1e-6, out=None, dw=None, weight_grad=True
     if dw is None and weight_grad:
         dw = torch.empty(K, dtype=f32, device=h.device)
     if dw is not None:
-        ws = _workspace(workspace, L.gemmq_rms_i8_grad_workspace(ty, M, K), h.device)
+        ws = _needed(workspace, L.gemmq_rms_i8_grad_workspace(ty, M, K), h.device)
     d, ldd = _optional(dh, "dh", dt, M, K, dev)
     _check(L.gemmq_rms_i8_grad(
         ty, h.data_ptr(), _matrix(h, "h", None, M, K, dev), _vector(w, "w", f32, K, dev), eps,
@@ -89,7 +94,7 @@ def rms_i8_grad(h, w, dy, dh=None, eps=1e-6, out=None, dw=None, weight_grad=True
 
 
 def rms_i8_grad_workspace(dtype, M, K):
-    """Bytes of rms_i8_grad's workspace for rows of `dtype` [M, K] with a dw."""
+    """Bytes of rms_i8_grad's workspace for rows of `dtype` [M, K] with a dw (0: none)."""
     L = lib_i8()
     return L.gemmq_rms_i8_grad_workspace(_type(dtype, "dtype"), M, K)
 
@@ -217,7 +222,7 @@ def act_grad(act, z, dy, up=None, out=None, dup=None, dbias=None, dbias_up=None,
         dup = torch.empty((M, N), dtype=dt, device=z.device)
     ws = None
     if dbias is not None or dbias_up is not None:
-        ws = _workspace(workspace, L.gemmq_act_grad_workspace(ty, M, N), z.device)
+        ws = _needed(workspace, L.gemmq_act_grad_workspace(ty, M, N), z.device)
     u, ldu = _optional(up, "up", dt, M, N, dev)
     du, lddu = _optional(dup, "dup", dt, M, N, dev)
     _check(L.gemmq_act_grad(
@@ -231,7 +236,7 @@ def act_grad(act, z, dy, up=None, out=None, dup=None, dbias=None, dbias_up=None,
 
 
 def act_grad_workspace(dtype, M, N):
-    """Bytes of act_grad's workspace for [M, N] of `dtype`, with a bias's gradient."""
+    """Bytes of act_grad's workspace for [M, N] of `dtype`, with a bias's gradient (0: none)."""
     L = lib_i8()
     return L.gemmq_act_grad_workspace(_type(dtype, "dtype"), M, N)
 
@@ -257,7 +262,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         out = torch.empty(M, dtype=torch.int64, device=logits.device)
     if logprob is None:
         logprob = torch.empty(M, dtype=f32, device=logits.device)
-    ws = _workspace(workspace, L.gemmq_sample_workspace(M, N), logits.device)
+    ws = _needed(workspace, L.gemmq_sample_workspace(M, N), logits.device)
     _check(L.gemmq_sample(
         _type(logits.dtype, "logits"), logits.data_ptr(), _matrix(logits, "logits", None, M, N, dev),
         None if temperature is None else _vector(temperature, "temperature", f32, M, dev),
@@ -265,10 +270,11 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         None if top_p is None else _vector(top_p, "top_p", f32, M, dev),
         None if min_p is None else _vector(min_p, "min_p", f32, M, dev), _vector(u, "u", f32, M, dev),
         _vector(out, "out", torch.int64, M, dev), _vector(logprob, "logprob", f32, M, dev), M, N,
-        ws.data_ptr(), ws.nbytes, _here(dev)), "gemmq_sample")
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _here(dev)),
+        "gemmq_sample")
     return out, logprob
 
 
 def sample_workspace(M, N):
-    """Bytes of sample's workspace for logits [M, N]."""
+    """Bytes of sample's workspace for logits [M, N] (0: none)."""
     return lib_i8().gemmq_sample_workspace(M, N)

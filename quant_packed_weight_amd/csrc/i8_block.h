@@ -27,17 +27,22 @@ struct RmsGradArgs {
   const void *H, *dY, *dH;  // dH may be null
   const float* w;
   void* dX;
-  float* part;  // [rms_grad_groups][kp], or null: no dw
-  int64_t ldh, lddy, lddh, lddx, kp;  // kp: K rounded up to a multiple of 4
+  float* part;  // [rms_grad_groups][kp], of one group dw itself; or null: no dw
+  int64_t ldh, lddy, lddh, lddx, kp;  // kp: K rounded up to a multiple of 4, or K of dw itself
   int type, M, K;
   float eps;
-  bool wide_h, wide_dy, wide_dh, wide_dx, wide_w;
+  bool wide_h, wide_dy, wide_dh, wide_dx, wide_w, wide_part;
 };
 int rms_grad_groups(int64_t M, int64_t K);
 int launch_rms_grad(const RmsGradArgs& a, hipStream_t st);
 
-// out[k] = the sum of `count` rows of part, in a fixed order (count 0: zeros)
-int launch_join(const float* part, int64_t pitch, int count, float* out, int K, hipStream_t st);
+// out[k] = the sum of `count` rows of part, in a fixed order (count 0: zeros); and of a second
+// one in the same launch, where it is not null
+struct Join {
+  const float* part;
+  float* out;
+};
+int launch_join(Join a, Join b, int64_t pitch, int count, int K, hipStream_t st);
 
 // The product with an activation, and the gated pair of products (i8_act.hip):
 // y = act(z) (+ r), or act(z) u.  A matrix of results or residuals has 16-bit rows that
@@ -64,11 +69,11 @@ int launch_act_fused(int xtype, const void* X, int64_t ldx, const Operands& op, 
                      bool pair, hipStream_t st);
 
 // i8_act_grad.hip: dZ = dY act'(Z), or with U dZ = dY U act'(Z) and dU = dY act(Z);
-// part (or null) receives [2 of a pair][act_grad_groups][np] sums over rows.
+// sums[0] and sums[1] (or null) receive the groups' sums over rows of dZ and dU, np apart.
 struct ActGradArgs {
   Rows Z, U, dY, dZ, dU;  // U, dU null: no pair
-  float* part;
-  int64_t np;  // N rounded up to a multiple of 4
+  float* sums[2];
+  int64_t np;
   int act, type, M, N, groups;
 };
 int act_grad_groups(int type, int64_t M, int64_t N);  // with sums over rows

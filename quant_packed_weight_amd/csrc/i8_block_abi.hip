@@ -103,6 +103,11 @@ int run_linear(int xtype, const void* X, int64_t ldx, int8_t* Xq, int64_t ldq, f
   return launched(launch_act(op, out, pair, st));
 }
 
+// a workspace where one is needed
+int check_need(const void* ws, size_t have, size_t need) {
+  return need > 0 ? check_ws(ws, have, need) : GEMMQ_OK;
+}
+
 bool eps_ok(float eps) { return eps >= 0.0f && eps < __builtin_inff(); }
 
 }  // namespace
@@ -136,7 +141,8 @@ int gemmq_rms_i8(int type, const void* X, int64_t ldx, const void* R, int64_t ld
 
 size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K) {
   if (!known(type) || check_shape(M, 0, K) != GEMMQ_OK || M == 0) return 0;
-  return align_up(4 * rms_grad_groups(M, K) * (int64_t)align_up(K, 4), 256);
+  const int64_t groups = rms_grad_groups(M, K);
+  return groups > 1 ? align_up(4 * groups * (int64_t)align_up(K, 4), 256) : 0;
 }
 
 int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, float eps,
@@ -153,7 +159,7 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
     rc = check_device();
     if (rc != GEMMQ_OK) return rc;
     clear_pending();
-    return launched(launch_join(nullptr, 0, 0, dw, (int)K, st));
+    return launched(launch_join({nullptr, dw}, {}, 0, 0, (int)K, st));
   }
   rc = check_rows(type, H, ldh, K);
   if (rc == GEMMQ_OK) rc = check_rows(type, dY, lddy, K);
@@ -163,20 +169,22 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
   if (rc == GEMMQ_OK && !aligned(w, 4)) rc = GEMMQ_E_ALIGNMENT;
   if (rc == GEMMQ_OK && !(same_rows(dX, lddx, dY, lddy, M) && same_rows(dX, lddx, dH, lddh, M)))
     rc = GEMMQ_E_INVALID_ARG;
-  if (rc == GEMMQ_OK && dw) rc = check_ws(ws, ws_bytes, gemmq_rms_i8_grad_workspace(type, M, K));
+  if (rc == GEMMQ_OK && dw) rc = check_need(ws, ws_bytes, gemmq_rms_i8_grad_workspace(type, M, K));
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
-  const int64_t kp = (int64_t)align_up(K, 4);
-  float* part = dw ? static_cast<float*>(ws) : nullptr;
+  const int groups = rms_grad_groups(M, K);
+  const bool join = dw && groups > 1;  // else the kernel's sums are dw
+  const int64_t kp = join ? (int64_t)align_up(K, 4) : K;
+  float* part = join ? static_cast<float*>(ws) : dw;
   const RmsGradArgs a{H,    dY,   dH,   w,    dX,     part,   ldh,
                       lddy, lddh, lddx, kp,   type,   (int)M, (int)K,
                       eps,  wide_rows(H, ldh, type),  wide_rows(dY, lddy, type),
                       wide_rows(dH, lddh, type),      wide_rows(dX, lddx, type),
-                      aligned(w, 16)};
+                      aligned(w, 16),                 aligned(part, 16)};
   clear_pending();
   rc = launched(launch_rms_grad(a, st));
-  if (rc != GEMMQ_OK || !dw) return rc;
-  return launched(launch_join(part, kp, rms_grad_groups(M, K), dw, (int)K, st));
+  if (rc != GEMMQ_OK || !join) return rc;
+  return launched(launch_join({part, dw}, {}, kp, groups, (int)K, st));
 }
 
 int gemmq_gemm_i8_act(const int8_t* W, int64_t ldw, const float* sw, const int8_t* Xq, int64_t ldq,
@@ -239,7 +247,8 @@ int gemmq_linear_i8_gate(const int8_t* W, int64_t ldw, const float* sw, const in
 
 size_t gemmq_act_grad_workspace(int type, int64_t M, int64_t N) {
   if (!known(type) || check_shape(M, N, 1) != GEMMQ_OK || M == 0 || N == 0) return 0;
-  return align_up(8 * act_grad_groups(type, M, N) * (int64_t)align_up(N, 4), 256);
+  const int64_t groups = act_grad_groups(type, M, N);
+  return groups > 1 ? align_up(8 * groups * (int64_t)align_up(N, 4), 256) : 0;
 }
 
 int gemmq_act_grad(int act, int type, const void* Z, int64_t ldz, const void* U, int64_t ldu,
@@ -251,6 +260,7 @@ int gemmq_act_grad(int act, int type, const void* Z, int64_t ldz, const void* U,
   if (!known(type) || !known_act(act)) return GEMMQ_E_INVALID_ARG;
   // (a matrix without rows may have no address)
   if (M > 0 && (!U != !dU || (dbu && !U))) return GEMMQ_E_INVALID_ARG;
+  if (db && db == dbu) return GEMMQ_E_INVALID_ARG;
   if (!aligned(db, 4) || !aligned(dbu, 4)) return GEMMQ_E_ALIGNMENT;
   const bool sums = db || dbu;
   if (N == 0 || (M == 0 && !sums)) return GEMMQ_OK;
@@ -265,25 +275,27 @@ int gemmq_act_grad(int act, int type, const void* Z, int64_t ldz, const void* U,
     if (!same_rows(dZ, lddz, Z, ldz, M) || !same_rows(dZ, lddz, dY, lddy, M) ||
         !same_rows(dU, lddu, U, ldu, M) || !same_rows(dU, lddu, dY, lddy, M) || dZ == dU)
       return GEMMQ_E_INVALID_ARG;
-    if (sums) rc = check_ws(ws, ws_bytes, gemmq_act_grad_workspace(type, M, N));
+    if (sums) rc = check_need(ws, ws_bytes, gemmq_act_grad_workspace(type, M, N));
   }
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   clear_pending();
-  float* part = sums && M > 0 ? static_cast<float*>(ws) : nullptr;
+  if (M == 0)  // sums of nothing
+    return launched(launch_join({nullptr, db}, {nullptr, dbu}, 0, 0, (int)N, st));
+  const int groups = act_grad_groups(type, M, N);
+  const bool join = sums && groups > 1;  // else the kernel's sums are the results
   const int64_t np = (int64_t)align_up(N, 4);
-  const int groups = part ? act_grad_groups(type, M, N) : 0;
-  if (M > 0) {
-    const ActGradArgs a{rows(type, Z, ldz),   rows(type, U, ldu), rows(type, dY, lddy),
-                        rows(type, dZ, lddz), rows(type, dU, lddu), part, np, act, type,
-                        (int)M, (int)N, 0};
-    rc = launched(launch_act_grad(a, st));
-    if (rc != GEMMQ_OK) return rc;
+  float* part = static_cast<float*>(ws);
+  ActGradArgs a{rows(type, Z, ldz),   rows(type, U, ldu),   rows(type, dY, lddy),
+                rows(type, dZ, lddz), rows(type, dU, lddu), {db, dbu}, np, act, type,
+                (int)M, (int)N, 0};
+  if (join) {
+    a.sums[0] = db ? part : nullptr;
+    a.sums[1] = dbu ? part + groups * np : nullptr;
   }
-  if (db) rc = launched(launch_join(part, np, groups, db, (int)N, st));
-  if (rc == GEMMQ_OK && dbu)
-    rc = launched(launch_join(part ? part + groups * np : nullptr, np, groups, dbu, (int)N, st));
-  return rc;
+  rc = launched(launch_act_grad(a, st));
+  if (rc != GEMMQ_OK || !join) return rc;
+  return launched(launch_join({a.sums[0], db}, {a.sums[1], dbu}, np, groups, (int)N, st));
 }
 
 size_t gemmq_sample_workspace(int64_t M, int64_t N) {
@@ -306,7 +318,7 @@ int gemmq_sample(int type, const void* Z, int64_t ldz, const float* temperature,
   if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) ||
       !aligned(u, 4) || !aligned(token, 8) || !aligned(logprob, 4))
     return GEMMQ_E_ALIGNMENT;
-  rc = check_ws(ws, ws_bytes, gemmq_sample_workspace(M, N));
+  rc = check_need(ws, ws_bytes, gemmq_sample_workspace(M, N));
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   SampleArgs a{};

@@ -260,9 +260,8 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
       const int k = kSpan * i + V * t;
 #pragma unroll
       for (int e = 0; e < V; e += 4)
-        if (k + e < a.kp)  // a multiple of 4
-          *reinterpret_cast<float4*>(part + k + e) =
-              make_float4(dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]);
+        store4_as(part, k + e, GEMMQ_F32, a.wide_part, a.kp - (k + e), dw[i][e], dw[i][e + 1],
+                  dw[i][e + 2], dw[i][e + 3]);
     }
   }
 }
@@ -270,9 +269,11 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
 // out[k] = the sum of part[g][k] over g < count: 64 columns a workgroup, its waves a
 // sixteenth of the rows each
 constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const float* part, int64_t pitch,
-                                                               int count, float* out, int K) {
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Join a, Join b, int64_t pitch,
+                                                               int count, int K) {
   __shared__ float sums[kJoinWaves][64];
+  const float* part = blockIdx.y ? b.part : a.part;
+  float* out = blockIdx.y ? b.out : a.out;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t k = (int64_t)blockIdx.x * 64 + lane;
   const int each = (count + kJoinWaves - 1) / kJoinWaves, end = min(count, each * (wave + 1));
@@ -338,8 +339,11 @@ int launch_rms(const RmsArgs& a, hipStream_t st) {
 // twice as much (us with 512 and 256 workgroups: bf16, 2048 x 4096 17.0 / 19.6, 1024 x 8192 24.8
 // / 19.6, 680 x 12288 27.8 / 22.6; f32, 2048 x 4096 27.9 / 31.5, 1024 x 8192 37.8 / 33.9).  Without
 // partial sums two are never slower by more than 6% (f32, 2048 x 4096 23.9 / 28.7).
+// A few short rows go through one workgroup, whose sums are dw itself: a launch less.  A call in
+// bf16 that way is 8.0 us of 2 x 4096, 8.5 of 4 x 4096, 10.0 of 2 x 12288 and 16.1 of 4 x 12288; one
+// that joins the sums of five workgroups 12.5 at any of these widths.
 int rms_grad_groups(int64_t M, int64_t K) {
-  const int64_t most = K <= 4096 ? 512 : 256;
+  const int64_t most = M <= 4 && M * K <= 24576 ? 1 : K <= 4096 ? 512 : 256;
   return (int)(M < most ? M : most);
 }
 
@@ -355,8 +359,10 @@ int launch_rms_grad(const RmsGradArgs& a, hipStream_t st) {
   return 0;
 }
 
-int launch_join(const float* part, int64_t pitch, int count, float* out, int K, hipStream_t st) {
-  join_kernel<<<(uint32_t)ceil_div(K, 64), 64 * kJoinWaves, 0, st>>>(part, pitch, count, out, K);
+int launch_join(Join a, Join b, int64_t pitch, int count, int K, hipStream_t st) {
+  if (!a.out) a = b, b.out = nullptr;
+  const dim3 grid((uint32_t)ceil_div(K, 64), b.out ? 2 : 1);
+  join_kernel<<<grid, 64 * kJoinWaves, 0, st>>>(a, b, pitch, count, K);
   return 0;
 }
 

@@ -239,7 +239,7 @@ def test_empty_products():
 
 # ------------------------------------------------------------------ the gradient
 GRADS = [(1, 1), (3, 7), (1, 4096), (2, 255), (5, 512), (9, 513), (77, 1037), (300, 2050),
-         (1000, 130), (33, 12289), (4099, 64), (2048, 300), (7, 100000)]
+         (1000, 130), (33, 12289), (4099, 64), (2048, 300), (7, 100000), (16, 520), (17, 520)]
 
 
 @pytest.mark.parametrize("M,N", GRADS)

@@ -273,6 +273,7 @@ def test_refusals_on_the_device():
     w, sw, xq, sx = i8(40, 64, g), scales(40, g), i8(4, 64, g), scales(4, g)
     x, w1 = torch.zeros((4, 64), device="cuda"), torch.ones(64, device="cuda")
     z, u = torch.zeros((4, 40), device="cuda"), torch.zeros(4, device="cuda")
+    x9, far = torch.zeros((9, 64), device="cuda"), torch.zeros((1, 50000), device="cuda")
     half = lambda t: t.half()  # noqa: E731
     bad = [
         lambda: gq.rms_i8(x, w1[:63]),                                # a weight of another width
@@ -289,7 +290,7 @@ def test_refusals_on_the_device():
         lambda: gq.rms_i8_grad(x, w1, half(x)),
         lambda: gq.rms_i8_grad(x, w1, x, dh=x[:3]),
         lambda: gq.rms_i8_grad(x, w1, x, dw=w1[:63]),
-        lambda: gq.rms_i8_grad(x, w1, x, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: gq.rms_i8_grad(x9, w1, x9, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
         lambda: gq.gemm_i8_act(w, sw, xq, sx, 9),                     # no such activation
         lambda: gq.gemm_i8_act(w, sw, xq, sx, gq.ACT_SILU, residual=half(z)),
         lambda: gq.gemm_i8_act(w, sw, xq, sx, gq.ACT_SILU, pre=z[:, :39]),
@@ -309,7 +310,7 @@ def test_refusals_on_the_device():
         lambda: gq.sample(z, u, temperature=torch.ones(8, device="cuda")[::2]),
         lambda: gq.sample(z[:, :0], u),                               # no vocabulary
         lambda: gq.sample(z, u, out=torch.zeros(4, dtype=torch.int32, device="cuda")),
-        lambda: gq.sample(z, u, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: gq.sample(far, u[:1], workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
         lambda: gq.sample(z, u.cpu()),
     ]
     for i, call in enumerate(bad):

@@ -151,7 +151,8 @@ def check_grad(got, h, w, dy, dh, eps):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
-@pytest.mark.parametrize("M,K", SHAPES + [(513, 130), (1100, 40), (2, 2049), (5, 4097), (300, 5000), (600, 16400)])
+@pytest.mark.parametrize("M,K", SHAPES + [(513, 130), (1100, 40), (2, 2049), (5, 4097), (300, 5000), (600, 16400),
+                                          (4, 6144), (4, 6145), (6, 4100)])
 @pytest.mark.parametrize("extra", [0, 3, 8])
 def test_rms_grad(M, K, dtype, extra):
     g = gen(M * 31 + K)

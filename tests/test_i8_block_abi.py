@@ -22,7 +22,7 @@ NAN, INF = float("nan"), float("inf")
 RMS = dict(type=1, X=A, ldx=100, R=A, ldr=100, H=B, ldh=100, w=A, eps=1e-6, Q=A, ldq=112, s=A, M=4,
            K=100)
 RGRAD = dict(type=1, H=A, ldh=100, w=A, eps=1e-6, dY=A, lddy=100, dH=A, lddh=100, dX=B, lddx=100,
-             dw=A, M=4, K=100, ws=A, bytes=1 << 40)
+             dw=A, M=40, K=100, ws=A, bytes=1 << 40)
 GEMM = dict(W=A, ldw=112, sw=A, Xq=A, ldq=112, sx=A, bias=A, act=1, R=A, ldr=50, ytype=0, Y=B,
             ldy=50, Z=B, ldz=50, M=4, N=50, K=100)
 LINEAR = dict(W=A, ldw=112, sw=A, xtype=1, X=A, ldx=100, Xq=A, ldq=112, sx=A, bias=A, act=1, R=A,
@@ -33,9 +33,9 @@ LGATE = dict(W=A, ldw=112, sw=A, Wu=A, ldwu=112, swu=A, xtype=1, X=A, ldx=100, X
              bias=A, biasu=A, act=1, ytype=2, Y=B, ldy=50, Z=B, ldz=50, U=B, ldu=50, M=4, N=50,
              K=100)
 AGRAD = dict(act=1, type=1, Z=A, ldz=50, U=A, ldu=50, dY=A, lddy=50, dZ=B, lddz=50, dU=2 * B,
-             lddu=50, db=A, dbu=A, M=4, N=50, ws=A, bytes=1 << 40)
-SAMPLE = dict(type=1, Z=A, ldz=50, temperature=A, top_k=A, top_p=A, min_p=A, u=A, token=A, logprob=A,
-              M=4, N=50, ws=A, bytes=1 << 40)
+             lddu=50, db=A, dbu=3 * B, M=40, N=50, ws=A, bytes=1 << 40)
+SAMPLE = dict(type=1, Z=A, ldz=50000, temperature=A, top_k=A, top_p=A, min_p=A, u=A, token=A,
+              logprob=A, M=4, N=50000, ws=A, bytes=1 << 40)
 ENTRIES = {"sample": SAMPLE, "rms_i8": RMS, "rms_i8_grad": RGRAD, "gemm_i8_act": GEMM, "linear_i8_act": LINEAR,
            "gemm_i8_gate": GATE, "linear_i8_gate": LGATE, "act_grad": AGRAD}
 _Y = [("Y", "ldy", "N", False), ("Z", "ldz", "N", True)]
@@ -69,7 +69,7 @@ OWN = {"rms_i8": [(dict(H=A, ldh=104, R=B), INVALID),            # X, but not as
        "rms_i8_grad": [(dict(dX=A, lddx=104, dH=B), INVALID), (dict(dX=B, lddx=104, dH=B), INVALID)],
        "gemm_i8_act": [(dict(R=B, ldr=52), INVALID)], "linear_i8_act": [(dict(R=B, ldr=52), INVALID)],
        "sample": [(dict(N=0), SHAPE), (dict(token=A + 4), ALIGN)],
-       "act_grad": [(dict(U=None), INVALID), (dict(dU=None), INVALID),
+       "act_grad": [(dict(U=None), INVALID), (dict(dU=None), INVALID), (dict(dbu=A), INVALID),
                     (dict(U=None, dU=None), INVALID),   # a dbu without a pair
                     (dict(dZ=A, lddz=52), INVALID), (dict(dU=A, lddu=52), INVALID),
                     (dict(dU=B), INVALID)]}            # dZ's place
@@ -153,26 +153,30 @@ def test_workspace_sizes(L):
     import torch
 
     for ty, dtype in enumerate((torch.float32, torch.bfloat16, torch.float16)):
-        need = L.gemmq_rms_i8_grad_workspace(ty, 4, 100)
-        assert need >= 4 * 100 * 4
+        need = L.gemmq_rms_i8_grad_workspace(ty, 40, 100)
+        assert need >= 40 * 100 * 4
+        assert L.gemmq_rms_i8_grad_workspace(ty, 4, 100) == 0  # none is needed
         assert L.gemmq_rms_i8_grad(*dict(RGRAD, type=ty, bytes=need - 1).values(), None) == INVALID
-        assert gq.rms_i8_grad_workspace(dtype, 4, 100) == need
-        need = L.gemmq_act_grad_workspace(ty, 4, 50)
-        assert need >= 2 * 50 * 4 and gq.act_grad_workspace(dtype, 4, 50) == need
+        assert gq.rms_i8_grad_workspace(dtype, 40, 100) == need
+        need = L.gemmq_act_grad_workspace(ty, 40, 50)
+        assert need >= 2 * 50 * 4 and gq.act_grad_workspace(dtype, 40, 50) == need
+        assert L.gemmq_act_grad_workspace(ty, 16, 50) == 0
         assert L.gemmq_act_grad(*dict(AGRAD, type=ty, bytes=need - 1).values(), None) == INVALID
         assert L.gemmq_act_grad_workspace(ty, 1 << 20, 12288) < 64 << 20
         # a few rows of partial sums, not one for each row
         assert L.gemmq_rms_i8_grad_workspace(ty, 1 << 20, 4096) < 64 << 20
-    for bad in ((3, 4, 100), (0, -1, 100), (0, 4, 0), (0, 0, 100)):
+    for bad in ((3, 40, 100), (0, -1, 100), (0, 40, 0), (0, 0, 100)):
         assert L.gemmq_rms_i8_grad_workspace(*bad) == 0
         assert L.gemmq_act_grad_workspace(*bad) == 0
 
 
 def test_sample_workspace(L):
-    need = L.gemmq_sample_workspace(4, 50)
-    assert need > 0 and gq.sample_workspace(4, 50) == need
+    need = L.gemmq_sample_workspace(4, 50000)
+    assert need > 0 and gq.sample_workspace(4, 50000) == need
+    assert L.gemmq_sample_workspace(4, 5000) == 0  # none is needed
     assert L.gemmq_sample(*dict(SAMPLE, bytes=need - 1).values(), None) == INVALID
-    for bad in ((0, 50), (4, 0), (-1, 50), (4, -1), (gq.I8_MAX_ROWS + 1, 4), (4, gq.I8_MAX_ROWS + 1)):
+    for bad in ((0, 50000), (4, 0), (-1, 50000), (4, -1), (gq.I8_MAX_ROWS + 1, 50000),
+                (4, gq.I8_MAX_ROWS + 1)):
         assert L.gemmq_sample_workspace(*bad) == 0
     # bounded for any number of rows
     assert L.gemmq_sample_workspace(1 << 24, 151936) < 64 << 20
