@@ -208,7 +208,7 @@ size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K);
  * dX is the gradient with respect to x and to r, where dH is what arrives at h by the
  * residual path.
  *   type  of H, dY, dH and dX, all [M, K].   dH  may be NULL.
- *   dX    may be dY or dH itself (the same pointer and pitch).
+ *   dX    may be H, dY or dH itself (the same pointer and pitch).
  *   dw    f32 [K], overwritten (zeros where M == 0), or NULL: not computed.
  *   ws    may be NULL where dw is.
  * Errors: as gemmq_rms_i8, and GEMMQ_E_INVALID_ARG for a workspace that is too small.
@@ -231,8 +231,9 @@ int gemmq_rms_i8_grad(int type, const void *H, int64_t ldh, const float *w, floa
  *   Y[m, n] = act(z[m, n])  (+ R[m, n])
  * in f32, rounded once to Y's type.
  *   R, ldr  [M, N] of Y's type, or NULL; Y may be R itself (the same pointer and pitch).
- *   Z, ldz  [M, N] of Y's type, or NULL: receives z, rounded, for gemmq_act_grad.
- * Errors: as gemmq_gemm_i8, and GEMMQ_E_INVALID_ARG for an unknown act.
+ *   Z, ldz  [M, N] of Y's type, or NULL: receives z, rounded, for gemmq_act_grad; not R.
+ * Errors: as gemmq_gemm_i8, and GEMMQ_E_INVALID_ARG for an unknown act, or one matrix as
+ *         two of the results.
  */
 int gemmq_gemm_i8_act(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Xq, int64_t ldq,
                       const float *sx, const float *bias, int act, const void *R, int64_t ldr,

@@ -58,7 +58,9 @@ int check_act(const int8_t* W, int64_t ldw, const float* sw, const Pair* pair, c
   if (rc == GEMMQ_OK && pair) rc = check_optional(ytype, pair->U, pair->ldu, N);
   if (rc != GEMMQ_OK) return rc;
   if (!aligned(bias, 4) || (pair && !aligned(pair->bias, 4))) return GEMMQ_E_ALIGNMENT;
-  if (!same_rows(Y, ldy, R, ldr, M)) return GEMMQ_E_INVALID_ARG;
+  const void* U = pair ? pair->U : nullptr;
+  if (!same_rows(Y, ldy, R, ldr, M) || Y == Z || Y == U || (Z && (Z == U || Z == R)))
+    return GEMMQ_E_INVALID_ARG;
   if (!act_fits((int)M, (int)N, (int)K, pair != nullptr)) return GEMMQ_E_SHAPE;
   op = Operands{W, sw, Xq, sx, ldw, ldq, (int)M, (int)N, (int)K};
   out = ActOut{};
@@ -167,7 +169,8 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
   if (rc == GEMMQ_OK) rc = check_rows(type, dX, lddx, K);
   if (rc == GEMMQ_OK && !w) rc = GEMMQ_E_INVALID_ARG;
   if (rc == GEMMQ_OK && !aligned(w, 4)) rc = GEMMQ_E_ALIGNMENT;
-  if (rc == GEMMQ_OK && !(same_rows(dX, lddx, dY, lddy, M) && same_rows(dX, lddx, dH, lddh, M)))
+  if (rc == GEMMQ_OK && !(same_rows(dX, lddx, dY, lddy, M) && same_rows(dX, lddx, dH, lddh, M) &&
+                          same_rows(dX, lddx, H, ldh, M)))
     rc = GEMMQ_E_INVALID_ARG;
   if (rc == GEMMQ_OK && dw) rc = check_need(ws, ws_bytes, gemmq_rms_i8_grad_workspace(type, M, K));
   if (rc == GEMMQ_OK) rc = check_device();
@@ -180,7 +183,7 @@ int gemmq_rms_i8_grad(int type, const void* H, int64_t ldh, const float* w, floa
                       lddy, lddh, lddx, kp,   type,   (int)M, (int)K,
                       eps,  wide_rows(H, ldh, type),  wide_rows(dY, lddy, type),
                       wide_rows(dH, lddh, type),      wide_rows(dX, lddx, type),
-                      aligned(w, 16),                 aligned(part, 16)};
+                      aligned(w, 16),                 kp % 4 == 0 && aligned(part, 16)};
   clear_pending();
   rc = launched(launch_rms_grad(a, st));
   if (rc != GEMMQ_OK || !join) return rc;

@@ -259,9 +259,17 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
     for (int i = 0; i < HELD; ++i) {
       const int k = kSpan * i + V * t;
 #pragma unroll
-      for (int e = 0; e < V; e += 4)
-        store4_as(part, k + e, GEMMQ_F32, a.wide_part, a.kp - (k + e), dw[i][e], dw[i][e + 1],
-                  dw[i][e + 2], dw[i][e + 3]);
+      for (int e = 0; e < V; e += 4) {
+        if (k + e >= a.kp) continue;
+        if (a.wide_part) {
+          *reinterpret_cast<float4*>(part + k + e) =
+              make_float4(dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]);
+        } else {
+#pragma unroll
+          for (int f = e; f < e + 4; ++f)
+            if (k + f < a.kp) part[k + f] = dw[i][f];
+        }
+      }
     }
   }
 }

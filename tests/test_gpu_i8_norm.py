@@ -167,13 +167,16 @@ def test_rms_grad(M, K, dtype, extra):
     check_grad(got, h, w, dy, dh, 1e-5)
     dx, dw = gq.rms_i8_grad(h, w, dy, eps=1e-5)
     check_grad((dx, dw), h, w, dy, None, 1e-5)
-    # without dw: the same dx; and in the place of either gradient
+    # without dw: the same dx; and in the place of each of the three
     dx2, none = gq.rms_i8_grad(h, w, dy, eps=1e-5, weight_grad=False)
     assert none is None and torch.equal(dx2, dx)
     for where in (0, 1):
         a = [dy.clone(), dh.clone()]
         dx3, dw3 = gq.rms_i8_grad(h, w, a[0], dh=a[1], eps=1e-5, out=a[where])
         assert torch.equal(dx3, got[0]) and torch.equal(dw3, got[1])
+    c = h.clone()
+    dx3, dw3 = gq.rms_i8_grad(c, w, dy, dh=dh, eps=1e-5, out=c)
+    assert torch.equal(dx3, got[0]) and torch.equal(dw3, got[1])
 
 
 @pytest.mark.parametrize("eps", [0.0, 1e-6, 0.5])

@@ -24,13 +24,13 @@ RMS = dict(type=1, X=A, ldx=100, R=A, ldr=100, H=B, ldh=100, w=A, eps=1e-6, Q=A,
 RGRAD = dict(type=1, H=A, ldh=100, w=A, eps=1e-6, dY=A, lddy=100, dH=A, lddh=100, dX=B, lddx=100,
              dw=A, M=40, K=100, ws=A, bytes=1 << 40)
 GEMM = dict(W=A, ldw=112, sw=A, Xq=A, ldq=112, sx=A, bias=A, act=1, R=A, ldr=50, ytype=0, Y=B,
-            ldy=50, Z=B, ldz=50, M=4, N=50, K=100)
+            ldy=50, Z=2 * B, ldz=50, M=4, N=50, K=100)
 LINEAR = dict(W=A, ldw=112, sw=A, xtype=1, X=A, ldx=100, Xq=A, ldq=112, sx=A, bias=A, act=1, R=A,
-              ldr=50, ytype=2, Y=B, ldy=50, Z=B, ldz=50, M=4, N=50, K=100)
+              ldr=50, ytype=2, Y=B, ldy=50, Z=2 * B, ldz=50, M=4, N=50, K=100)
 GATE = dict(W=A, ldw=112, sw=A, Wu=A, ldwu=112, swu=A, Xq=A, ldq=112, sx=A, bias=A, biasu=A, act=1,
-            ytype=0, Y=B, ldy=50, Z=B, ldz=50, U=B, ldu=50, M=4, N=50, K=100)
+            ytype=0, Y=B, ldy=50, Z=2 * B, ldz=50, U=3 * B, ldu=50, M=4, N=50, K=100)
 LGATE = dict(W=A, ldw=112, sw=A, Wu=A, ldwu=112, swu=A, xtype=1, X=A, ldx=100, Xq=A, ldq=112, sx=A,
-             bias=A, biasu=A, act=1, ytype=2, Y=B, ldy=50, Z=B, ldz=50, U=B, ldu=50, M=4, N=50,
+             bias=A, biasu=A, act=1, ytype=2, Y=B, ldy=50, Z=2 * B, ldz=50, U=3 * B, ldu=50, M=4, N=50,
              K=100)
 AGRAD = dict(act=1, type=1, Z=A, ldz=50, U=A, ldu=50, dY=A, lddy=50, dZ=B, lddz=50, dU=2 * B,
              lddu=50, db=A, dbu=3 * B, M=40, N=50, ws=A, bytes=1 << 40)
@@ -66,8 +66,12 @@ VECTORS = {"rms_i8": [("w", False), ("s", False)], "rms_i8_grad": [("w", False),
                       ("u", False), ("token", False), ("logprob", True)]}
 OWN = {"rms_i8": [(dict(H=A, ldh=104, R=B), INVALID),            # X, but not as X lies
                   (dict(H=B, ldh=104, R=B), INVALID)],
-       "rms_i8_grad": [(dict(dX=A, lddx=104, dH=B), INVALID), (dict(dX=B, lddx=104, dH=B), INVALID)],
-       "gemm_i8_act": [(dict(R=B, ldr=52), INVALID)], "linear_i8_act": [(dict(R=B, ldr=52), INVALID)],
+       "rms_i8_grad": [(dict(dX=A, lddx=104, dH=B), INVALID), (dict(dX=B, lddx=104, dH=B), INVALID),
+                       (dict(dX=B, lddx=104, H=B), INVALID)],
+       "gemm_i8_act": [(dict(R=B, ldr=52), INVALID), (dict(Z=B), INVALID), (dict(Z=A), INVALID)],
+       "linear_i8_act": [(dict(R=B, ldr=52), INVALID), (dict(Z=B), INVALID), (dict(Z=A), INVALID)],
+       "gemm_i8_gate": [(dict(Z=B), INVALID), (dict(U=B), INVALID), (dict(U=2 * B), INVALID)],
+       "linear_i8_gate": [(dict(Z=B), INVALID), (dict(U=B), INVALID), (dict(U=2 * B), INVALID)],
        "sample": [(dict(N=0), SHAPE), (dict(token=A + 4), ALIGN)],
        "act_grad": [(dict(U=None), INVALID), (dict(dU=None), INVALID), (dict(dbu=A), INVALID),
                     (dict(U=None, dU=None), INVALID),   # a dbu without a pair
