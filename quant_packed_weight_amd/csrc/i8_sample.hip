@@ -168,7 +168,7 @@ struct Row {
   __device__ bool exact() const { return l.k == 0 && l.p >= 1.0; }
 };
 
-// places from lo to below hi, some of them none
+// places that are lo at least and not at hi (a NaN: without an end), some of them none
 struct Ranges {
   float lo[4], hi[4];
   bool one;  // from the first place on
@@ -185,15 +185,17 @@ __device__ __forceinline__ RowAndRanges* rows_of(const SampleArgs& a) {
 __device__ __forceinline__ double log2_weight(const Row& r, float z) {
   return ((double)z - (double)r.top) * r.rate;
 }
-// the distance from the largest logit in bins (0 <= , infinite where z is -inf), which never
-// rises with z, and for z >= r.floor the bin: the last one holds all that lies behind it too
+// the distance from the largest logit in bins (0 <= ; infinite, or with a scale of 0 NaN, where
+// z is -inf), which never rises with z, and for z >= r.floor the bin: the last one holds all that
+// lies behind it too
 __device__ __forceinline__ float place_of(const Row& r, float z) { return (r.top - z) * r.scale; }
 __device__ __forceinline__ int bin_of(const Row& r, float z) {
   return (int)fminf(place_of(r, z), (float)(kBins - 1));
 }
-// places of bins lo .. hi: from first(lo) to below past(hi)
+// places of bins lo .. hi: from lo to below past(hi), which for the last is a NaN: no place is
+// behind it, nor is an infinite one, of a distance past f32
 __device__ __forceinline__ float past(int hi) {
-  return hi == kBins - 1 ? __builtin_inff() : (float)(hi + 1);
+  return hi == kBins - 1 ? __builtin_nanf("") : (float)(hi + 1);
 }
 
 __device__ __forceinline__ void join(SamplePart& s, const SamplePart& o) {
@@ -549,8 +551,12 @@ __global__ __launch_bounds__(kDraw) void plan_kernel(SampleArgs a) {
 template <class P, class Take>
 __device__ __forceinline__ void select(const P& part, const Row& r, const Ranges& g, Take take) {
   constexpr int V = P::V;
-  const float far = fmaxf(fmaxf(g.hi[0], g.hi[1]), fmaxf(g.hi[2], g.hi[3]));
-  if (g.one && far < __builtin_inff()) {
+  // what lies below the floor has places from about kBins on, or where all else is equal the
+  // same one as that
+  const float ends = g.hi[0] + g.hi[1] + g.hi[2] + g.hi[3];
+  const bool apart = ends == ends && r.scale > 0.0f;
+  if (g.one && apart) {
+    const float far = g.hi[0];
     part.pieces([&](const float(&v)[V], int n) {
       uint32_t mask = 0;
 #pragma unroll
@@ -559,8 +565,6 @@ __device__ __forceinline__ void select(const P& part, const Row& r, const Ranges
     });
     return;
   }
-  // what lies below the floor has places from about kBins on
-  const float floor = far < __builtin_inff() ? -__builtin_inff() : r.floor;
   part.pieces([&](const float(&v)[V], int n) {
     float x[V];
     uint32_t mask = 0;
@@ -568,13 +572,13 @@ __device__ __forceinline__ void select(const P& part, const Row& r, const Ranges
     for (int e = 0; e < V; ++e) x[e] = place_of(r, v[e]);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (g.lo[i] < g.hi[i]) {  // the same in all lanes
+      if (!(g.lo[i] >= g.hi[i])) {  // the same in all lanes
 #pragma unroll
-        for (int e = 0; e < V; ++e) mask |= x[e] >= g.lo[i] && x[e] < g.hi[i] ? 1u << e : 0u;
+        for (int e = 0; e < V; ++e) mask |= x[e] >= g.lo[i] && !(x[e] >= g.hi[i]) ? 1u << e : 0u;
       }
-    if (floor > -__builtin_inff()) {
+    if (!apart) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) mask &= v[e] >= floor ? ~0u : ~(1u << e);
+      for (int e = 0; e < V; ++e) mask &= v[e] >= r.floor ? ~0u : ~(1u << e);
     }
     if (mask) take(v, n, mask);
   });

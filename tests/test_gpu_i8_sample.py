@@ -240,6 +240,21 @@ def test_settings_at_their_ends():
         check(z, col("u", f), col("t", f), col("k", torch.int32), col("p", f), col("q", f))
 
 
+@pytest.mark.parametrize("N", [3000, 50000])
+@pytest.mark.parametrize("t,scale", [(1e-9, 5.0), (1e-7, 5.0), (1e37, 1e38), (1e38, 1e38), (3e38, 1.5e38)])
+def test_temperatures_next_to_the_logits_ends(N, t, scale):
+    # differences past f32, and a range of weights below a step of the largest logit
+    g = gen(N)
+    rows = [(k, p, q) for k in (0, 1, 3, 50, 2500) for p in (1.0, 0.7) for q in (0.0, 0.1)]
+    M = len(rows)
+    z = (torch.randn((M, N), generator=g, device="cuda") * scale).clamp(-3.4e38, 3.4e38)
+    z[1::2] = torch.where(z[1::2] > 2 * scale, 2 * scale, z[1::2])  # equal ones at the top
+    z[::3, ::7] = -math.inf
+    u = torch.rand(M, generator=g, device="cuda")
+    k, p, q = (torch.tensor(c, device="cuda") for c in zip(*rows))
+    check(z, u, torch.full((M,), t, device="cuda"), k.int(), p, q)
+
+
 def test_rows_that_cannot_be_drawn_from():
     g = gen(6)
     z = torch.randn((9, 5000), generator=g, device="cuda")
