@@ -197,22 +197,39 @@ __device__ __forceinline__ float quantized(float x, float s, float inv) {
   return __builtin_amdgcn_fmed3f(q, -127.0f, 127.0f);
 }
 
+// 16 bytes, with ONCE as those of a stream that nothing reads or writes again soon
+template <bool ONCE>
+__device__ __forceinline__ uint4 load_line(const void* p) {
+  typedef uint32_t Line __attribute__((ext_vector_type(4)));
+  if constexpr (!ONCE) return *static_cast<const uint4*>(p);
+  const Line v = __builtin_nontemporal_load(static_cast<const Line*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool ONCE>
+__device__ __forceinline__ void store_line(void* p, uint4 w) {
+  typedef uint32_t Line __attribute__((ext_vector_type(4)));
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(Line{w.x, w.y, w.z, w.w}, static_cast<Line*>(p));
+  else
+    *static_cast<uint4*>(p) = w;
+}
+
 // 16 bytes of a row from element i, zero from element `end` of the row on (`left`
 // values are left before it); at once where the row allows 16-byte loads and all
 // are there
-template <int TYPE>
+template <int TYPE, bool ONCE = false>
 __device__ __forceinline__ uint4 load_raw(const void* p, int64_t i, int64_t left, bool wide) {
   constexpr int V = TYPE == GEMMQ_F32 ? 4 : 8;
   uint32_t u[4] = {0, 0, 0, 0};
   if constexpr (TYPE == GEMMQ_F32) {
     const uint32_t* x = static_cast<const uint32_t*>(p) + i;
-    if (wide && left >= V) return *reinterpret_cast<const uint4*>(x);
+    if (wide && left >= V) return load_line<ONCE>(x);
 #pragma unroll
     for (int e = 0; e < V; ++e)
       if (e < left) u[e] = x[e];
   } else {
     const uint16_t* x = static_cast<const uint16_t*>(p) + i;
-    if (wide && left >= V) return *reinterpret_cast<const uint4*>(x);
+    if (wide && left >= V) return load_line<ONCE>(x);
 #pragma unroll
     for (int e = 0; e < V; ++e)
       if (e < left) u[e >> 1] |= (uint32_t)x[e] << (16 * (e & 1));
@@ -265,14 +282,14 @@ __device__ __forceinline__ uint4 pack(const float (&v)[V]) {
 }
 
 // 16 bytes to a row from element i on, those of its first `left` values
-template <int TYPE>
+template <int TYPE, bool ONCE = false>
 __device__ __forceinline__ void store_raw(void* p, int64_t i, int left, bool wide, uint4 w) {
   constexpr int V = kValues<TYPE>;
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   if constexpr (TYPE == GEMMQ_F32) {
     uint32_t* to = static_cast<uint32_t*>(p) + i;
     if (wide && left >= V) {
-      *reinterpret_cast<uint4*>(to) = w;
+      store_line<ONCE>(to, w);
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e)
@@ -281,7 +298,7 @@ __device__ __forceinline__ void store_raw(void* p, int64_t i, int left, bool wid
   } else {
     uint16_t* to = static_cast<uint16_t*>(p) + i;
     if (wide && left >= V) {
-      *reinterpret_cast<uint4*>(to) = w;
+      store_line<ONCE>(to, w);
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e)

@@ -12,6 +12,34 @@ namespace gemmq {
 namespace i8 {
 namespace {
 
+// Of a row, h and what is read to make it, and in the gradient h (which the forward pass left
+// long ago) and dx, are accessed as streams (ONCE) that the L2 need not keep; dy and dh come
+// from the calls just before.  Out of memory, in bf16, that takes the norm of 2048 x 4096 from
+// 17.6 to 14.8 us and of 8192 x 4096 from 53 to 46, the gradient from 21.6 to 20.8 and from 57.5
+// to 54.6 (dy and dh as streams too 52.8; but 18 instead of 16 where they are in the caches).
+// In a decoder block whose products follow at once there is no difference either way.
+
+// a thread's 16 bytes of a piece of SPAN values from element `first` of a row on
+template <int TYPE, int SPAN, bool ONCE>
+__device__ __forceinline__ uint4 load_piece(const void* p, int64_t row, int first, int t, int K,
+                                            bool wide) {
+  constexpr int V = kValues<TYPE>;
+  const int k = first + V * t;
+  if (wide && first + SPAN <= K)  // the same way in all lanes
+    return load_raw<TYPE, ONCE>(p, row + k, V, true);
+  return load_raw<TYPE, ONCE>(p, row + k, K - k, wide);
+}
+template <int TYPE, int SPAN, bool ONCE>
+__device__ __forceinline__ void store_piece(void* p, int64_t row, int first, int t, int K,
+                                            bool wide, uint4 w) {
+  constexpr int V = kValues<TYPE>;
+  const int k = first + V * t;
+  if (wide && first + SPAN <= K)
+    store_raw<TYPE, ONCE>(p, row + k, V, true, w);
+  else
+    store_raw<TYPE, ONCE>(p, row + k, K - k, wide, w);
+}
+
 // V values of an f32 vector from element k on, zero from element `end` on
 template <int V>
 __device__ __forceinline__ void load_vector(const float* w, int k, int end, bool wide,
@@ -39,10 +67,9 @@ __global__ __launch_bounds__(T) void rms_kernel(RmsArgs a) {
   auto load = [&](int64_t m) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const int k = kSpan * i + V * t;
       if (kSpan * i < K) {
-        x[i] = load_raw<TYPE>(a.X, m * a.ldx + k, K - k, a.wide_x);
-        if (a.R) r[i] = load_raw<TYPE>(a.R, m * a.ldr + k, K - k, a.wide_r);
+        x[i] = load_piece<TYPE, kSpan, true>(a.X, m * a.ldx, kSpan * i, t, K, a.wide_x);
+        if (a.R) r[i] = load_piece<TYPE, kSpan, true>(a.R, m * a.ldr, kSpan * i, t, K, a.wide_r);
       }
     }
   };
@@ -66,8 +93,8 @@ __global__ __launch_bounds__(T) void rms_kernel(RmsArgs a) {
     uint32_t top = 0;
     double ss[1] = {0.0};
     // the share of 16 bytes of h in the two statistics, and H written
-    auto take = [&](int k, uint4 h, const float(&wv)[V]) {
-      if (a.H) store_raw<TYPE>(a.H, m * a.ldh + k, K - k, a.wide_h, h);
+    auto take = [&](int first, uint4 h, const float(&wv)[V]) {
+      if (a.H) store_piece<TYPE, kSpan, (HELD > 0)>(a.H, m * a.ldh, first, t, K, a.wide_h, h);
       float v[V];
       unpack<TYPE, V>(h, v);
 #pragma unroll
@@ -84,13 +111,13 @@ __global__ __launch_bounds__(T) void rms_kernel(RmsArgs a) {
       if (m + gridDim.x < a.M) load(m + gridDim.x);
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
-        if (kSpan * i < K) take(kSpan * i + V * t, held[i], w[i]);
+        if (kSpan * i < K) take(kSpan * i, held[i], w[i]);
     } else {
       for (int k = V * t; k < K; k += kSpan) {
         const uint4 xw = load_raw<TYPE>(a.X, m * a.ldx + k, K - k, a.wide_x);
         const uint4 h = add(xw, a.R ? load_raw<TYPE>(a.R, m * a.ldr + k, K - k, a.wide_r) : xw);
         load_vector<V>(a.w, k, K, a.wide_w, w[0]);
-        take(k, h, w[0]);
+        take(k - V * t, h, w[0]);
       }
     }
     top = wave_max(top);
@@ -171,11 +198,10 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
   auto load = [&](int64_t m) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const int k = kSpan * i + V * t;
       if (kSpan * i < K) {
-        hn[i] = load_raw<TYPE>(a.H, m * a.ldh + k, K - k, a.wide_h);
-        yn[i] = load_raw<TYPE>(a.dY, m * a.lddy + k, K - k, a.wide_dy);
-        if (a.dH) dn[i] = load_raw<TYPE>(a.dH, m * a.lddh + k, K - k, a.wide_dh);
+        hn[i] = load_piece<TYPE, kSpan, true>(a.H, m * a.ldh, kSpan * i, t, K, a.wide_h);
+        yn[i] = load_piece<TYPE, kSpan, false>(a.dY, m * a.lddy, kSpan * i, t, K, a.wide_dy);
+        if (a.dH) dn[i] = load_piece<TYPE, kSpan, false>(a.dH, m * a.lddh, kSpan * i, t, K, a.wide_dh);
       }
     }
   };
@@ -213,7 +239,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
     sum_all<T>(s, sums[turn], t);
     const double r = 1.0 / sqrt(s[0] / K + (double)a.eps);
     const float rstd = (float)r, mean = (float)(s[1] * r / K);
-    auto give = [&](int k, uint4 hw, uint4 yw, uint4 dw4, const float(&wv)[V], float(&dwv)[V]) {
+    auto give = [&](int first, uint4 hw, uint4 yw, uint4 dw4, const float(&wv)[V], float(&dwv)[V]) {
       float h[V], y[V], dx[V];
       unpack<TYPE, V>(hw, h);
       unpack<TYPE, V>(yw, y);
@@ -229,12 +255,12 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) dx[e] += o[e];
       }
-      store_raw<TYPE>(a.dX, x0 + k, K - k, a.wide_dx, pack<TYPE, V>(dx));
+      store_piece<TYPE, kSpan, true>(a.dX, x0, first, t, K, a.wide_dx, pack<TYPE, V>(dx));
     };
     if constexpr (HELD > 0) {
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
-        if (kSpan * i < K) give(kSpan * i + V * t, hr[i], yr[i], dr[i], w[i], dw[DW ? i : 0]);
+        if (kSpan * i < K) give(kSpan * i, hr[i], yr[i], dr[i], w[i], dw[DW ? i : 0]);
     } else {
       for (int k = V * t; k < K; k += kSpan) {
         load_vector<V>(a.w, k, K, a.wide_w, w[0]);
@@ -244,7 +270,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
             dw[0][e] = m < gridDim.x || k + e >= a.kp ? 0.0f : part[k + e];
         }
         const uint4 h = load_raw<TYPE>(a.H, h0 + k, K - k, a.wide_h);
-        give(k, h, load_raw<TYPE>(a.dY, y0 + k, K - k, a.wide_dy),
+        give(k - V * t, h, load_raw<TYPE>(a.dY, y0 + k, K - k, a.wide_dy),
              a.dH ? load_raw<TYPE>(a.dH, d0 + k, K - k, a.wide_dh) : h, w[0], dw[0]);
         if constexpr (DW) {
 #pragma unroll
@@ -301,10 +327,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Join a, Join b, i
 // Rows in flight: four workgroups a CU (2048 x 4096 in bf16 with 512 / 1024 / 2048 workgroups
 // 18.7 / 16.0 / 17.0 us).  A row of up to 4096 16-bit values is shared by 256 threads, of more
 // by 512 (us, 512 / 256 threads: 1024 x 5120 in bf16 13.2 / 15.8, 2048 x 4096 in f32 21 / 31), of
-// f32 beyond 4096 by 1024 (1024 x 8192 26.9, by 512 29.5); of more than 16384 16-bit or 8192
-// f32 values it is read twice.
+// f32 beyond 4096 by 1024 (1024 x 8192 26.9, by 512 29.5); of more than 16384 values it is read
+// twice (2048 x 12288 in f32 held 72, read twice 90; 512 x 20480 in bf16 32 / 26).
 constexpr int kRmsGroups = 1024;
 
+// In the gradient a row's thread holds three times as much: f32 beyond 4096 by 1024 threads (us,
+// 1024 / 512: 1024 x 8192 35.4 / 42.6, 4096 x 8192 109 / 143), and of more than 8192 f32 values it
+// is read twice (2048 x 12288 155, by 1024 threads at once 158; 680 x 12288 61 / 73).
 template <int TYPE, bool DW>
 void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
   constexpr int V = kValues<TYPE>;
@@ -312,6 +341,8 @@ void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
     rms_grad_kernel<TYPE, 256, 2, DW><<<groups, 256, 0, st>>>(a);
   else if (a.K <= 512 * 2 * V)
     rms_grad_kernel<TYPE, 512, 2, DW><<<groups, 512, 0, st>>>(a);
+  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
+    rms_grad_kernel<GEMMQ_F32, 1024, 2, DW><<<groups, 1024, 0, st>>>(a);
   else if (a.K <= 512 * 4 * V)
     rms_grad_kernel<TYPE, 512, 4, DW><<<groups, 512, 0, st>>>(a);
   else
@@ -328,6 +359,8 @@ void launch_type(const RmsArgs& a, hipStream_t st) {
     rms_kernel<TYPE, 512, 2><<<g, 512, 0, st>>>(a);
   else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
     rms_kernel<GEMMQ_F32, 1024, 2><<<g, 1024, 0, st>>>(a);
+  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 4 * V)
+    rms_kernel<GEMMQ_F32, 1024, 4><<<g, 1024, 0, st>>>(a);
   else if (a.K <= 512 * 4 * V)
     rms_kernel<TYPE, 512, 4><<<g, 512, 0, st>>>(a);
   else
