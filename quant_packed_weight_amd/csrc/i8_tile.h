@@ -50,7 +50,10 @@ struct Image {
 };
 
 // rows m0 .. of results [M, N] from column n0: between memory and their image (T threads,
-// BM rows).  STORE: from the image; else to it, zero where there is nothing.
+// BM rows).  STORE: from the image; else to it, zero where there is nothing.  The stores are a
+// stream's: what the L2 holds of the operands matters more to the tiles that follow (a pair of
+// 2 x 12288 over 4096 with z and u kept, us: 128 tokens 33.7 -> 30.5, 2048 220 -> 215.5, 8192 856
+// -> 838; with the next product 65 -> 62, 352 -> 343, 1277 -> 1240).
 template <int CH, int BM, int T, bool STORE>
 __device__ __forceinline__ void move_image(uint8_t* image, const Rows& rows, int64_t m0, int64_t n0,
                                            int M, int N, int t) {
@@ -65,7 +68,7 @@ __device__ __forceinline__ void move_image(uint8_t* image, const Rows& rows, int
       uint16_t* to = p + (m0 + ml) * rows.ld + n;
       if (n + 8 <= N) {
         if constexpr (STORE)
-          *reinterpret_cast<v4i*>(to) = *in;
+          __builtin_nontemporal_store(*in, reinterpret_cast<v4i*>(to));
         else
           *in = *reinterpret_cast<const v4i*>(to);
       } else if constexpr (STORE) {
@@ -197,83 +200,83 @@ __device__ __forceinline__ void finish_act(const TileArgs& a, const v16i (&acc)[
   const Operands& op = a.op;
   const int h = lane >> 5, nw = wn * TN * 32 + 4 * h;
   const bool edge = n0 + CH > op.N;
-      const Act act = act_of(a.act.act);
-      const int type = a.act.type;
-      const bool wide16 = type != GEMMQ_F32;  // through LDS, as below
-      if (wide16 && EPI == kAct && a.act.R.p) {
-            move_image<CH, BM, T, false>(lds, a.act.R, m0, n0, op.M, op.N, t);
-        __syncthreads();
-      }
-      // what: 0 the result, 1 and 2 the products before the activation
-      auto emit = [&](int what, const Rows& rows) {
-  #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          if (group > 0) break;
-          const int ml = (wm * TM + j) * 32 + (lane & 31);
-          const int64_t m = m0 + ml;
-          if (m >= op.M) continue;
-          const float sx = op.sx[m];
-  #pragma unroll
-          for (int i = 0; i < TN; ++i) {
-            // four channels of registers 4 g .. 4 g + 3
-            auto scaled4 = [&](int g, float(&v)[4]) {
-              const int row = nw + 32 * i + 8 * g;
-              const float4 sw = *reinterpret_cast<const float4*>(swl + row);
-              const float4 b = *reinterpret_cast<const float4*>(bias + row);
-              const v16i& c = acc[i][j];
-              v[0] = fmaf((float)c[4 * g] * sx, sw.x, b.x);
-              v[1] = fmaf((float)c[4 * g + 1] * sx, sw.y, b.y);
-              v[2] = fmaf((float)c[4 * g + 2] * sx, sw.z, b.z);
-              v[3] = fmaf((float)c[4 * g + 3] * sx, sw.w, b.w);
-            };
-  #pragma unroll
-            for (int g = 0; g < 4; g += EPI == kGate ? 2 : 1) {
-              const int nl = EPI == kGate ? 16 * (wn * TN + i) + 4 * g + 4 * h : nw + 32 * i + 8 * g;
-              const int64_t n = n0 + nl;
-              const int count = edge ? (int)min((int64_t)4, op.N - n) : 4;
-              uint2* in = reinterpret_cast<uint2*>(lds + Image<CH>::at(ml, nl >> 3) + 8 * h);
-              float v[4];
-              scaled4(EPI == kGate && what == 2 ? g + 1 : g, v);
-              if (what == 0) {
-                activate(act, v);
-                float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (EPI == kGate) {
-                  scaled4(g + 1, o);
-  #pragma unroll
-                  for (int e = 0; e < 4; ++e) v[e] *= o[e];
-                } else if (a.act.R.p) {
-                  if (wide16) {
-                    const uint2 r = *in;
-                    const float2 lo = halves(r.x, type), hi = halves(r.y, type);
-                    o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
-                  } else {
-                    load4_as(a.act.R.p, m * a.act.R.ld + n, type, a.act.R.wide, count, o);
-                  }
-  #pragma unroll
-                  for (int e = 0; e < 4; ++e) v[e] += o[e];
-                }
+  const Act act = act_of(a.act.act);
+  const int type = a.act.type;
+  const bool wide16 = type != GEMMQ_F32;  // through LDS, as below
+  if (wide16 && EPI == kAct && a.act.R.p) {
+    move_image<CH, BM, T, false>(lds, a.act.R, m0, n0, op.M, op.N, t);
+    __syncthreads();
+  }
+  // what: 0 the result, 1 and 2 the products before the activation
+  auto emit = [&](int what, const Rows& rows) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      if (group > 0) break;
+      const int ml = (wm * TM + j) * 32 + (lane & 31);
+      const int64_t m = m0 + ml;
+      if (m >= op.M) continue;
+      const float sx = op.sx[m];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        // four channels of registers 4 g .. 4 g + 3
+        auto scaled4 = [&](int g, float(&v)[4]) {
+          const int row = nw + 32 * i + 8 * g;
+          const float4 sw = *reinterpret_cast<const float4*>(swl + row);
+          const float4 b = *reinterpret_cast<const float4*>(bias + row);
+          const v16i& c = acc[i][j];
+          v[0] = fmaf((float)c[4 * g] * sx, sw.x, b.x);
+          v[1] = fmaf((float)c[4 * g + 1] * sx, sw.y, b.y);
+          v[2] = fmaf((float)c[4 * g + 2] * sx, sw.z, b.z);
+          v[3] = fmaf((float)c[4 * g + 3] * sx, sw.w, b.w);
+        };
+#pragma unroll
+        for (int g = 0; g < 4; g += EPI == kGate ? 2 : 1) {
+          const int nl = EPI == kGate ? 16 * (wn * TN + i) + 4 * g + 4 * h : nw + 32 * i + 8 * g;
+          const int64_t n = n0 + nl;
+          const int count = edge ? (int)min((int64_t)4, op.N - n) : 4;
+          uint2* in = reinterpret_cast<uint2*>(lds + Image<CH>::at(ml, nl >> 3) + 8 * h);
+          float v[4];
+          scaled4(EPI == kGate && what == 2 ? g + 1 : g, v);
+          if (what == 0) {
+            activate(act, v);
+            float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (EPI == kGate) {
+              scaled4(g + 1, o);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] *= o[e];
+            } else if (a.act.R.p) {
+              if (wide16) {
+                const uint2 r = *in;
+                const float2 lo = halves(r.x, type), hi = halves(r.y, type);
+                o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
+              } else {
+                load4_as(a.act.R.p, m * a.act.R.ld + n, type, a.act.R.wide, count, o);
               }
-              if (wide16)
-                *in = make_uint2(two_bits(v[0], v[1], type), two_bits(v[2], v[3], type));
-              else
-                store4_as(rows.p, m * rows.ld + n, type, rows.wide, count, v[0], v[1], v[2], v[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += o[e];
             }
           }
+          if (wide16)
+            *in = make_uint2(two_bits(v[0], v[1], type), two_bits(v[2], v[3], type));
+          else
+            store4_as(rows.p, m * rows.ld + n, type, rows.wide, count, v[0], v[1], v[2], v[3]);
         }
-        if (wide16) {
-          __syncthreads();
-          move_image<CH, BM, T, true>(lds, rows, m0, n0, op.M, op.N, t);
-        }
-      };
-      emit(0, a.act.Y);
-      if (a.act.Z.p) {
-        if (wide16) __syncthreads();
-        emit(1, a.act.Z);
       }
-      if (EPI == kGate && a.act.U.p) {
-        if (wide16) __syncthreads();
-        emit(2, a.act.U);
-      }
+    }
+    if (wide16) {
+      __syncthreads();
+      move_image<CH, BM, T, true>(lds, rows, m0, n0, op.M, op.N, t);
+    }
+  };
+  emit(0, a.act.Y);
+  if (a.act.Z.p) {
+    if (wide16) __syncthreads();
+    emit(1, a.act.Z);
+  }
+  if (EPI == kGate && a.act.U.p) {
+    if (wide16) __syncthreads();
+    emit(2, a.act.U);
+  }
 }
 
 // GROUPS groups of WN x WM waves compute the tile, group g the steps g, g + GROUPS,
