@@ -36,7 +36,8 @@ __global__ __launch_bounds__(64 * kWaves) void act_grad_kernel(ActGradArgs a) {
     float z[V], y[V], u[V], dz[V], du[V];
     const uint4 zr = load_raw<TYPE, true>(a.Z.p, m * a.Z.ld + n, left, a.Z.lines);
     const uint4 yr = load_raw<TYPE, true>(a.dY.p, m * a.dY.ld + n, left, a.dY.lines);
-    if constexpr (PAIR) unpack<TYPE, V>(load_raw<TYPE, true>(a.U.p, m * a.U.ld + n, left, a.U.lines), u);
+    if constexpr (PAIR)
+      unpack<TYPE, V>(load_raw<TYPE, true>(a.U.p, m * a.U.ld + n, left, a.U.lines), u);
     unpack<TYPE, V>(zr, z);
     unpack<TYPE, V>(yr, y);
 #pragma unroll
@@ -104,7 +105,9 @@ int ranges(int type, int64_t M, int64_t N, int64_t most) {
 // Up to 16 rows (four a wave) go through one workgroup for each strip of columns, whose sums
 // are the gradients of the biases themselves: a launch less (N = 4096 in bf16, a call with a
 // bias's gradient 7.7 us of 16 rows, 12.2 of 17; of a gated pair with both 9.1 and 13.6).
-int act_grad_groups(int type, int64_t M, int64_t N) { return M <= 16 ? 1 : ranges(type, M, N, 1024); }
+int act_grad_groups(int type, int64_t M, int64_t N) {
+  return M <= 16 ? 1 : ranges(type, M, N, 1024);
+}
 
 int launch_act_grad(ActGradArgs a, hipStream_t st) {
   a.groups = a.sums[0] || a.sums[1] ? act_grad_groups(a.type, a.M, a.N)

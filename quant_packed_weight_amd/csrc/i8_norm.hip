@@ -19,13 +19,14 @@ namespace {
 // to 54.6 (dy and dh as streams too 52.8; but 18 instead of 16 where they are in the caches).
 // In a decoder block whose products follow at once there is no difference either way.
 
-// a thread's 16 bytes of a piece of SPAN values from element `first` of a row on
+// a thread's 16 bytes of a piece of SPAN values from element `first` of a row on (SPAN 0: not
+// asked whether all of it is there)
 template <int TYPE, int SPAN, bool ONCE>
 __device__ __forceinline__ uint4 load_piece(const void* p, int64_t row, int first, int t, int K,
                                             bool wide) {
   constexpr int V = kValues<TYPE>;
   const int k = first + V * t;
-  if (wide && first + SPAN <= K)  // the same way in all lanes
+  if (SPAN > 0 && wide && first + SPAN <= K)  // the same way in all lanes
     return load_raw<TYPE, ONCE>(p, row + k, V, true);
   return load_raw<TYPE, ONCE>(p, row + k, K - k, wide);
 }
@@ -34,7 +35,7 @@ __device__ __forceinline__ void store_piece(void* p, int64_t row, int first, int
                                             bool wide, uint4 w) {
   constexpr int V = kValues<TYPE>;
   const int k = first + V * t;
-  if (wide && first + SPAN <= K)
+  if (SPAN > 0 && wide && first + SPAN <= K)
     store_raw<TYPE, ONCE>(p, row + k, V, true, w);
   else
     store_raw<TYPE, ONCE>(p, row + k, K - k, wide, w);
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(T) void rms_kernel(RmsArgs a) {
 template <int TYPE, int T, int HELD, bool DW>
 __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
   constexpr int V = kValues<TYPE>, kSpan = T * V, kKeep = HELD > 0 ? HELD : 1;
+  constexpr int kPiece = HELD < 4 ? kSpan : 0;  // (of four, two ways to each leave registers short)
   __shared__ double sums[2][2 * T / 64];
   const int t = threadIdx.x, K = a.K;
   float* part = DW ? a.part + (int64_t)blockIdx.x * a.kp : nullptr;
@@ -199,9 +201,10 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       if (kSpan * i < K) {
-        hn[i] = load_piece<TYPE, kSpan, true>(a.H, m * a.ldh, kSpan * i, t, K, a.wide_h);
-        yn[i] = load_piece<TYPE, kSpan, false>(a.dY, m * a.lddy, kSpan * i, t, K, a.wide_dy);
-        if (a.dH) dn[i] = load_piece<TYPE, kSpan, false>(a.dH, m * a.lddh, kSpan * i, t, K, a.wide_dh);
+        hn[i] = load_piece<TYPE, kPiece, true>(a.H, m * a.ldh, kSpan * i, t, K, a.wide_h);
+        yn[i] = load_piece<TYPE, kPiece, false>(a.dY, m * a.lddy, kSpan * i, t, K, a.wide_dy);
+        if (a.dH)
+          dn[i] = load_piece<TYPE, kPiece, false>(a.dH, m * a.lddh, kSpan * i, t, K, a.wide_dh);
       }
     }
   };
@@ -255,7 +258,7 @@ __global__ __launch_bounds__(T) void rms_grad_kernel(RmsGradArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) dx[e] += o[e];
       }
-      store_piece<TYPE, kSpan, true>(a.dX, x0, first, t, K, a.wide_dx, pack<TYPE, V>(dx));
+      store_piece<TYPE, kPiece, true>(a.dX, x0, first, t, K, a.wide_dx, pack<TYPE, V>(dx));
     };
     if constexpr (HELD > 0) {
 #pragma unroll
@@ -324,12 +327,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(Join a, Join b, i
   out[k] = s;
 }
 
-// Rows in flight: four workgroups a CU (2048 x 4096 in bf16 with 512 / 1024 / 2048 workgroups
-// 18.7 / 16.0 / 17.0 us).  A row of up to 4096 16-bit values is shared by 256 threads, of more
-// by 512 (us, 512 / 256 threads: 1024 x 5120 in bf16 13.2 / 15.8, 2048 x 4096 in f32 21 / 31), of
-// f32 beyond 4096 by 1024 (1024 x 8192 26.9, by 512 29.5); of more than 16384 values it is read
-// twice (2048 x 12288 in f32 held 72, read twice 90; 512 x 20480 in bf16 32 / 26).
-constexpr int kRmsGroups = 1024;
+// Threads a row (us, out of memory): up to 4096 16-bit values 256, of more 512 (512 / 256: 1024 x
+// 5120 in bf16 13.2 / 15.8, 2048 x 4096 in f32 21 / 31), of f32 beyond 4096 1024 (1024 x 8192 26.9,
+// by 512 29.5); of more than 16384 values it is read twice (2048 x 12288 in f32 held 72, read
+// twice 90; 512 x 20480 in bf16 32 / 26).  Rows in flight: four waves a SIMD, whatever that is in
+// workgroups (half / that / twice: 2048 x 4096 in bf16 18.2 / 14.8 / 17.3; that / twice: 1024 x
+// 8192 in bf16 14.7 / 17.5, 2048 x 4096 in f32 22.1 / 23.7, 1024 x 8192 in f32 22.7 / 24.4).
+constexpr int kRmsThreads = 1024 * 256;
 
 // In the gradient a row's thread holds three times as much: f32 beyond 4096 by 1024 threads (us,
 // 1024 / 512: 1024 x 8192 35.4 / 42.6, 4096 x 8192 109 / 143), and of more than 8192 f32 values it
@@ -349,22 +353,27 @@ void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
     rms_grad_kernel<TYPE, 1024, 0, DW><<<groups, 1024, 0, st>>>(a);
 }
 
+template <int TYPE, int T, int HELD>
+void launch_rows(const RmsArgs& a, hipStream_t st) {
+  const int most = kRmsThreads / T;
+  rms_kernel<TYPE, T, HELD><<<a.M < most ? a.M : most, T, 0, st>>>(a);
+}
+
 template <int TYPE>
 void launch_type(const RmsArgs& a, hipStream_t st) {
   constexpr int V = kValues<TYPE>;
-  const uint32_t g = a.M < kRmsGroups ? a.M : kRmsGroups;
   if (a.K <= 256 * 2 * V)
-    rms_kernel<TYPE, 256, 2><<<g, 256, 0, st>>>(a);
+    launch_rows<TYPE, 256, 2>(a, st);
   else if (a.K <= 512 * 2 * V)
-    rms_kernel<TYPE, 512, 2><<<g, 512, 0, st>>>(a);
+    launch_rows<TYPE, 512, 2>(a, st);
   else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
-    rms_kernel<GEMMQ_F32, 1024, 2><<<g, 1024, 0, st>>>(a);
+    launch_rows<GEMMQ_F32, 1024, 2>(a, st);
   else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 4 * V)
-    rms_kernel<GEMMQ_F32, 1024, 4><<<g, 1024, 0, st>>>(a);
+    launch_rows<GEMMQ_F32, 1024, 4>(a, st);
   else if (a.K <= 512 * 4 * V)
-    rms_kernel<TYPE, 512, 4><<<g, 512, 0, st>>>(a);
+    launch_rows<TYPE, 512, 4>(a, st);
   else
-    rms_kernel<TYPE, 1024, 0><<<g, 1024, 0, st>>>(a);
+    launch_rows<TYPE, 1024, 0>(a, st);
 }
 
 }  // namespace
@@ -381,8 +390,8 @@ int launch_rms(const RmsArgs& a, hipStream_t st) {
 // / 19.6, 680 x 12288 27.8 / 22.6; f32, 2048 x 4096 27.9 / 31.5, 1024 x 8192 37.8 / 33.9).  Without
 // partial sums two are never slower by more than 6% (f32, 2048 x 4096 23.9 / 28.7).
 // A few short rows go through one workgroup, whose sums are dw itself: a launch less.  A call in
-// bf16 that way is 8.0 us of 2 x 4096, 8.5 of 4 x 4096, 10.0 of 2 x 12288 and 16.1 of 4 x 12288; one
-// that joins the sums of five workgroups 12.5 at any of these widths.
+// bf16 that way is 8.0 us of 2 x 4096, 8.5 of 4 x 4096, 10.0 of 2 x 12288 and 16.1 of 4 x 12288;
+// one that joins the sums of five workgroups 12.5 at any of these widths.
 int rms_grad_groups(int64_t M, int64_t K) {
   const int64_t most = M <= 4 && M * K <= 24576 ? 1 : K <= 4096 ? 512 : 256;
   return (int)(M < most ? M : most);
