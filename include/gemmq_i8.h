@@ -101,6 +101,7 @@ int gemmq_gemm_i8(const int8_t *W, int64_t ldw, const float *sw, const int8_t *X
 /*
  * The whole linear layer: quantize X into Xq and sx, then gemmq_gemm_i8 -- the
  * same bits as the two calls, for Xq, sx and Y.  N == 0 still quantizes.
+ * Y may lie in X's place: X is quantized before anything of Y is written.
  * Errors: those of the two calls; nothing is launched on an error.
  */
 int gemmq_linear_i8(const int8_t *W, int64_t ldw, const float *sw, int xtype, const void *X,
@@ -240,7 +241,8 @@ int gemmq_gemm_i8_act(const int8_t *W, int64_t ldw, const float *sw, const int8_
                       int ytype, void *Y, int64_t ldy, void *Z, int64_t ldz, int64_t M, int64_t N,
                       int64_t K, void *stream);
 
-/* Quantize X into Xq and sx, then gemmq_gemm_i8_act: the same bits as the two calls. */
+/* Quantize X into Xq and sx, then gemmq_gemm_i8_act: the same bits as the two calls, also
+   where Y or Z lies in X's place. */
 int gemmq_linear_i8_act(const int8_t *W, int64_t ldw, const float *sw, int xtype, const void *X,
                         int64_t ldx, int8_t *Xq, int64_t ldq, float *sx, const float *bias,
                         int act, const void *R, int64_t ldr, int ytype, void *Y, int64_t ldy,
@@ -262,7 +264,8 @@ int gemmq_gemm_i8_gate(const int8_t *W, int64_t ldw, const float *sw, const int8
                        void *Y, int64_t ldy, void *Z, int64_t ldz, void *U, int64_t ldu, int64_t M,
                        int64_t N, int64_t K, void *stream);
 
-/* Quantize X into Xq and sx, then gemmq_gemm_i8_gate: the same bits as the two calls. */
+/* Quantize X into Xq and sx, then gemmq_gemm_i8_gate: the same bits as the two calls, also
+   where Y, Z or U lies in X's place. */
 int gemmq_linear_i8_gate(const int8_t *W, int64_t ldw, const float *sw, const int8_t *Wu,
                          int64_t ldwu, const float *swu, int xtype, const void *X, int64_t ldx,
                          int8_t *Xq, int64_t ldq, float *sx, const float *bias, const float *biasu,

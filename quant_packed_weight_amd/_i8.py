@@ -252,7 +252,8 @@ def gemm_i8(w, sw, xq, sx, bias=None, out=None, out_dtype=None, stream=None):
 def linear_i8(w, sw, x, bias=None, out=None, out_dtype=None, xq=None, sx=None, stream=None):
     """The linear layer on activations x (f32, bf16 or f16 [M, K]): quantize per
     token, then gemm_i8 (gemmq_linear_i8).  Returns [M, N] in `out_dtype` (x's by
-    default); xq and sx, when given, receive the quantized activations."""
+    default); xq and sx, when given, receive the quantized activations.  `out` may lie
+    in x's place."""
     L = _fns or lib_i8()
     if sw.requires_grad or x.requires_grad or (bias is not None and bias.requires_grad):
         _untracked()

@@ -158,7 +158,8 @@ def gemm_i8_act(w, sw, xq, sx, act, bias=None, residual=None, pre=None, out=None
 def linear_i8_act(w, sw, x, act, bias=None, residual=None, pre=None, out=None, out_dtype=None,
                   xq=None, sx=None, stream=None):
     """gemm_i8_act on activations x (f32, bf16 or f16 [M, K]), quantized per token
-    (gemmq_linear_i8_act): [M, N] in `out_dtype` (x's by default)."""
+    (gemmq_linear_i8_act): [M, N] in `out_dtype` (x's by default).  out and pre may lie in
+    x's place."""
     _i8._fns or lib_i8()
     _tracked(sw, x, bias, residual)
     at = _elsewhere(w, w.get_device(), stream)
@@ -186,7 +187,8 @@ def gemm_i8_gate(w, sw, wu, swu, xq, sx, act=ACT_SILU, bias=None, bias_up=None, 
 def linear_i8_gate(w, sw, wu, swu, x, act=ACT_SILU, bias=None, bias_up=None, pre=None, up=None,
                    out=None, out_dtype=None, xq=None, sx=None, stream=None):
     """gemm_i8_gate on activations x (f32, bf16 or f16 [M, K]), quantized per token
-    (gemmq_linear_i8_gate): the gate and up projections of a feed-forward block."""
+    (gemmq_linear_i8_gate): the gate and up projections of a feed-forward block.  out, pre
+    and up may lie in x's place."""
     _i8._fns or lib_i8()
     _tracked(sw, swu, x, bias, bias_up)
     at = _elsewhere(w, w.get_device(), stream)

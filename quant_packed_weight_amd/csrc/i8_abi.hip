@@ -204,7 +204,8 @@ int gemmq_linear_i8(const int8_t* W, int64_t ldw, const float* sw, int xtype, co
   if (rc != GEMMQ_OK) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_pending();
-  if (N > 0 && fuses((int)M, (int)N, (int)K))
+  if (N > 0 && fuses((int)M, (int)N, (int)K) &&
+      !share_memory(span(xtype, X, ldx, K), span(ytype, Y, ldy, N), M))
     return launched(launch_fused(xtype, X, ldx, op, out, st));
   rc = launched(launch_quantize(xtype, X, ldx, Xq, ldq, sx, (int)M, (int)K, st));
   if (rc != GEMMQ_OK || N == 0) return rc;

@@ -87,6 +87,14 @@ int run_gemm(const Operands& op, const ActOut& out, bool pair, hipStream_t st) {
   return launched(launch_act(op, out, pair, st));
 }
 
+// whether a result lies in X's place
+bool in_place(int xtype, const void* X, int64_t ldx, const Operands& op, const ActOut& out) {
+  const Span x = span(xtype, X, ldx, op.K);
+  for (const Rows* r : {&out.Y, &out.Z, &out.U})
+    if (share_memory(x, span(out.type, r->p, r->ld, op.N), op.M)) return true;
+  return false;
+}
+
 // the same with the quantizer before it or in the same launch
 int run_linear(int xtype, const void* X, int64_t ldx, int8_t* Xq, int64_t ldq, float* sx, int64_t M,
                int64_t K, bool empty, const Operands& op, const ActOut& out, bool pair,
@@ -98,7 +106,7 @@ int run_linear(int xtype, const void* X, int64_t ldx, int8_t* Xq, int64_t ldq, f
   if (rc == GEMMQ_OK) rc = check_device();
   if (rc != GEMMQ_OK) return rc;
   clear_pending();
-  if (!empty && act_fuses(op.M, op.N, op.K, pair))
+  if (!empty && act_fuses(op.M, op.N, op.K, pair) && !in_place(xtype, X, ldx, op, out))
     return launched(launch_act_fused(xtype, X, ldx, op, out, pair, st));
   rc = launched(launch_quantize(xtype, X, ldx, Xq, ldq, sx, (int)M, (int)K, st));
   if (rc != GEMMQ_OK || empty) return rc;

@@ -40,6 +40,27 @@ inline int check_ws(const void* ws, size_t have, size_t need) {
   return aligned(ws, 16) ? GEMMQ_OK : GEMMQ_E_ALIGNMENT;
 }
 
+// Whether a row of one matrix shares memory with a row of the other, for the few rows of the
+// products that quantize X in their own launch: each of its workgroups reads all of X while
+// others already store results, so results in X's place need the launches apart.
+struct Span {
+  const void* p;  // null: no matrix
+  int64_t pitch, width;  // bytes
+};
+inline Span span(int type, const void* p, int64_t ld, int64_t width) {
+  return {p, ld * type_bytes(type), width * type_bytes(type)};
+}
+inline bool share_memory(const Span& a, const Span& b, int64_t M) {
+  if (!a.p || !b.p) return false;
+  for (int64_t i = 0; i < M; ++i)
+    for (int64_t j = 0; j < M; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p) + i * a.pitch;
+      const uintptr_t y = reinterpret_cast<uintptr_t>(b.p) + j * b.pitch;
+      if (x < y + b.width && y < x + a.width) return true;
+    }
+  return false;
+}
+
 inline size_t align_up(int64_t v, int64_t a) { return (size_t)((v + a - 1) / a * a); }
 
 }  // namespace i8

@@ -213,6 +213,55 @@ def test_linear_is_quantize_then_gemm(M, N, K, xt, yt):
     assert gq.linear_i8_gate(w, sw, wu, swu, x).dtype == xt
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 512, 512), (2, 640, 640), (3, 640, 640), (40, 512, 512),
+                                   (1, 40000, 1024), (2, 16000, 1000), (1, 1000, 16384)])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_results_in_the_place_of_x(M, N, K, dtype):
+    # x, and a result in the same memory: all of it, its beginning, or around it; with one and
+    # two rows, where the quantizer is in the product's launch otherwise, as with more
+    g = gen(M + N + K)
+    w, sw, wu, swu = i8(N, K, g), scales(N, g, 0.01), i8(N, K, g), scales(N, g, 0.01)
+    x, r = normal(M, K, g, dtype), normal(M, N, g, dtype)
+    width = max(N, K)
+
+    def held(v):  # v and the place of a result, from the same address on
+        b = torch.zeros((M, width), dtype=dtype, device="cuda")
+        b[:, :v.shape[1]] = v
+        return b[:, :K], b[:, :N]
+
+    ref = gq.linear_i8(w, sw, x)
+    a, out = held(x)
+    assert torch.equal(gq.linear_i8(w, sw, a, out=out), ref)
+    pre, up = torch.empty((M, N), dtype=dtype, device="cuda"), torch.empty((M, N), dtype=dtype, device="cuda")
+    ref = gq.linear_i8_act(w, sw, x, gq.ACT_SILU, residual=r, pre=pre)
+    a, out = held(x)
+    assert torch.equal(gq.linear_i8_act(w, sw, a, gq.ACT_SILU, residual=r, out=out), ref)
+    a, out = held(x)
+    assert torch.equal(gq.linear_i8_act(w, sw, a, gq.ACT_SILU, residual=r, pre=out), ref)
+    assert torch.equal(out, pre)
+    if N == K:  # x, the residual and the result in one place
+        ref = gq.linear_i8_act(w, sw, x, gq.ACT_NONE, residual=x)
+        a, out = held(x)
+        assert torch.equal(gq.linear_i8_act(w, sw, a, gq.ACT_NONE, residual=a, out=a), ref)
+    ref = gq.linear_i8_gate(w, sw, wu, swu, x, pre=pre, up=up)
+    for name, want in (("out", ref), ("pre", pre), ("up", up)):
+        a, out = held(x)
+        assert torch.equal(gq.linear_i8_gate(w, sw, wu, swu, a, **{name: out}), ref)
+        assert torch.equal(out, want), name
+    # a result of another type whose second row begins inside x
+    if dtype == torch.float32:
+        b = torch.zeros(M * width + 8 * N, device="cuda")
+        a = b[:M * K].view(M, K).copy_(x)
+        out = b.view(torch.bfloat16)[K:K + M * N].view(M, N)
+        assert torch.equal(gq.linear_i8_act(w, sw, a, gq.ACT_GELU, out=out),
+                           gq.linear_i8_act(w, sw, x, gq.ACT_GELU, out_dtype=torch.bfloat16))
+    # side by side in one buffer they share nothing
+    b = torch.zeros((M, K + N), dtype=dtype, device="cuda")
+    b[:, :K] = x
+    assert torch.equal(gq.linear_i8_act(w, sw, b[:, :K], gq.ACT_NONE, out=b[:, K:]), gq.linear_i8(w, sw, x))
+    assert torch.equal(b[:, :K], x)
+
+
 def test_without_an_activation_it_is_the_plain_product():
     g = gen(9)
     for M, N, K in ((1, 300, 500), (9, 300, 500), (200, 300, 500)):
