@@ -212,6 +212,8 @@ size_t gemmq_rms_i8_grad_workspace(int type, int64_t M, int64_t K);
  *   dX    may be H, dY or dH itself (the same pointer and pitch).
  *   dw    f32 [K], overwritten (zeros where M == 0), or NULL: not computed.
  *   ws    may be NULL where dw is.
+ * A row of zeros has rstd = 0 where eps is 0, as it has s = 0 in gemmq_rms_i8: dX is dH, or 0,
+ * and dw has nothing of it.
  * Errors: as gemmq_rms_i8, and GEMMQ_E_INVALID_ARG for a workspace that is too small.
  */
 int gemmq_rms_i8_grad(int type, const void *H, int64_t ldh, const float *w, float eps,

@@ -219,6 +219,32 @@ def test_rms_grad_special_rows():
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,K", [(3, 500), (40, 500), (6, 5000), (5, 12288), (5, 20000)])
+def test_rms_grad_without_eps(M, K, dtype):
+    # a row of zeros is finite forward (scale 0), and takes nothing from the other rows back
+    g = gen(M + K)
+    w = torch.randn(K, generator=g, device="cuda")
+    h, dy = normal(M, K, g, dtype, 2), normal(M, K, g, dtype, 0.3)
+    dh = normal(M, K, g, dtype, 0.2)
+    h[1], h[M - 1] = 0, -0.0
+    kept = torch.tensor([m for m in range(M) if m not in (1, M - 1)], device="cuda")
+    for add in (None, dh):
+        dx, dw = gq.rms_i8_grad(h, w, dy, dh=add, eps=0.0)
+        check_grad((dx[kept], dw), h[kept], w, dy[kept], None if add is None else add[kept], 0.0)
+        for m in (1, M - 1):
+            assert torch.equal(dx[m], torch.zeros_like(dx[m]) if add is None else add[m])
+        assert torch.equal(gq.rms_i8_grad(h, w, dy, dh=add, eps=0.0, weight_grad=False)[0], dx)
+    if dtype == torch.float16:
+        return
+    # a row of subnormal values: 1 / rms is past f32, dx is not; dw has the row as any other
+    h[1], dy[1] = normal(1, K, g, dtype)[0] * 1e-40, normal(1, K, g, dtype)[0] * 1e-5
+    h[M - 1, 7] = 1e-40
+    dy[M - 1] = 0
+    assert bool(h[1].any()) and bool(h[M - 1].any())
+    check_grad(gq.rms_i8_grad(h, w, dy, eps=0.0), h, w, dy, None, 0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_rms_many_rows(dtype):
     # more rows than a grid dimension of 32768 takes, and not a multiple of it
     g = gen(13)
