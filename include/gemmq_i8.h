@@ -221,7 +221,7 @@ int gemmq_rms_i8_grad(int type, const void *H, int64_t ldh, const float *w, floa
                       int64_t lddx, float *dw, int64_t M, int64_t K, void *ws, size_t ws_bytes,
                       void *stream);
 
-/* The activations, act(z). */
+/* The activations, act(z); at an infinite z act and act' are their limits. */
 #define GEMMQ_ACT_NONE 0
 #define GEMMQ_ACT_SILU 1      /* z / (1 + exp(-z)) */
 #define GEMMQ_ACT_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2 */

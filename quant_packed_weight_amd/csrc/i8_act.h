@@ -1,6 +1,8 @@
 // i8_act.h -- the activations (GEMMQ_ACT_*) on the device.
 #pragma once
 
+#include <float.h>
+
 #include "i8_block.h"
 #include "i8_common.h"
 
@@ -40,18 +42,23 @@ __device__ __forceinline__ float normal_of(float z) {
   return fmaf(0.5f, erff(z * 0.7071067811865476f), 0.5f);
 }
 
+// At an infinite z (a sum past f32, or z kept in f16, which ends at 65504) act and its slope are
+// their limits: the factor z of sigma(z) = 0 is held at the lowest f32, where 0 * infinity would
+// come up.  A NaN is kept by the other factor.
+__device__ __forceinline__ float above_lowest(float z) { return fmaxf(z, -FLT_MAX); }
+
 // act(z) for each of z[0..N)
 template <int N>
 __device__ __forceinline__ void activate(const Act& a, float (&z)[N]) {
   if (a.form == Act::kSilu) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) z[e] *= sigmoid(z[e]);
+    for (int e = 0; e < N; ++e) z[e] = above_lowest(z[e]) * sigmoid(z[e]);
   } else if (a.form == Act::kSigmoid) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) z[e] *= sigmoid_of(a, z[e]);
+    for (int e = 0; e < N; ++e) z[e] = above_lowest(z[e]) * sigmoid_of(a, z[e]);
   } else if (a.form == Act::kErf) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) z[e] *= normal_of(z[e]);
+    for (int e = 0; e < N; ++e) z[e] = above_lowest(z[e]) * normal_of(z[e]);
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) z[e] = z[e] < a.c0 ? a.c0 : z[e];
@@ -63,13 +70,13 @@ __device__ __forceinline__ void activate(const Act& a, float (&z)[N]) {
 __device__ __forceinline__ void activate_slope(const Act& a, float z, float& value, float& slope) {
   if (a.form == Act::kSilu || a.form == Act::kSigmoid) {
     const float p = sigmoid_of(a, z);
-    value = z * p;
-    slope = fmaf(value * (1.0f - p), fmaf(3.0f * a.c1, fminf(z * z, 1e30f), a.c0), p);
+    value = above_lowest(z) * p;
+    slope = fmaf(fminf(value, FLT_MAX) * (1.0f - p), fmaf(3.0f * a.c1, fminf(z * z, 1e30f), a.c0), p);
   } else if (a.form == Act::kErf) {
     const float p = normal_of(z);
     const float density = 0.3989422804014327f * __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
-    value = z * p;
-    slope = fmaf(z, density, p);
+    value = above_lowest(z) * p;
+    slope = fmaf(fminf(above_lowest(z), FLT_MAX), density, p);
   } else {
     value = z < a.c0 ? a.c0 : z;
     slope = a.c0 == 0.0f && z <= 0.0f ? 0.0f : 1.0f;

@@ -180,6 +180,57 @@ def test_far_and_special_values(act, M):
     assert torch.equal(y2[1:].nan_to_num(), y3[1:].nan_to_num())
 
 
+LIMITS = {gq.ACT_NONE: (math.inf, -math.inf, 1.0, 1.0), gq.ACT_RELU: (math.inf, 0.0, 1.0, 0.0),
+          **{a: (math.inf, 0.0, 1.0, 0.0) for a in (gq.ACT_SILU, gq.ACT_GELU, gq.ACT_GELU_TANH)}}
+
+
+@pytest.mark.parametrize("act", ACTS, ids=NAMES)
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_infinite_arguments(act, dtype):
+    # at +inf and -inf: act and its slope are their limits; a NaN stays one
+    high, low, up, down = LIMITS[act]
+    N = 40
+    bias = torch.zeros(N, device="cuda")
+    bias[0::4], bias[1::4], bias[2::4] = math.inf, -math.inf, math.nan
+    want = torch.zeros(N, device="cuda")
+    want[0::4], want[1::4], want[2::4] = high, low, math.nan
+    w, sw = torch.zeros((N, 32), dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda")
+    for M in (1, 40):
+        xq, sx = torch.zeros((M, 32), dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda")
+        pre = torch.empty((M, N), dtype=dtype, device="cuda")
+        y = gq.gemm_i8_act(w, sw, xq, sx, act, bias=bias, pre=pre, out_dtype=dtype)
+        same = lambda a, b: torch.equal(a.float().nan_to_num(7.0, 8.0, 9.0), b.expand(a.shape).nan_to_num(7.0, 8.0, 9.0))  # noqa: E731,E501
+        assert same(y, want) and same(pre, bias)
+        two = torch.full((N,), 2.0, device="cuda")
+        y = gq.gemm_i8_gate(w, sw, w, sw, xq, sx, act, bias=bias, bias_up=two, out_dtype=dtype)
+        assert same(y, 2 * want)
+        # the gradients from the z that was kept
+        dy = torch.full((M, N), 3.0, dtype=dtype, device="cuda")
+        slope = torch.zeros(N, device="cuda")
+        slope[0::4], slope[1::4] = up, down
+        at = [n for n in range(N) if n % 4 < 2]
+        dz, _ = gq.act_grad(act, pre, dy)
+        assert torch.equal(dz[:, at].float(), (3 * slope[at]).expand(M, -1))
+        if act in (gq.ACT_SILU, gq.ACT_GELU, gq.ACT_GELU_TANH):
+            assert bool(torch.isnan(dz[:, 2::4]).all())
+        dz, du = gq.act_grad(act, pre, dy, up=torch.full_like(dy, 2.0))
+        assert torch.equal(dz[:, at].float(), (6 * slope[at]).expand(M, -1))
+        assert same(du, 3 * want)
+
+
+@pytest.mark.parametrize("act", ACTS, ids=NAMES)
+def test_kept_products_past_f16(act):
+    # z of 10^5 is kept in f16 as an infinity: the slope is that of a large z, 1 or 0
+    w = torch.tensor([[100], [-100]], dtype=torch.int8, device="cuda").repeat(1, 16)
+    sw, xq = torch.ones(2, device="cuda"), torch.full((3, 16), 100, dtype=torch.int8, device="cuda")
+    sx, pre = torch.ones(3, device="cuda"), torch.empty((3, 2), dtype=torch.float16, device="cuda")
+    gq.gemm_i8_act(w, sw, xq, sx, act, pre=pre, out_dtype=torch.float16)
+    assert bool(torch.isinf(pre).all())
+    dz, du = gq.act_grad(act, pre, torch.ones_like(pre), up=torch.ones_like(pre))
+    assert dz.tolist() == [list(LIMITS[act][2:])] * 3
+    assert du.tolist() == [list(LIMITS[act][:2])] * 3
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (1, 100, 77), (2, 64, 4096), (5, 321, 333),
                                    (16, 256, 12288), (33, 100, 512), (300, 512, 640), (1, 9000, 100),
                                    (1, 40000, 515), (1, 64, 16384), (1, 64, 16400), (2, 10000, 257),
