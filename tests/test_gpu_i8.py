@@ -91,6 +91,25 @@ def test_quantize(M, K, dtype, extra):
     assert torch.equal(q2, q) and torch.equal(s2, s)
 
 
+# rows by 256 and by 512 threads, on both sides of where the one gives way to the other
+@pytest.mark.parametrize("M", [767, 768, 1024, 1025, 2048, 2049])
+@pytest.mark.parametrize("dtype,K", [(torch.float32, K) for K in (1024, 1025, 3071, 3073, 4096, 4097)]
+                         + [(t, K) for t in TYPES[1:] for K in (2048, 2049, 6144, 6145, 8193)])
+@pytest.mark.parametrize("extra", [0, 3])
+def test_quantize_many_rows(M, K, dtype, extra):
+    g = gen(M + K)
+    x = torch.zeros((M, K + extra), dtype=dtype, device="cuda")[:, :K]
+    x.copy_(torch.randn((M, K), generator=g, device="cuda"))
+    out = Guarded(M, K, torch.int8, extra=(-K) % 16 + 16)
+    q, s = gq.quantize_i8(x, out=out.t)
+    torch.cuda.synchronize()
+    out.check()
+    xd = x.double()
+    sr = (xd.abs().amax(1) / 127).float()
+    assert torch.equal(s, sr)
+    assert torch.equal(q.float(), (xd / sr.double()[:, None]).float().round().clamp(-127, 127))
+
+
 def test_quantize_ties():
     # values on and one step beside the ties between two integers, at scales of all
     # sizes: the rounded quotient decides
