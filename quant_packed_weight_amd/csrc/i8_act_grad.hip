@@ -91,8 +91,8 @@ int launch_type(const ActGradArgs& a, hipStream_t st) {
   return 0;
 }
 
-// ranges of rows: enough workgroups to fill the chip several times, of eight rows at least
-// where that leaves enough
+// ranges of rows: enough workgroups to fill the chip several times, but no more than a quarter
+// of the rows (rounded up): a row for each wave
 int ranges(int type, int64_t M, int64_t N, int64_t most) {
   const int64_t strips = ceil_div(N, type == GEMMQ_F32 ? 256 : 512);
   int64_t g = ceil_div(most, strips);

@@ -352,12 +352,12 @@ void launch_grad(const RmsGradArgs& a, int groups, hipStream_t st) {
     rms_grad_kernel<TYPE, 256, 2, DW, BARE><<<groups, 256, 0, st>>>(a);
   else if (a.K <= 512 * 2 * V)
     rms_grad_kernel<TYPE, 512, 2, DW, BARE><<<groups, 512, 0, st>>>(a);
-  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
-    rms_grad_kernel<GEMMQ_F32, 1024, 2, DW, BARE><<<groups, 1024, 0, st>>>(a);
-  else if (a.K <= 512 * 4 * V)
-    rms_grad_kernel<TYPE, 512, 4, DW, BARE><<<groups, 512, 0, st>>>(a);
-  else
+  else if (a.K > (TYPE == GEMMQ_F32 ? 1024 * 2 * V : 512 * 4 * V))
     rms_grad_kernel<TYPE, 1024, 0, DW, BARE><<<groups, 1024, 0, st>>>(a);
+  else if constexpr (TYPE == GEMMQ_F32)
+    rms_grad_kernel<TYPE, 1024, 2, DW, BARE><<<groups, 1024, 0, st>>>(a);
+  else
+    rms_grad_kernel<TYPE, 512, 4, DW, BARE><<<groups, 512, 0, st>>>(a);
 }
 
 template <int TYPE>
@@ -382,14 +382,14 @@ void launch_type(const RmsArgs& a, hipStream_t st) {
     launch_rows<TYPE, 256, 2>(a, st);
   else if (a.K <= 512 * 2 * V)
     launch_rows<TYPE, 512, 2>(a, st);
-  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 2 * V)
-    launch_rows<GEMMQ_F32, 1024, 2>(a, st);
-  else if (TYPE == GEMMQ_F32 && a.K <= 1024 * 4 * V)
-    launch_rows<GEMMQ_F32, 1024, 4>(a, st);
-  else if (a.K <= 512 * 4 * V)
-    launch_rows<TYPE, 512, 4>(a, st);
-  else
+  else if (a.K > 16384)
     launch_rows<TYPE, 1024, 0>(a, st);
+  else if constexpr (TYPE != GEMMQ_F32)
+    launch_rows<TYPE, 512, 4>(a, st);
+  else if (a.K <= 1024 * 2 * V)
+    launch_rows<TYPE, 1024, 2>(a, st);
+  else
+    launch_rows<TYPE, 1024, 4>(a, st);
 }
 
 }  // namespace
