@@ -393,6 +393,24 @@ def test_act_grad(M, N, dtype, act):
             assert torch.equal(one, dbu)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N", [(1, 40), (5, 513), (16, 40), (17, 40), (255, 12289), (2048, 300),
+                                 (4099, 64), (70001, 40)])
+def test_act_grad_sums_every_row(M, N, dtype):
+    # whole numbers, none of them zero, without an activation: the sums over rows are exact in
+    # any order, and a row that is missing or counted twice shows
+    g = gen(M + N)
+    whole = lambda: ((2.0 * torch.randint(0, 2, (M, N), generator=g, device="cuda") - 1)  # noqa: E731
+                     * torch.randint(1, 5, (M, N), generator=g, device="cuda")).to(dtype)
+    z, dy, up = whole(), whole(), whole()
+    db, dbu = (torch.empty(N, device="cuda") for _ in range(2))
+    gq.act_grad(gq.ACT_NONE, z, dy, dbias=db)
+    assert torch.equal(db.double(), dy.double().sum(0))
+    gq.act_grad(gq.ACT_NONE, z, dy, up=up, dbias=db, dbias_up=dbu)
+    assert torch.equal(db.double(), (dy.double() * up.double()).sum(0))
+    assert torch.equal(dbu.double(), (dy.double() * z.double()).sum(0))
+
+
 def test_act_grad_without_rows():
     z = torch.zeros((0, 9), device="cuda")
     db, dbu = torch.full((9,), 3.0, device="cuda"), torch.full((9,), 3.0, device="cuda")

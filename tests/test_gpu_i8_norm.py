@@ -255,6 +255,24 @@ def test_rms_many_rows(dtype):
     check_grad(gq.rms_i8_grad(got[2], w, r, dh=x), got[2], w, r, x, 1e-6)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,K", [(1, 40), (4, 40), (5, 40), (255, 4096), (513, 4097), (1025, 8192),
+                                 (1500, 8200), (700, 12288), (777, 16400), (70001, 40)])
+def test_rms_grad_sums_every_row(M, K, dtype):
+    # h of +-1 and eps = 3: rstd is 1/2 and n +-1/2, and with whole numbers for dy, none of them
+    # zero, dw's sums are exact in any order: a row that is missing or counted twice shows
+    g = gen(M + K)
+    sign = lambda: 2.0 * torch.randint(0, 2, (M, K), generator=g, device="cuda") - 1  # noqa: E731
+    h = sign().to(dtype)
+    dy = (sign() * torch.randint(1, 9, (M, K), generator=g, device="cuda")).to(dtype)
+    w = torch.ones(K, device="cuda")
+    _, dw = gq.rms_i8_grad(h, w, dy, eps=3.0)
+    assert torch.equal(dw.double(), (dy.double() * h.double()).sum(0) / 2)
+    # and without an eps, rstd 1
+    _, dw = gq.rms_i8_grad(h, w, dy, eps=0.0)
+    assert torch.equal(dw.double(), (dy.double() * h.double()).sum(0))
+
+
 def test_rms_offsets_past_32_bits():
     # rows 1.2 10^9 elements apart: element offsets pass 2^31, byte offsets 2^32
     g = gen(3)
