@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GEMMQ_I8_ABI_VERSION 1
+#define GEMMQ_I8_ABI_VERSION 2
 
 #define GEMMQ_F32 0
 #define GEMMQ_BF16 1

@@ -21,7 +21,7 @@ from . import _lib
 from ._lib import GemmqError, _check  # noqa: F401
 
 F32, BF16, F16 = 0, 1, 2  # GEMMQ_F32, GEMMQ_BF16, GEMMQ_F16
-I8_ABI_VERSION = 1
+I8_ABI_VERSION = 2
 I8_MAX_K = 131071
 I8_MAX_ROWS = 1 << 24
 I8_MAX_PITCH = 1 << 20
@@ -74,13 +74,14 @@ def lib_i8():
         import torch
 
         L = _lib.lib()
+        # the version first: an older library lacks some of the entry points
+        if L.gemmq_i8_abi_version() != I8_ABI_VERSION:
+            raise GemmqError(-101, "libgemmq int8 ABI %d, binding expects %d"
+                             % (L.gemmq_i8_abi_version(), I8_ABI_VERSION))
         for name, (res, args) in EXPORTS_I8.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        if L.gemmq_i8_abi_version() != I8_ABI_VERSION:
-            raise GemmqError(-101, "libgemmq int8 ABI %d, binding expects %d"
-                             % (L.gemmq_i8_abi_version(), I8_ABI_VERSION))
         _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
         _torch = torch
         _fns = L

@@ -31,6 +31,24 @@ def test_every_declared_symbol_exported(L):
     assert L.gemmq_i8_abi_version() == gq.I8_ABI_VERSION
 
 
+def test_an_older_library_is_named(monkeypatch):
+    # one of another version, which lacks entry points that this binding has
+    from quant_packed_weight_amd import _i8, _lib
+
+    class Older:
+        @staticmethod
+        def gemmq_i8_abi_version():
+            return gq.I8_ABI_VERSION - 1
+
+    monkeypatch.setattr(_lib, "lib", Older)
+    monkeypatch.setattr(_i8, "_fns", None)
+    with pytest.raises(gq.GemmqError, match="int8 ABI %d, binding expects %d"
+                       % (gq.I8_ABI_VERSION - 1, gq.I8_ABI_VERSION)):
+        gq.lib_i8()
+    src = open(HEADER).read()
+    assert int(re.search(r"#define GEMMQ_I8_ABI_VERSION (\d+)", src).group(1)) == gq.I8_ABI_VERSION
+
+
 def test_constants_follow_the_header():
     src = open(HEADER).read()
     for name, value in [("GEMMQ_F32", gq.F32), ("GEMMQ_BF16", gq.BF16), ("GEMMQ_F16", gq.F16),
