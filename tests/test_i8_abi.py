@@ -40,6 +40,10 @@ def test_an_older_library_is_named(monkeypatch):
         def gemmq_i8_abi_version():
             return gq.I8_ABI_VERSION - 1
 
+        @staticmethod
+        def gemmq_status_str(status):
+            return b"GEMMQ_E_UNKNOWN"
+
     monkeypatch.setattr(_lib, "lib", Older)
     monkeypatch.setattr(_i8, "_fns", None)
     with pytest.raises(gq.GemmqError, match="int8 ABI %d, binding expects %d"
