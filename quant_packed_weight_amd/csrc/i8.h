@@ -95,7 +95,8 @@ constexpr int kSkinnyMaxM = 16, kSkinnyChannels = 16;  // channels per workgroup
 int launch_skinny(const Operands& op, const LinearOut& out, hipStream_t st);
 int launch_skinny(const Operands& op, const LossOut& out, hipStream_t st);
 int launch_skinny(const Operands& op, const FactorOut& out, hipStream_t st);
-// the layer in one launch: X quantized by every workgroup, one writes op.X and op.sx
+// the layer in one launch: X quantized by every workgroup, one writes op.X and op.sx; no result
+// may lie in X's place (share_memory in i8_check.h)
 bool fuses(int M, int N, int K);
 int launch_fused(int xtype, const void* X, int64_t ldx, const Operands& op, const LinearOut& out,
                  hipStream_t st);
